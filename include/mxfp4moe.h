@@ -345,6 +345,74 @@ int moe_nvfp4_forward(const uint16_t* x, const float* router_logits,
                       int64_t I, int64_t E, int64_t top_k, void* workspace, size_t* workspace_bytes,
                       void* stream);
 
+/*
+ * moe_permute, moe_unpermute - token rows sorted by expert, and the experts'
+ * rows summed back per token with the routing weights; moe_permute_backward
+ * and moe_unpermute_backward their gradients.  The two steps that the fused
+ * layer makes inside its GEMM launches, for callers that run the experts in
+ * parts, train through them, or hold a share of them ("Restore GPT-OSS's
+ * router-masked expert-parallel plan", transformers PR #49431, description).
+ *
+ *   pair p = t * top_k + j is pick j of token t.
+ *   sorted_pairs [R] int32: the pair of every row, as moe_mxfp4_route writes
+ *                it (R = T * top_k), or any list of distinct pairs: a rank's
+ *                share of them, rows of padding between or behind them.  An
+ *                entry outside [0, T * top_k), e.g. -1, is an empty row.  Of
+ *                a pair listed twice, the later row holds the pair and the
+ *                earlier one counts as empty in the gradients.
+ *   pair_rows    [T * top_k] int32: the row of every pair, -1 for a pair
+ *                without a row (moe_permute writes it, the others read it; any
+ *                value outside [0, R) counts as none).
+ *   x, y, dx, dy [T, H];  rows, d_rows [R, H]: all of one element type,
+ *                MXFP4MOE_BF16, MXFP4MOE_F16 or MXFP4MOE_F32, aligned to it
+ *                (16-byte aligned rows move in 16-byte pieces, others in 4-byte
+ *                pieces or single elements).  Outputs alias no input.
+ *   topk_weights, d_weights [T, top_k] float32.
+ *   T, R >= 0, 1 <= H <= MXFP4MOE_MAX_ROW, 1 <= top_k <= MXFP4MOE_MAX_TOPK,
+ *   T * top_k and R below 2^31.
+ *
+ *   moe_permute:            rows[i] = x[sorted_pairs[i] / top_k]; empty rows are
+ *                           written as zeros; pair_rows as above
+ *   moe_permute_backward:   dx[t] = sum_j d_rows[pair_rows[t, j]]
+ *   moe_unpermute:          y[t] = sum_j topk_weights[t, j] * rows[pair_rows[t, j]]
+ *   moe_unpermute_backward: d_rows[i] = topk_weights[p] * dy[p / top_k] for the
+ *                           pair p of row i, zeros for empty rows;
+ *                           d_weights[t, j] = <dy[t], rows[pair_rows[t, j]]>, 0
+ *                           for a pair without a row.  sorted_pairs and
+ *                           pair_rows belong together, as moe_permute leaves them.
+ * Sums run over the pairs that have a row, in fp32, j ascending (a token
+ * without any gets zeros; rows that hold no pair are never read, whatever they
+ * hold); each result is rounded once, and the same inputs give the same bits.
+ */
+#define MXFP4MOE_BF16 0
+#define MXFP4MOE_F16 1
+#define MXFP4MOE_F32 2
+#define MXFP4MOE_MAX_ROW (1 << 28)
+int moe_permute(const void* x, int dtype, const int32_t* sorted_pairs, int64_t T, int64_t H, int64_t top_k, int64_t R,
+                void* rows, int32_t* pair_rows, void* stream);
+int moe_permute_backward(const void* d_rows, int dtype, const int32_t* pair_rows, int64_t T, int64_t H, int64_t top_k,
+                         int64_t R, void* dx, void* stream);
+int moe_unpermute(const void* rows, int dtype, const int32_t* pair_rows, const float* topk_weights, int64_t T,
+                  int64_t H, int64_t top_k, int64_t R, void* y, void* stream);
+int moe_unpermute_backward(const void* dy, const void* rows, int dtype, const int32_t* sorted_pairs,
+                           const int32_t* pair_rows, const float* topk_weights, int64_t T, int64_t H, int64_t top_k,
+                           int64_t R, void* d_rows, float* d_weights, void* stream);
+
+/*
+ * moe_route_backward - the gradient of moe_mxfp4_route's softmax over the
+ * picks: d_logits[t, topk_ids[t, j]] = w_j * (d_w_j - sum_i w_i * d_w_i), 0
+ * for every expert that token t did not pick (the choice itself has no
+ * gradient).
+ *
+ *   topk_ids [T, top_k] int32, topk_weights [T, top_k] float32: as
+ *            moe_mxfp4_route or moe_mxfp4_router writes them; an id outside
+ *            [0, E) is skipped, the terms of an id listed twice add up
+ *   d_weights [T, top_k] float32;  d_logits [T, E] float32 out, written whole
+ *   E, top_k, T as moe_mxfp4_route.  fp32, j ascending.  T == 0 is a no-op.
+ */
+int moe_route_backward(const int32_t* topk_ids, const float* topk_weights, const float* d_weights, int64_t T,
+                       int64_t E, int64_t top_k, float* d_logits, void* stream);
+
 /* Short English text for a status code (static storage). */
 const char* mxfp4moe_status_string(int status);
 
@@ -355,7 +423,10 @@ const char* mxfp4moe_status_string(int status);
  * 1 route, 2 group, 3 gate_up GEMM, 4 down GEMM, 5 combine, 6 dequant,
  * then single launches of the GEMM stages: 7 / 11 / 8 the full-tile /
  * mid-remainder / streaming launch of gate_up, 9 / 12 / 10 the same for down,
- * 13 the MXFP8 activation quantizer of the ACT flags.
+ * 13 the MXFP8 activation quantizer of the ACT flags, 14 permute,
+ * 15 unpermute (and the gradient of permute), 16 the gradient of unpermute,
+ * 17 the gradient of the routing softmax, 18 the linear product, 19 its
+ * gradient.
  * mxfp4moe_profile_end(ms, capacity) synchronises on the recorded events,
  * stores up to `capacity` per-launch durations in milliseconds (host array),
  * releases the events and returns how many were stored (negative on error).

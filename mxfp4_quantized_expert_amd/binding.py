@@ -28,7 +28,8 @@ STATUS = {
 
 STAGES = {"route": 1, "group": 2, "gate_up": 3, "down": 4, "combine": 5, "dequant": 6,
           "gate_up_wide": 7, "gate_up_stream": 8, "down_wide": 9, "down_stream": 10,
-          "gate_up_mid": 11, "down_mid": 12, "act_quant": 13}
+          "gate_up_mid": 11, "down_mid": 12, "act_quant": 13, "permute": 14, "unpermute": 15,
+          "unpermute_backward": 16, "route_backward": 17, "linear": 18, "linear_backward": 19}
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -79,6 +80,17 @@ def load() -> ctypes.CDLL:
     lib.moe_mxfp4_forward_router.restype = ctypes.c_int
     lib.moe_mxfp8_quantize.argtypes = [_vp, _i64, _i64, ctypes.c_int, _vp, _vp, _vp]
     lib.moe_mxfp8_quantize.restype = ctypes.c_int
+    lib.moe_permute.argtypes = [_vp, ctypes.c_int, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp]
+    lib.moe_permute.restype = ctypes.c_int
+    lib.moe_permute_backward.argtypes = [_vp, ctypes.c_int, _vp, _i64, _i64, _i64, _i64, _vp, _vp]
+    lib.moe_permute_backward.restype = ctypes.c_int
+    lib.moe_unpermute.argtypes = [_vp, ctypes.c_int, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]
+    lib.moe_unpermute.restype = ctypes.c_int
+    lib.moe_unpermute_backward.argtypes = [_vp, _vp, ctypes.c_int, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp,
+                                           _vp]
+    lib.moe_unpermute_backward.restype = ctypes.c_int
+    lib.moe_route_backward.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]
+    lib.moe_route_backward.restype = ctypes.c_int
     lib.mxfp4moe_status_string.argtypes = [ctypes.c_int]
     lib.mxfp4moe_status_string.restype = ctypes.c_char_p
     lib.mxfp4moe_profile_begin.argtypes = [ctypes.c_int, ctypes.c_int]
@@ -385,6 +397,193 @@ def moe_nvfp4_forward(x: torch.Tensor, router_logits: torch.Tensor,
                                w2_bias.data_ptr(), out.data_ptr(), T, H, I, E, top_k, workspace.data_ptr(),
                                ctypes.byref(n), _stream(stream))
     _raise("moe_nvfp4_forward", st)
+    return out
+
+
+# ---- the layer's steps as operators of their own
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _elsewhere(t: torch.Tensor, stream) -> bool:
+    """Whether a call on t has to be moved to another device or stream than the current ones."""
+    return stream is not None or (isinstance(t, torch.Tensor) and t.is_cuda
+                                  and t.device.index != torch.cuda.current_device())
+
+
+def _place(t: torch.Tensor, stream):
+    """Context in which t's device and the stream asked for are the current ones, so that the
+    outputs and workspaces allocated in it belong to the stream that the kernels run on."""
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream), device=t.device) if int(stream)
+                  else torch.cuda.default_stream(t.device))
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _check_on(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: torch.device):
+    _check(t, name, dtype, shape)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _element_type(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} has {t.dim()} dimensions, expected 2")
+    return code
+
+
+def _count(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError(f"{name} must be a tensor of one dimension")
+    return t.shape[0]
+
+
+def moe_permute(x: torch.Tensor, sorted_pairs: torch.Tensor, top_k: int, out: Optional[torch.Tensor] = None,
+                pair_rows: Optional[torch.Tensor] = None, stream=None):
+    """Token rows in expert order: rows[i] = x[sorted_pairs[i] // top_k] for x [T, H] (bfloat16,
+    float16 or float32) and sorted_pairs [R] int32, as moe_mxfp4_route gives them; an entry
+    outside [0, T * top_k) makes an empty row of zeros.  Returns (rows [R, H], pair_rows
+    [T * top_k] int32: every pair's row, -1 for none)."""
+    if _elsewhere(x, stream):
+        with _place(x, stream):
+            return moe_permute(x, sorted_pairs, top_k, out, pair_rows)
+    code = _element_type(x, "x")
+    T, H = x.shape
+    R = _count(sorted_pairs, "sorted_pairs")
+    if top_k < 1:
+        raise ValueError(f"top_k must be at least 1, got {top_k}")
+    dev = x.device
+    _check(x, "x", x.dtype)
+    _check_on(sorted_pairs, "sorted_pairs", torch.int32, (R,), dev)
+    if out is None:
+        out = torch.empty((R, H), dtype=x.dtype, device=dev)
+    else:
+        _check_on(out, "out", x.dtype, (R, H), dev)
+    if pair_rows is None:
+        pair_rows = torch.empty((T * top_k,), dtype=torch.int32, device=dev)
+    else:
+        _check_on(pair_rows, "pair_rows", torch.int32, (T * top_k,), dev)
+    st = load().moe_permute(x.data_ptr(), code, sorted_pairs.data_ptr(), T, H, top_k, R, out.data_ptr(),
+                            pair_rows.data_ptr(), _stream(None))
+    _raise("moe_permute", st)
+    return out, pair_rows
+
+
+def moe_permute_backward(d_rows: torch.Tensor, pair_rows: torch.Tensor, top_k: int,
+                         out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of moe_permute: dx[t] = sum_j d_rows[pair_rows[t * top_k + j]] over the pairs
+    that have a row; d_rows [R, H], pair_rows [T * top_k].  Returns dx [T, H]."""
+    if _elsewhere(d_rows, stream):
+        with _place(d_rows, stream):
+            return moe_permute_backward(d_rows, pair_rows, top_k, out)
+    code = _element_type(d_rows, "d_rows")
+    R, H = d_rows.shape
+    P = _count(pair_rows, "pair_rows")
+    if top_k < 1 or P % top_k:
+        raise ValueError(f"pair_rows has {P} entries, not a multiple of top_k = {top_k}")
+    T, dev = P // top_k, d_rows.device
+    _check(d_rows, "d_rows", d_rows.dtype)
+    _check_on(pair_rows, "pair_rows", torch.int32, (P,), dev)
+    if out is None:
+        out = torch.empty((T, H), dtype=d_rows.dtype, device=dev)
+    else:
+        _check_on(out, "out", d_rows.dtype, (T, H), dev)
+    st = load().moe_permute_backward(d_rows.data_ptr(), code, pair_rows.data_ptr(), T, H, top_k, R, out.data_ptr(),
+                                     _stream(None))
+    _raise("moe_permute_backward", st)
+    return out
+
+
+def moe_unpermute(rows: torch.Tensor, pair_rows: torch.Tensor, topk_weights: torch.Tensor,
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The experts' rows summed back: y[t] = sum_j topk_weights[t, j] * rows[pair_rows[t * top_k + j]]
+    over the pairs that have a row (fp32, rounded once).  rows [R, H] (bfloat16, float16 or
+    float32), pair_rows [T * top_k] int32 of moe_permute, topk_weights [T, top_k] float32.
+    Returns y [T, H]."""
+    if _elsewhere(rows, stream):
+        with _place(rows, stream):
+            return moe_unpermute(rows, pair_rows, topk_weights, out)
+    code = _element_type(rows, "rows")
+    R, H = rows.shape
+    T, top_k = topk_weights.shape
+    dev = rows.device
+    _check(rows, "rows", rows.dtype)
+    _check_on(topk_weights, "topk_weights", torch.float32, (T, top_k), dev)
+    _check_on(pair_rows, "pair_rows", torch.int32, (T * top_k,), dev)
+    if out is None:
+        out = torch.empty((T, H), dtype=rows.dtype, device=dev)
+    else:
+        _check_on(out, "out", rows.dtype, (T, H), dev)
+    st = load().moe_unpermute(rows.data_ptr(), code, pair_rows.data_ptr(), topk_weights.data_ptr(), T, H, top_k, R,
+                              out.data_ptr(), _stream(None))
+    _raise("moe_unpermute", st)
+    return out
+
+
+def moe_unpermute_backward(dy: torch.Tensor, rows: torch.Tensor, sorted_pairs: torch.Tensor,
+                           pair_rows: torch.Tensor, topk_weights: torch.Tensor,
+                           d_rows: Optional[torch.Tensor] = None, d_weights: Optional[torch.Tensor] = None,
+                           stream=None):
+    """Gradients of moe_unpermute for dy [T, H]: d_rows [R, H] (the pair's weight times its token's
+    dy; zeros for empty rows) and d_weights [T, top_k] float32 (dot products of dy[t] and the pairs'
+    rows; 0 for a pair without one).  sorted_pairs and pair_rows as moe_permute read and wrote them."""
+    if _elsewhere(rows, stream):
+        with _place(rows, stream):
+            return moe_unpermute_backward(dy, rows, sorted_pairs, pair_rows, topk_weights, d_rows, d_weights)
+    code = _element_type(rows, "rows")
+    R, H = rows.shape
+    T, top_k = topk_weights.shape
+    dev = rows.device
+    _check(rows, "rows", rows.dtype)
+    _check_on(dy, "dy", rows.dtype, (T, H), dev)
+    _check_on(sorted_pairs, "sorted_pairs", torch.int32, (R,), dev)
+    _check_on(pair_rows, "pair_rows", torch.int32, (T * top_k,), dev)
+    _check_on(topk_weights, "topk_weights", torch.float32, (T, top_k), dev)
+    if d_rows is None:
+        d_rows = torch.empty((R, H), dtype=rows.dtype, device=dev)
+    else:
+        _check_on(d_rows, "d_rows", rows.dtype, (R, H), dev)
+    if d_weights is None:
+        d_weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    else:
+        _check_on(d_weights, "d_weights", torch.float32, (T, top_k), dev)
+    st = load().moe_unpermute_backward(dy.data_ptr(), rows.data_ptr(), code, sorted_pairs.data_ptr(),
+                                       pair_rows.data_ptr(), topk_weights.data_ptr(), T, H, top_k, R,
+                                       d_rows.data_ptr(), d_weights.data_ptr(), _stream(None))
+    _raise("moe_unpermute_backward", st)
+    return d_rows, d_weights
+
+
+def moe_route_backward(topk_ids: torch.Tensor, topk_weights: torch.Tensor, d_weights: torch.Tensor,
+                       num_experts: int, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of the softmax over a token's picks: topk_ids [T, top_k] int32, topk_weights and
+    d_weights [T, top_k] float32 -> d_logits [T, num_experts] float32, zero at experts not picked."""
+    if _elsewhere(topk_weights, stream):
+        with _place(topk_weights, stream):
+            return moe_route_backward(topk_ids, topk_weights, d_weights, num_experts, out)
+    T, top_k = topk_weights.shape
+    dev = topk_weights.device
+    _check(topk_weights, "topk_weights", torch.float32)
+    _check_on(topk_ids, "topk_ids", torch.int32, (T, top_k), dev)
+    _check_on(d_weights, "d_weights", torch.float32, (T, top_k), dev)
+    if num_experts < 1:
+        raise ValueError(f"num_experts must be at least 1, got {num_experts}")
+    if out is None:
+        out = torch.empty((T, num_experts), dtype=torch.float32, device=dev)
+    else:
+        _check_on(out, "out", torch.float32, (T, num_experts), dev)
+    st = load().moe_route_backward(topk_ids.data_ptr(), topk_weights.data_ptr(), d_weights.data_ptr(), T,
+                                   num_experts, top_k, out.data_ptr(), _stream(None))
+    _raise("moe_route_backward", st)
     return out
 
 

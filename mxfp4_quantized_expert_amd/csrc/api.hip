@@ -120,6 +120,18 @@ Layout make_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k, bo
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned8(const void* p) { return ((uintptr_t)p & 7u) == 0; }
 
+bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// Sizes of the sorted-rows operators.
+int check_rows(int dtype, int64_t T, int64_t H, int64_t top_k, int64_t R) {
+  static_assert(MXFP4MOE_BF16 == kBf16 && MXFP4MOE_F16 == kF16 && MXFP4MOE_F32 == kF32, "one set of element types");
+  if (dtype < kBf16 || dtype > kF32) return MXFP4MOE_ERR_ARG;
+  if (T < 0 || R < 0 || H < 1 || H > MXFP4MOE_MAX_ROW || top_k < 1 || top_k > MXFP4MOE_MAX_TOPK)
+    return MXFP4MOE_ERR_SHAPE;
+  if (T > (int64_t)0x7fffffff / top_k || R > (int64_t)0x7fffffff) return MXFP4MOE_ERR_SHAPE;
+  return MXFP4MOE_OK;
+}
+
 int check_route_shape(int64_t T, int64_t E, int64_t top_k) {
   if (T < 0 || E < 1 || E > MXFP4MOE_MAX_EXPERTS) return MXFP4MOE_ERR_SHAPE;
   if (top_k < 1 || top_k > E || top_k > MXFP4MOE_MAX_TOPK) return MXFP4MOE_ERR_SHAPE;
@@ -478,6 +490,75 @@ int moe_mxfp4_forward_router(const uint16_t* x, const uint16_t* router_w, const 
   return forward_impl(x, nullptr, router_w ? router_w : &kRouterQuery, router_b, w13_blocks, w13_scales, nullptr,
                       w13_bias, w2_blocks, w2_scales, nullptr, w2_bias, y, T, H, I, E, top_k, flags, workspace,
                       workspace_bytes, stream);
+}
+
+int moe_permute(const void* x, int dtype, const int32_t* sorted_pairs, int64_t T, int64_t H, int64_t top_k, int64_t R,
+                void* rows, int32_t* pair_rows, void* stream) {
+  int st = check_rows(dtype, T, H, top_k, R);
+  if (st != MXFP4MOE_OK) return st;
+  const size_t el = element_bytes(dtype);
+  if ((T > 0 && (x == nullptr || pair_rows == nullptr)) || (R > 0 && (sorted_pairs == nullptr || rows == nullptr)))
+    return MXFP4MOE_ERR_ARG;
+  if (!aligned_to(x, el) || !aligned_to(rows, el) || !aligned_to(sorted_pairs, 4) || !aligned_to(pair_rows, 4))
+    return MXFP4MOE_ERR_ALIGN;
+  hipError_t err = launch_permute(x, dtype, sorted_pairs, T, H, top_k, R, rows, pair_rows, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_permute_backward(const void* d_rows, int dtype, const int32_t* pair_rows, int64_t T, int64_t H, int64_t top_k,
+                         int64_t R, void* dx, void* stream) {
+  int st = check_rows(dtype, T, H, top_k, R);
+  if (st != MXFP4MOE_OK) return st;
+  if ((T > 0 && (pair_rows == nullptr || dx == nullptr)) || (R > 0 && d_rows == nullptr)) return MXFP4MOE_ERR_ARG;
+  const size_t el = element_bytes(dtype);
+  if (!aligned_to(d_rows, el) || !aligned_to(dx, el) || !aligned_to(pair_rows, 4)) return MXFP4MOE_ERR_ALIGN;
+  hipError_t err = launch_unpermute(d_rows, dtype, pair_rows, nullptr, T, H, top_k, R, dx, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_unpermute(const void* rows, int dtype, const int32_t* pair_rows, const float* topk_weights, int64_t T,
+                  int64_t H, int64_t top_k, int64_t R, void* y, void* stream) {
+  int st = check_rows(dtype, T, H, top_k, R);
+  if (st != MXFP4MOE_OK) return st;
+  if ((T > 0 && (pair_rows == nullptr || topk_weights == nullptr || y == nullptr)) || (R > 0 && rows == nullptr))
+    return MXFP4MOE_ERR_ARG;
+  const size_t el = element_bytes(dtype);
+  if (!aligned_to(rows, el) || !aligned_to(y, el) || !aligned_to(pair_rows, 4) || !aligned_to(topk_weights, 4))
+    return MXFP4MOE_ERR_ALIGN;
+  hipError_t err = launch_unpermute(rows, dtype, pair_rows, topk_weights, T, H, top_k, R, y, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_unpermute_backward(const void* dy, const void* rows, int dtype, const int32_t* sorted_pairs,
+                           const int32_t* pair_rows, const float* topk_weights, int64_t T, int64_t H, int64_t top_k,
+                           int64_t R, void* d_rows, float* d_weights, void* stream) {
+  int st = check_rows(dtype, T, H, top_k, R);
+  if (st != MXFP4MOE_OK) return st;
+  if (T > 0 && (dy == nullptr || pair_rows == nullptr || topk_weights == nullptr || d_weights == nullptr))
+    return MXFP4MOE_ERR_ARG;
+  if (R > 0 && (rows == nullptr || sorted_pairs == nullptr || d_rows == nullptr)) return MXFP4MOE_ERR_ARG;
+  const size_t el = element_bytes(dtype);
+  if (!aligned_to(dy, el) || !aligned_to(rows, el) || !aligned_to(d_rows, el) || !aligned_to(sorted_pairs, 4) ||
+      !aligned_to(pair_rows, 4) || !aligned_to(topk_weights, 4) || !aligned_to(d_weights, 4))
+    return MXFP4MOE_ERR_ALIGN;
+  hipError_t err = launch_unpermute_backward(dy, rows, dtype, sorted_pairs, pair_rows, topk_weights, T, H, top_k, R,
+                                             d_rows, d_weights, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_route_backward(const int32_t* topk_ids, const float* topk_weights, const float* d_weights, int64_t T,
+                       int64_t E, int64_t top_k, float* d_logits, void* stream) {
+  int st = check_route_shape(T, E, top_k);
+  if (st != MXFP4MOE_OK) return st;
+  if (T == 0) return MXFP4MOE_OK;
+  if (topk_ids == nullptr || topk_weights == nullptr || d_weights == nullptr || d_logits == nullptr)
+    return MXFP4MOE_ERR_ARG;
+  if (!aligned_to(topk_ids, 4) || !aligned_to(topk_weights, 4) || !aligned_to(d_weights, 4) ||
+      !aligned_to(d_logits, 4))
+    return MXFP4MOE_ERR_ALIGN;
+  hipError_t err =
+      launch_route_backward(topk_ids, topk_weights, d_weights, T, E, top_k, d_logits, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
 }
 
 int mxfp4moe_profile_begin(int stage, int max_calls) {

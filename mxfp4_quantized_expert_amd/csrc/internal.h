@@ -22,7 +22,13 @@ enum Stage : int {
   kStageGateUpMid = 11,    // the mid-size remainder launch of gate_up alone
   kStageDownMid = 12,
   kStageActQuant = 13,     // the MXFP8 activation quantizer of the FP4 scaled-MFMA path
-  kStageLast = kStageActQuant,
+  kStagePermute = 14,           // token rows sorted by expert
+  kStageUnpermute = 15,         // ... and summed back (also the gradient of the former)
+  kStageUnpermuteBackward = 16,
+  kStageRouteBackward = 17,
+  kStageLinear = 18,            // rows times 4-bit weights
+  kStageLinearBackward = 19,    // ... and the gradient to the rows
+  kStageLast = kStageLinearBackward,
 };
 
 // Records a HIP event pair around one launch when the benchmark hook asked for
@@ -144,6 +150,20 @@ size_t act_quant_row_bytes(int K);
 size_t act_quant_scale_row_bytes(int K);
 hipError_t launch_act_quant(const uint16_t* src, int rows, int K, bool split, uint8_t* codes, uint8_t* scales,
                             hipStream_t stream);
+
+// Token rows sorted by expert and back, their gradients, and the routing
+// softmax's (permute.hip).  dtype: ElementType; R rows; top_k = 1.. pairs per token.
+enum ElementType : int { kBf16 = 0, kF16 = 1, kF32 = 2 };
+size_t element_bytes(int dtype);
+hipError_t launch_permute(const void* x, int dtype, const int32_t* sorted_pairs, int64_t T, int64_t H, int64_t top_k,
+                          int64_t R, void* rows, int32_t* pair_rows, hipStream_t stream);
+hipError_t launch_unpermute(const void* rows, int dtype, const int32_t* pair_rows, const float* weights, int64_t T,
+                            int64_t H, int64_t top_k, int64_t R, void* y, hipStream_t stream);
+hipError_t launch_unpermute_backward(const void* dy, const void* rows, int dtype, const int32_t* sorted_pairs,
+                                     const int32_t* pair_rows, const float* weights, int64_t T, int64_t H,
+                                     int64_t top_k, int64_t R, void* d_rows, float* d_weights, hipStream_t stream);
+hipError_t launch_route_backward(const int32_t* ids, const float* weights, const float* d_weights, int64_t T,
+                                 int64_t E, int64_t top_k, float* d_logits, hipStream_t stream);
 
 hipError_t launch_dequant(const uint8_t* blocks, const uint8_t* scales, uint16_t* out, int64_t N, int64_t K,
                           hipStream_t stream);

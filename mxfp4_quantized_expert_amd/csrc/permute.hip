@@ -1,0 +1,353 @@
+// Token rows sorted by expert and summed back, with their gradients, and the
+// gradient of the routing softmax.
+//
+// The fused layer gathers and combines inside its GEMM launches; these are
+// the same two steps as operators of their own ("Restore GPT-OSS's
+// router-masked expert-parallel plan", transformers PR #49431, description:
+// experts take routing data and route their tokens themselves), for callers
+// that run the experts in parts, train through them, or hold a share of them.
+//
+//   pair p = t * top_k + j is pick j of token t; sorted_pairs[i] is the pair
+//   of row i (out of range: an empty row); pair_rows[p] is the row of pair p
+//   (out of range: a pair without a row, e.g. of an expert held elsewhere).
+//   permute:            rows[i] = x[sorted_pairs[i] / top_k], empty rows 0
+//   permute_backward:   dx[t] = sum_j d_rows[row of (t, j)]
+//   unpermute:          y[t] = sum_j w[t, j] rows[row of (t, j)]
+//   unpermute_backward: d_rows[row of (t, j)] = w[t, j] dy[t]
+//                       d_w[t, j] = <dy[t], rows[row of (t, j)]>
+//   route_backward:     d_logits[t, id_j] = w_j (d_w_j - sum_i w_i d_w_i)
+// Sums run in fp32 in ascending j (dot products in a fixed tree), each result
+// is rounded once, and no result depends on the order of blocks.  Every
+// kernel here moves each byte a few flops at most: HBM is the bound, and for
+// a handful of tokens the latency of a launch.
+#include "internal.h"
+#include "mx_device.h"
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Row pieces: kBytes of a row as one vector of elements.
+template <typename E, int kBytes>
+struct Piece {
+  static constexpr int kN = kBytes / (int)sizeof(E);
+  typedef E vec __attribute__((ext_vector_type(kN)));
+  typedef float fvec __attribute__((ext_vector_type(kN)));
+};
+
+// How lanes share a row: groups of 2^lg lanes (a power of two up to the
+// wave, so that short rows do not idle most of a wave), `segs` groups to a
+// row, each lane taking `per` pieces, 2^lg apart.
+struct RowSplit {
+  int nv;    // pieces of a row
+  int lg;    // log2 of the lanes of a group
+  int segs;  // groups of a row
+};
+
+__device__ __forceinline__ bool in_range(int32_t i, int64_t n) { return i >= 0 && (int64_t)i < n; }
+
+// pair_rows of the kPairChunk pairs from chunk * kPairChunk, by one block:
+// every row's pair is read and those of the chunk are kept in LDS (the later
+// row wins where a pair is listed twice), so that pairs without a row come
+// out as -1 without a launch that clears first.
+constexpr int kPairChunk = 2048;
+__device__ void invert_chunk(const int32_t* __restrict__ sorted_pairs, int64_t R, int64_t P, int chunk,
+                             int32_t* __restrict__ pair_rows) {
+  __shared__ int32_t lds[kPairChunk];
+  for (int i = threadIdx.x; i < kPairChunk; i += kThreads) lds[i] = -1;
+  __syncthreads();
+  const int64_t first = (int64_t)chunk * kPairChunk;
+  for (int64_t i = threadIdx.x; i < R; i += kThreads) {
+    const int64_t d = (int64_t)sorted_pairs[i] - first;
+    if (d >= 0 && d < kPairChunk) atomicMax(&lds[d], (int)i);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kPairChunk; i += kThreads)
+    if (first + i < P) pair_rows[first + i] = lds[i];
+}
+
+// ... and for a batch of many pairs, where every block reading every row's
+// pair would cost more than a launch: this clears pair_rows, and the copying
+// blocks enter their rows (the larger one wins, whatever the order).
+constexpr int64_t kInvertInBlocks = 65536;
+__global__ __launch_bounds__(kThreads) void clear_pair_rows_kernel(int32_t* __restrict__ pair_rows, int64_t P) {
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < P; i += (int64_t)gridDim.x * kThreads)
+    pair_rows[i] = -1;
+}
+
+// rows[i] = x[sorted_pairs[i] / top_k]; the blocks before copy_block0 write
+// pair_rows (copy_block0 == 0: it is cleared, and the copying blocks do).
+template <typename V>
+__global__ __launch_bounds__(kThreads) void permute_kernel(const V* __restrict__ x,
+                                                           const int32_t* __restrict__ sorted_pairs,
+                                                           V* __restrict__ rows, int32_t* __restrict__ pair_rows,
+                                                           int64_t R, int64_t P, int top_k, RowSplit sp,
+                                                           int copy_block0) {
+  if ((int)blockIdx.x < copy_block0) {
+    invert_chunk(sorted_pairs, R, P, blockIdx.x, pair_rows);
+    return;
+  }
+  const int lanes = 1 << sp.lg;
+  const unsigned blocks = gridDim.x - copy_block0;
+  for (int64_t g = ((int64_t)(blockIdx.x - copy_block0) * kThreads + threadIdx.x) >> sp.lg; g < R * sp.segs;
+       g += ((int64_t)blocks * kThreads) >> sp.lg) {
+    const unsigned i = (unsigned)g / (unsigned)sp.segs;
+    const int32_t p = sorted_pairs[i];
+    const bool live = in_range(p, P);
+    if (copy_block0 == 0 && live && (threadIdx.x & (lanes - 1)) == 0 && (unsigned)g % (unsigned)sp.segs == 0)
+      atomicMax(&pair_rows[p], (int)i);
+    const V* src = x + (size_t)(live ? p / top_k : 0) * sp.nv;
+    V* dst = rows + (size_t)i * sp.nv;
+    for (int v = (int)((unsigned)g % (unsigned)sp.segs) * lanes + (threadIdx.x & (lanes - 1)); v < sp.nv;
+         v += lanes * sp.segs)
+      dst[v] = live ? src[v] : V{};
+  }
+}
+
+// y[t] = sum_j w[t, j] rows[pair_rows[t, j]] (w == nullptr: 1), j ascending.
+template <typename E, int kBytes>
+__global__ __launch_bounds__(kThreads) void unpermute_kernel(const E* __restrict__ rows,
+                                                             const int32_t* __restrict__ pair_rows,
+                                                             const float* __restrict__ weights, E* __restrict__ y,
+                                                             int64_t T, int64_t R, int top_k, RowSplit sp) {
+  using P = Piece<E, kBytes>;
+  const int lanes = 1 << sp.lg;
+  const typename P::vec* src = reinterpret_cast<const typename P::vec*>(rows);
+  for (int64_t g = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> sp.lg; g < T * sp.segs;
+       g += ((int64_t)gridDim.x * kThreads) >> sp.lg) {
+    const unsigned t = (unsigned)g / (unsigned)sp.segs;
+    typename P::vec* dst = reinterpret_cast<typename P::vec*>(y) + (size_t)t * sp.nv;
+    for (int v = (int)((unsigned)g % (unsigned)sp.segs) * lanes + (threadIdx.x & (lanes - 1)); v < sp.nv;
+         v += lanes * sp.segs) {
+      typename P::fvec sum = {};
+      for (int j = 0; j < top_k; ++j) {
+        const size_t p = (size_t)t * top_k + j;
+        const int32_t r = pair_rows[p];
+        if (!in_range(r, R)) continue;
+        const typename P::fvec z = __builtin_convertvector(src[(size_t)r * sp.nv + v], typename P::fvec);
+        const float w = weights != nullptr ? weights[p] : 1.0f;
+#pragma unroll
+        for (int c = 0; c < P::kN; ++c) sum[c] = __builtin_fmaf(w, z[c], sum[c]);
+      }
+      dst[v] = __builtin_convertvector(sum, typename P::vec);
+    }
+  }
+}
+
+// d_rows and d_w, one wave per token; the blocks from zero_block0 on clear the rows that hold no pair.
+template <typename E, int kBytes>
+__global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
+    const E* __restrict__ dy, const E* __restrict__ rows, const int32_t* __restrict__ sorted_pairs,
+    const int32_t* __restrict__ pair_rows, const float* __restrict__ weights, E* __restrict__ d_rows,
+    float* __restrict__ d_weights, int64_t T, int64_t R, int top_k, int nv, int zero_block0) {
+  using P = Piece<E, kBytes>;
+  const int lane = mx::lane_id();
+  typename P::vec* out = reinterpret_cast<typename P::vec*>(d_rows);
+  if ((int)blockIdx.x >= zero_block0) {
+    const int64_t step = (int64_t)(gridDim.x - zero_block0) * kThreads;
+    for (int64_t r0 = (int64_t)(blockIdx.x - zero_block0) * kThreads + (threadIdx.x - lane); r0 < R; r0 += step) {
+      const int64_t r = r0 + lane;
+      bool empty = false;
+      if (r < R) {
+        const int32_t p = sorted_pairs[r];
+        empty = !(in_range(p, T * top_k) && pair_rows[p] == (int32_t)r);
+      }
+      uint64_t todo = __ballot(empty);
+      while (todo != 0) {
+        const int b = __builtin_ctzll(todo);
+        todo &= todo - 1;
+        for (int v = lane; v < nv; v += 64) out[(size_t)(r0 + b) * nv + v] = typename P::vec{};
+      }
+    }
+    return;
+  }
+  const typename P::vec* z = reinterpret_cast<const typename P::vec*>(rows);
+  for (int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); t < T;
+       t += (int64_t)zero_block0 * (kThreads / 64)) {
+    const typename P::vec* g = reinterpret_cast<const typename P::vec*>(dy) + (size_t)t * nv;
+    for (int j = 0; j < top_k; ++j) {
+      const size_t p = (size_t)t * top_k + j;
+      const int32_t r = pair_rows[p];
+      float dot = 0.f;
+      if (in_range(r, R)) {
+        const bool own = (size_t)sorted_pairs[r] == p;
+        const float w = weights[p];
+        for (int v = lane; v < nv; v += 64) {
+          const typename P::fvec gv = __builtin_convertvector(g[v], typename P::fvec);
+          const typename P::fvec zv = __builtin_convertvector(z[(size_t)r * nv + v], typename P::fvec);
+#pragma unroll
+          for (int c = 0; c < P::kN; ++c) dot = __builtin_fmaf(gv[c], zv[c], dot);
+          if (own) out[(size_t)r * nv + v] = __builtin_convertvector(gv * w, typename P::vec);
+        }
+      }
+      dot = mx::wave_sum_f32(dot);
+      if (lane == 0) d_weights[p] = dot;
+    }
+  }
+}
+
+// kV logits per thread (4 where E allows), a block holding whole tokens.
+template <int kV>
+__global__ __launch_bounds__(kThreads) void route_backward_kernel(const int32_t* __restrict__ ids,
+                                                                  const float* __restrict__ weights,
+                                                                  const float* __restrict__ d_weights,
+                                                                  float* __restrict__ d_logits, int64_t T, int E,
+                                                                  int top_k, int per_token, int tokens_per_block) {
+  typedef float vec __attribute__((ext_vector_type(kV)));
+  const int lt = threadIdx.x / per_token;
+  if (lt >= tokens_per_block) return;
+  for (int64_t t = (int64_t)blockIdx.x * tokens_per_block + lt; t < T; t += (int64_t)gridDim.x * tokens_per_block) {
+    for (int part = threadIdx.x - lt * per_token; part * kV < E; part += per_token) {
+      const int32_t* id = ids + t * top_k;
+      const float* w = weights + t * top_k;
+      const float* dw = d_weights + t * top_k;
+      float s = 0.f;
+      for (int j = 0; j < top_k; ++j) s = __builtin_fmaf(w[j], dw[j], s);
+      vec g = {};
+      for (int j = 0; j < top_k; ++j) {
+        const int at = id[j] - part * kV;
+#pragma unroll
+        for (int c = 0; c < kV; ++c) g[c] += at == c ? w[j] * (dw[j] - s) : 0.f;
+      }
+      *reinterpret_cast<vec*>(d_logits + t * E + part * kV) = g;
+    }
+  }
+}
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// The widest piece that divides a row of `bytes` and the alignment of every
+// tensor: 16 or 4 bytes, or one element.
+int piece_bytes(size_t bytes, size_t element, const void* a, const void* b, const void* c) {
+  for (size_t v : {(size_t)16, (size_t)4})
+    if (v >= element && bytes % v == 0 && aligned(a, v) && aligned(b, v) && aligned(c, v)) return (int)v;
+  return (int)element;
+}
+
+RowSplit row_split(int64_t rows, int64_t nv) {
+  RowSplit s{(int)nv, 0, 1};
+  while (s.lg < 6 && (1 << s.lg) < nv) ++s.lg;
+  // one piece per lane while the groups can be counted in 31 bits
+  const int64_t segs = (nv + (1 << s.lg) - 1) >> s.lg;
+  s.segs = rows * segs <= (int64_t)1 << 24 ? (int)segs : 1;
+  return s;
+}
+
+// A launch holds fewer than 2^32 threads; the kernels loop past that.
+constexpr int64_t kMaxBlocks = 1 << 22;
+
+unsigned block_count(int64_t work, int64_t per_block) {
+  const int64_t n = (work + per_block - 1) / per_block;
+  return (unsigned)(n < kMaxBlocks ? n : kMaxBlocks);
+}
+
+unsigned split_blocks(int64_t rows, const RowSplit& s) { return block_count(rows * s.segs, kThreads >> s.lg); }
+
+template <typename V>
+hipError_t permute(const void* x, const int32_t* sorted_pairs, int64_t nv, int64_t R, int64_t P, int top_k,
+                   void* rows, int32_t* pair_rows, hipStream_t stream) {
+  const RowSplit sp = row_split(R, nv);
+  const int chunks = P <= kInvertInBlocks ? (int)((P + kPairChunk - 1) / kPairChunk) : 0;
+  if (P > kInvertInBlocks)
+    clear_pair_rows_kernel<<<block_count(P, kThreads), kThreads, 0, stream>>>(pair_rows, P);
+  if (chunks + R == 0) return hipGetLastError();
+  permute_kernel<V><<<chunks + split_blocks(R, sp), kThreads, 0, stream>>>(
+      static_cast<const V*>(x), sorted_pairs, static_cast<V*>(rows), pair_rows, R, P, top_k, sp, chunks);
+  return hipGetLastError();
+}
+
+template <typename E, int kBytes>
+hipError_t unpermute(const void* rows, const int32_t* pair_rows, const float* weights, int64_t T, int64_t H,
+                     int64_t R, int top_k, void* y, hipStream_t stream) {
+  const RowSplit sp = row_split(T, H * (int64_t)sizeof(E) / kBytes);
+  unpermute_kernel<E, kBytes><<<split_blocks(T, sp), kThreads, 0, stream>>>(
+      static_cast<const E*>(rows), pair_rows, weights, static_cast<E*>(y), T, R, top_k, sp);
+  return hipGetLastError();
+}
+
+template <typename E, int kBytes>
+hipError_t unpermute_backward(const void* dy, const void* rows, const int32_t* sorted_pairs,
+                              const int32_t* pair_rows, const float* weights, int64_t T, int64_t H, int64_t R,
+                              int top_k, void* d_rows, float* d_weights, hipStream_t stream) {
+  const int token_blocks = (int)block_count(T, kThreads / 64);
+  const int row_blocks = (int)block_count(R, kThreads);
+  unpermute_backward_kernel<E, kBytes><<<token_blocks + row_blocks, kThreads, 0, stream>>>(
+      static_cast<const E*>(dy), static_cast<const E*>(rows), sorted_pairs, pair_rows, weights,
+      static_cast<E*>(d_rows), d_weights, T, R, top_k, (int)(H * (int64_t)sizeof(E) / kBytes), token_blocks);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+namespace mxfp4moe {
+
+size_t element_bytes(int dtype) { return dtype == kF32 ? 4 : 2; }
+
+hipError_t launch_permute(const void* x, int dtype, const int32_t* sorted_pairs, int64_t T, int64_t H, int64_t top_k,
+                          int64_t R, void* rows, int32_t* pair_rows, hipStream_t stream) {
+  const int64_t P = T * top_k;
+  if (R == 0 && P == 0) return hipSuccess;
+  const size_t bytes = (size_t)H * element_bytes(dtype);
+  ProfileScope prof(kStagePermute, stream);
+  switch (piece_bytes(bytes, element_bytes(dtype), x, rows, nullptr)) {
+    case 16: return permute<mx::u32x4>(x, sorted_pairs, bytes / 16, R, P, (int)top_k, rows, pair_rows, stream);
+    case 4: return permute<uint32_t>(x, sorted_pairs, bytes / 4, R, P, (int)top_k, rows, pair_rows, stream);
+    default: return permute<uint16_t>(x, sorted_pairs, bytes / 2, R, P, (int)top_k, rows, pair_rows, stream);
+  }
+}
+
+hipError_t launch_unpermute(const void* rows, int dtype, const int32_t* pair_rows, const float* weights, int64_t T,
+                            int64_t H, int64_t top_k, int64_t R, void* y, hipStream_t stream) {
+  if (T == 0) return hipSuccess;
+  const size_t el = element_bytes(dtype);
+  const int piece = piece_bytes((size_t)H * el, el, rows, y, nullptr);
+  const int k = (int)top_k;
+  ProfileScope prof(kStageUnpermute, stream);
+  if (dtype == kF32)
+    return piece == 16 ? unpermute<float, 16>(rows, pair_rows, weights, T, H, R, k, y, stream)
+                       : unpermute<float, 4>(rows, pair_rows, weights, T, H, R, k, y, stream);
+  if (dtype == kF16)
+    return piece == 16  ? unpermute<_Float16, 16>(rows, pair_rows, weights, T, H, R, k, y, stream)
+           : piece == 4 ? unpermute<_Float16, 4>(rows, pair_rows, weights, T, H, R, k, y, stream)
+                        : unpermute<_Float16, 2>(rows, pair_rows, weights, T, H, R, k, y, stream);
+  return piece == 16  ? unpermute<__bf16, 16>(rows, pair_rows, weights, T, H, R, k, y, stream)
+         : piece == 4 ? unpermute<__bf16, 4>(rows, pair_rows, weights, T, H, R, k, y, stream)
+                      : unpermute<__bf16, 2>(rows, pair_rows, weights, T, H, R, k, y, stream);
+}
+
+hipError_t launch_unpermute_backward(const void* dy, const void* rows, int dtype, const int32_t* sorted_pairs,
+                                     const int32_t* pair_rows, const float* weights, int64_t T, int64_t H,
+                                     int64_t top_k, int64_t R, void* d_rows, float* d_weights, hipStream_t stream) {
+  if (T == 0 && R == 0) return hipSuccess;
+  const size_t el = element_bytes(dtype);
+  const int piece = piece_bytes((size_t)H * el, el, dy, rows, d_rows);
+  const int k = (int)top_k;
+  ProfileScope prof(kStageUnpermuteBackward, stream);
+#define MX_BACKWARD(E, B) \
+  unpermute_backward<E, B>(dy, rows, sorted_pairs, pair_rows, weights, T, H, R, k, d_rows, d_weights, stream)
+  if (dtype == kF32) return piece == 16 ? MX_BACKWARD(float, 16) : MX_BACKWARD(float, 4);
+  if (dtype == kF16)
+    return piece == 16 ? MX_BACKWARD(_Float16, 16) : piece == 4 ? MX_BACKWARD(_Float16, 4) : MX_BACKWARD(_Float16, 2);
+  return piece == 16 ? MX_BACKWARD(__bf16, 16) : piece == 4 ? MX_BACKWARD(__bf16, 4) : MX_BACKWARD(__bf16, 2);
+#undef MX_BACKWARD
+}
+
+hipError_t launch_route_backward(const int32_t* ids, const float* weights, const float* d_weights, int64_t T,
+                                 int64_t E, int64_t top_k, float* d_logits, hipStream_t stream) {
+  if (T == 0) return hipSuccess;
+  const bool four = E % 4 == 0 && aligned(d_logits, 16);
+  int per_token = (int)(four ? E / 4 : E);
+  per_token = per_token < kThreads ? per_token : kThreads;
+  const int tokens = kThreads / per_token;
+  const unsigned blocks = block_count(T, tokens);
+  ProfileScope prof(kStageRouteBackward, stream);
+  if (four)
+    route_backward_kernel<4><<<blocks, kThreads, 0, stream>>>(ids, weights, d_weights, d_logits, T, (int)E,
+                                                              (int)top_k, per_token, tokens);
+  else
+    route_backward_kernel<1><<<blocks, kThreads, 0, stream>>>(ids, weights, d_weights, d_logits, T, (int)E,
+                                                              (int)top_k, per_token, tokens);
+  return hipGetLastError();
+}
+
+}  // namespace mxfp4moe
