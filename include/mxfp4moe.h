@@ -413,6 +413,51 @@ int moe_unpermute_backward(const void* dy, const void* rows, int dtype, const in
 int moe_route_backward(const int32_t* topk_ids, const float* topk_weights, const float* d_weights, int64_t T,
                        int64_t E, int64_t top_k, float* d_logits, void* stream);
 
+/*
+ * moe_mxfp4_linear, moe_nvfp4_linear - rows times 4-bit weights with group
+ * scales, dense or with each row's expert, and their gradients to the rows
+ * (the weights, scales and biases are frozen and have none):
+ *
+ *   linear:          y[r, n]  = s2_e * sum_k x[r, k] W_e[n, k] + bias[e, n]
+ *   linear_backward: dx[r, k] = s2_e * sum_n dy[r, n] W_e[n, k]
+ *
+ * The products of the fused layer as operators of their own (formats and the
+ * order of second-level scale and bias as moe_mxfp4_forward and
+ * moe_nvfp4_forward; s2 = 1 for MXFP4), for one row to many.
+ *
+ *   x, dx  [R, K] bf16, 16-byte aligned;  y, dy [R, N] bf16, 16-byte aligned
+ *   blocks [E, N, K/2] uint8, 16-byte aligned
+ *   scales [E, N, K/32] uint8 E8M0, or [E, N, K/16] uint8 E4M3; 16-byte aligned
+ *   scale2 [E] float32 (NVFP4)
+ *   bias   [E, N] bf16, or NULL for none
+ *   expert_offsets [E + 1] int32, ascending: expert e has the rows
+ *          [expert_offsets[e], expert_offsets[e + 1]), as moe_mxfp4_route
+ *          writes them (or a slice of them: a rank's experts).  Rows before
+ *          the first and from the last offset on are neither read nor
+ *          written.  Values are clamped to [0, R].  NULL: one dense matrix
+ *          (E == 1), every row.
+ *   K a multiple of 32, any N; N, K <= MXFP4MOE_MAX_LINEAR, N * K < 2^32 - K;
+ *   1 <= E <= MXFP4MOE_MAX_EXPERTS; 0 <= R < 2^31.  R == 0 is a no-op.
+ * Products are exact, sums are fp32 in an order fixed by the sizes (the same
+ * inputs give the same bits), one rounding to bf16 at the end.  A NaN scale
+ * byte makes its weights NaN: y in its row n, dx in its group's columns, for
+ * every row of its expert.  E8M0 bytes 253 and 254 with the largest codes
+ * overflow to inf (unspecified outputs).  Outputs alias no input.
+ */
+#define MXFP4MOE_MAX_LINEAR (1 << 20)
+int moe_mxfp4_linear(const uint16_t* x, const uint8_t* blocks, const uint8_t* scales, const uint16_t* bias,
+                     const int32_t* expert_offsets, int64_t R, int64_t K, int64_t N, int64_t E, uint16_t* y,
+                     void* stream);
+int moe_nvfp4_linear(const uint16_t* x, const uint8_t* blocks, const uint8_t* scales, const float* scale2,
+                     const uint16_t* bias, const int32_t* expert_offsets, int64_t R, int64_t K, int64_t N, int64_t E,
+                     uint16_t* y, void* stream);
+int moe_mxfp4_linear_backward(const uint16_t* dy, const uint8_t* blocks, const uint8_t* scales,
+                              const int32_t* expert_offsets, int64_t R, int64_t K, int64_t N, int64_t E, uint16_t* dx,
+                              void* stream);
+int moe_nvfp4_linear_backward(const uint16_t* dy, const uint8_t* blocks, const uint8_t* scales, const float* scale2,
+                              const int32_t* expert_offsets, int64_t R, int64_t K, int64_t N, int64_t E, uint16_t* dx,
+                              void* stream);
+
 /* Short English text for a status code (static storage). */
 const char* mxfp4moe_status_string(int status);
 

@@ -91,6 +91,14 @@ def load() -> ctypes.CDLL:
     lib.moe_unpermute_backward.restype = ctypes.c_int
     lib.moe_route_backward.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]
     lib.moe_route_backward.restype = ctypes.c_int
+    lib.moe_mxfp4_linear.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]
+    lib.moe_mxfp4_linear.restype = ctypes.c_int
+    lib.moe_nvfp4_linear.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]
+    lib.moe_nvfp4_linear.restype = ctypes.c_int
+    lib.moe_mxfp4_linear_backward.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]
+    lib.moe_mxfp4_linear_backward.restype = ctypes.c_int
+    lib.moe_nvfp4_linear_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]
+    lib.moe_nvfp4_linear_backward.restype = ctypes.c_int
     lib.mxfp4moe_status_string.argtypes = [ctypes.c_int]
     lib.mxfp4moe_status_string.restype = ctypes.c_char_p
     lib.mxfp4moe_profile_begin.argtypes = [ctypes.c_int, ctypes.c_int]
@@ -585,6 +593,116 @@ def moe_route_backward(topk_ids: torch.Tensor, topk_weights: torch.Tensor, d_wei
                                    num_experts, top_k, out.data_ptr(), _stream(None))
     _raise("moe_route_backward", st)
     return out
+
+
+def _linear_sizes(rows: torch.Tensor, name: str, blocks: torch.Tensor, scales: torch.Tensor, group: int,
+                  expert_offsets: Optional[torch.Tensor], scale2: Optional[torch.Tensor],
+                  bias: Optional[torch.Tensor] = None):
+    """(E, N, K) of a linear operator's weights, after the checks of every tensor but the rows' width."""
+    if not isinstance(rows, torch.Tensor) or not isinstance(blocks, torch.Tensor):
+        raise TypeError(f"{name} and blocks must be torch.Tensors")
+    lead = 2 if expert_offsets is None else 3
+    if rows.dim() != 2:
+        raise ValueError(f"{name} has {rows.dim()} dimensions, expected 2")
+    if blocks.dim() != lead:
+        raise ValueError(f"blocks has {blocks.dim()} dimensions, expected {lead} "
+                         f"{'without' if lead == 2 else 'with'} expert_offsets")
+    E = 1 if lead == 2 else blocks.shape[0]
+    N, K = blocks.shape[-2], 2 * blocks.shape[-1]
+    dev = rows.device
+    _check(rows, name, torch.bfloat16)
+    _check_on(blocks, "blocks", torch.uint8, None, dev)
+    _check_on(scales, "scales", torch.uint8, (*blocks.shape[:-1], K // group), dev)
+    if expert_offsets is not None:
+        _check_on(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev)
+    if group == 16:
+        _check_on(scale2, "scale2", torch.float32, (E,), dev)
+    if bias is not None:
+        _check_on(bias, "bias", torch.bfloat16, tuple(blocks.shape[:-1]), dev)
+    return E, N, K
+
+
+def _address(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _linear(fn: str, x, blocks, scales, scale2, bias, expert_offsets, out):
+    group = 32 if fn == "moe_mxfp4_linear" else 16
+    E, N, K = _linear_sizes(x, "x", blocks, scales, group, expert_offsets, scale2, bias)
+    R = x.shape[0]
+    if x.shape[1] != K:
+        raise ValueError(f"x has rows of {x.shape[1]}, expected {K}")
+    if out is None:
+        out = torch.empty((R, N), dtype=torch.bfloat16, device=x.device)
+    else:
+        _check_on(out, "out", torch.bfloat16, (R, N), x.device)
+    weights = (blocks.data_ptr(), scales.data_ptr()) + ((scale2.data_ptr(),) if group == 16 else ())
+    st = getattr(load(), fn)(x.data_ptr(), *weights, _address(bias), _address(expert_offsets), R, K, N, E,
+                             out.data_ptr(), _stream(None))
+    _raise(fn, st)
+    return out
+
+
+def _linear_backward(fn: str, dy, blocks, scales, scale2, expert_offsets, out):
+    group = 32 if fn == "moe_mxfp4_linear_backward" else 16
+    E, N, K = _linear_sizes(dy, "dy", blocks, scales, group, expert_offsets, scale2)
+    R = dy.shape[0]
+    if dy.shape[1] != N:
+        raise ValueError(f"dy has rows of {dy.shape[1]}, expected {N}")
+    if out is None:
+        out = torch.empty((R, K), dtype=torch.bfloat16, device=dy.device)
+    else:
+        _check_on(out, "out", torch.bfloat16, (R, K), dy.device)
+    weights = (blocks.data_ptr(), scales.data_ptr()) + ((scale2.data_ptr(),) if group == 16 else ())
+    st = getattr(load(), fn)(dy.data_ptr(), *weights, _address(expert_offsets), R, K, N, E, out.data_ptr(),
+                             _stream(None))
+    _raise(fn, st)
+    return out
+
+
+def moe_mxfp4_linear(x: torch.Tensor, blocks: torch.Tensor, scales: torch.Tensor,
+                     bias: Optional[torch.Tensor] = None, expert_offsets: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rows times MXFP4 weights: y = x W^T (+ bias) for x [R, K] bfloat16.  Dense: blocks [N, K/2]
+    and scales [N, K/32] uint8, bias [N] bfloat16.  Per expert: blocks [E, N, K/2], scales
+    [E, N, K/32], bias [E, N] and expert_offsets [E + 1] int32 (expert e has the rows
+    [offsets[e], offsets[e + 1]); rows outside them keep what `out` held).  Returns y [R, N]."""
+    if _elsewhere(x, stream):
+        with _place(x, stream):
+            return moe_mxfp4_linear(x, blocks, scales, bias, expert_offsets, out)
+    return _linear("moe_mxfp4_linear", x, blocks, scales, None, bias, expert_offsets, out)
+
+
+def moe_nvfp4_linear(x: torch.Tensor, blocks: torch.Tensor, scales: torch.Tensor, scale2: torch.Tensor,
+                     bias: Optional[torch.Tensor] = None, expert_offsets: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_mxfp4_linear over NVFP4 weights: scales [..., N, K/16] uint8 (E4M3) and scale2 [E]
+    float32 ([1] dense), which multiplies the product before the bias."""
+    if _elsewhere(x, stream):
+        with _place(x, stream):
+            return moe_nvfp4_linear(x, blocks, scales, scale2, bias, expert_offsets, out)
+    return _linear("moe_nvfp4_linear", x, blocks, scales, scale2, bias, expert_offsets, out)
+
+
+def moe_mxfp4_linear_backward(dy: torch.Tensor, blocks: torch.Tensor, scales: torch.Tensor,
+                              expert_offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """Gradient of moe_mxfp4_linear to its rows: dx = dy W for dy [R, N] bfloat16 (weights and
+    offsets as there; the weights are frozen).  Returns dx [R, K]."""
+    if _elsewhere(dy, stream):
+        with _place(dy, stream):
+            return moe_mxfp4_linear_backward(dy, blocks, scales, expert_offsets, out)
+    return _linear_backward("moe_mxfp4_linear_backward", dy, blocks, scales, None, expert_offsets, out)
+
+
+def moe_nvfp4_linear_backward(dy: torch.Tensor, blocks: torch.Tensor, scales: torch.Tensor, scale2: torch.Tensor,
+                              expert_offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """Gradient of moe_nvfp4_linear to its rows: dx = scale2 * (dy W).  Returns dx [R, K]."""
+    if _elsewhere(dy, stream):
+        with _place(dy, stream):
+            return moe_nvfp4_linear_backward(dy, blocks, scales, scale2, expert_offsets, out)
+    return _linear_backward("moe_nvfp4_linear_backward", dy, blocks, scales, scale2, expert_offsets, out)
 
 
 def profile_begin(stage: str, max_calls: int) -> None:

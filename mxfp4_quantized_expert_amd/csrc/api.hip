@@ -132,6 +132,21 @@ int check_rows(int dtype, int64_t T, int64_t H, int64_t top_k, int64_t R) {
   return MXFP4MOE_OK;
 }
 
+// Sizes and pointers of the linear operators; `in` and `out` are the rows read and written.
+int check_linear(const void* in, const void* blocks, const void* scales, const void* bias, const void* offsets,
+                 const void* out, int64_t R, int64_t K, int64_t N, int64_t E) {
+  if (R < 0 || R > (int64_t)0x7fffffff || N < 1 || K < 32 || (K & 31) != 0) return MXFP4MOE_ERR_SHAPE;
+  if (N > MXFP4MOE_MAX_LINEAR || K > MXFP4MOE_MAX_LINEAR || N > ((int64_t)1 << 32) / K - 1) return MXFP4MOE_ERR_SHAPE;
+  if (E < 1 || E > MXFP4MOE_MAX_EXPERTS) return MXFP4MOE_ERR_SHAPE;
+  if (offsets == nullptr && E != 1) return MXFP4MOE_ERR_ARG;
+  if (R == 0) return MXFP4MOE_OK;
+  if (in == nullptr || blocks == nullptr || scales == nullptr || out == nullptr) return MXFP4MOE_ERR_ARG;
+  if (!aligned_to(in, 16) || !aligned_to(blocks, 16) || !aligned_to(out, 16) || !aligned_to(scales, 16) ||
+      !aligned_to(bias, 2) || !aligned_to(offsets, 4))
+    return MXFP4MOE_ERR_ALIGN;
+  return MXFP4MOE_OK;
+}
+
 int check_route_shape(int64_t T, int64_t E, int64_t top_k) {
   if (T < 0 || E < 1 || E > MXFP4MOE_MAX_EXPERTS) return MXFP4MOE_ERR_SHAPE;
   if (top_k < 1 || top_k > E || top_k > MXFP4MOE_MAX_TOPK) return MXFP4MOE_ERR_SHAPE;
@@ -558,6 +573,50 @@ int moe_route_backward(const int32_t* topk_ids, const float* topk_weights, const
     return MXFP4MOE_ERR_ALIGN;
   hipError_t err =
       launch_route_backward(topk_ids, topk_weights, d_weights, T, E, top_k, d_logits, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_mxfp4_linear(const uint16_t* x, const uint8_t* blocks, const uint8_t* scales, const uint16_t* bias,
+                     const int32_t* expert_offsets, int64_t R, int64_t K, int64_t N, int64_t E, uint16_t* y,
+                     void* stream) {
+  int st = check_linear(x, blocks, scales, bias, expert_offsets, y, R, K, N, E);
+  if (st != MXFP4MOE_OK) return st;
+  hipError_t err = launch_linear(x, blocks, scales, nullptr, bias, expert_offsets, R, K, N, E, y, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_nvfp4_linear(const uint16_t* x, const uint8_t* blocks, const uint8_t* scales, const float* scale2,
+                     const uint16_t* bias, const int32_t* expert_offsets, int64_t R, int64_t K, int64_t N, int64_t E,
+                     uint16_t* y, void* stream) {
+  int st = check_linear(x, blocks, scales, bias, expert_offsets, y, R, K, N, E);
+  if (st != MXFP4MOE_OK) return st;
+  if (R == 0) return MXFP4MOE_OK;
+  if (scale2 == nullptr) return MXFP4MOE_ERR_ARG;
+  if (!aligned_to(scale2, 4)) return MXFP4MOE_ERR_ALIGN;
+  hipError_t err = launch_linear(x, blocks, scales, scale2, bias, expert_offsets, R, K, N, E, y, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_mxfp4_linear_backward(const uint16_t* dy, const uint8_t* blocks, const uint8_t* scales,
+                              const int32_t* expert_offsets, int64_t R, int64_t K, int64_t N, int64_t E, uint16_t* dx,
+                              void* stream) {
+  int st = check_linear(dy, blocks, scales, nullptr, expert_offsets, dx, R, K, N, E);
+  if (st != MXFP4MOE_OK) return st;
+  hipError_t err =
+      launch_linear_backward(dy, blocks, scales, nullptr, expert_offsets, R, K, N, E, dx, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_nvfp4_linear_backward(const uint16_t* dy, const uint8_t* blocks, const uint8_t* scales, const float* scale2,
+                              const int32_t* expert_offsets, int64_t R, int64_t K, int64_t N, int64_t E, uint16_t* dx,
+                              void* stream) {
+  int st = check_linear(dy, blocks, scales, nullptr, expert_offsets, dx, R, K, N, E);
+  if (st != MXFP4MOE_OK) return st;
+  if (R == 0) return MXFP4MOE_OK;
+  if (scale2 == nullptr) return MXFP4MOE_ERR_ARG;
+  if (!aligned_to(scale2, 4)) return MXFP4MOE_ERR_ALIGN;
+  hipError_t err =
+      launch_linear_backward(dy, blocks, scales, scale2, expert_offsets, R, K, N, E, dx, (hipStream_t)stream);
   return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
 }
 

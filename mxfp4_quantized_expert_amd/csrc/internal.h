@@ -165,6 +165,15 @@ hipError_t launch_unpermute_backward(const void* dy, const void* rows, int dtype
 hipError_t launch_route_backward(const int32_t* ids, const float* weights, const float* d_weights, int64_t T,
                                  int64_t E, int64_t top_k, float* d_logits, hipStream_t stream);
 
+// Rows times 4-bit weights and the gradient to the rows (linear.hip).
+// scale2 != nullptr: NVFP4 weights.  offsets == nullptr: one expert, every row.
+hipError_t launch_linear(const uint16_t* x, const uint8_t* blocks, const uint8_t* scales, const float* scale2,
+                         const uint16_t* bias, const int32_t* offsets, int64_t R, int64_t K, int64_t N, int64_t E,
+                         uint16_t* y, hipStream_t stream);
+hipError_t launch_linear_backward(const uint16_t* dy, const uint8_t* blocks, const uint8_t* scales,
+                                  const float* scale2, const int32_t* offsets, int64_t R, int64_t K, int64_t N,
+                                  int64_t E, uint16_t* dx, hipStream_t stream);
+
 hipError_t launch_dequant(const uint8_t* blocks, const uint8_t* scales, uint16_t* out, int64_t N, int64_t K,
                           hipStream_t stream);
 

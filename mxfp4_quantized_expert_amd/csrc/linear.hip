@@ -1,0 +1,377 @@
+// Rows times 4-bit weights with group scales, dense or per expert, and the
+// gradient to the rows.
+//
+//   y[r, n]  = s2_e * sum_k x[r, k] W_e[n, k] + b_e[n]
+//   dx[r, k] = s2_e * sum_n dy[r, n] W_e[n, k]
+// for the rows r of expert e (expert_offsets; one expert without them), with
+// W_e[n, k] = E2M1(code) * group scale: MXFP4 has an E8M0 scale per 32 k and
+// s2 = 1, NVFP4 an E4M3 scale per 16 k and a float32 s2 per expert.  Formats
+// and the order of scale and bias as in the fused layer ("feat(gguf): serve
+// gpt-oss gguf checkpoints on gpt_oss", FreeToken PR #838, review item 3);
+// the weights are frozen, so the rows are all that has a gradient.
+//
+// A code times its scale is exact in bf16 (two significant bits for MXFP4,
+// at most five for NVFP4), so every product of the bf16 MFMA is exact and the
+// sums are its fp32 accumulation; s2 and the bias follow in fp32 and the
+// result is rounded once.
+#include "expert_device.h"
+#include "internal.h"
+#include "mx_device.h"
+
+namespace {
+
+using mx::bf16x8;
+using mx::f32x4;
+using mx::u32x4;
+using mxgemm::GroupScale;
+
+constexpr int kXcds = 8;
+constexpr int kRawBuffer = 0x00020000;  // descriptor word 3: 32-bit data format, for untyped loads
+// An offset past every buffer (they hold less than 2 GiB): the load returns zero.
+constexpr uint32_t kDead = 0x80000000u;
+
+struct LinearArgs {
+  const uint16_t* x;        // forward: x [R, K]; gradient: dy [R, N]
+  const uint8_t* blocks;    // [E, N, K/2]
+  const uint8_t* scales;    // [E, N, K/32], NVFP4 [E, N, K/16]
+  const float* scale2;      // [E] or nullptr
+  const uint16_t* bias;     // [E, N] or nullptr
+  const int32_t* offsets;   // [E + 1] or nullptr (E == 1, every row)
+  uint16_t* y;              // forward: y [R, N]; gradient: dx [R, K]
+  int R, K, N, E;
+  int max_tiles;            // row tiles, at most
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, kRawBuffer);
+}
+
+struct Tile {
+  int e, row0, rows;
+};
+
+// Row tile `idx` of at most tm rows, the experts' tiles one after another.
+// Offsets are clamped to [0, R], so that no tile reaches outside the rows.
+// Every lane of the wave returns the same; false past the last tile.
+__device__ bool find_tile(const LinearArgs& a, int tm, int idx, Tile& t) {
+  if (a.offsets == nullptr) {
+    t.e = 0;
+    t.row0 = idx * tm;
+    t.rows = min(tm, a.R - t.row0);
+    return idx < (int)(((int64_t)a.R + tm - 1) / tm);
+  }
+  const int lane = mx::lane_id();
+  int before = 0;
+  for (int e0 = 0; e0 < a.E; e0 += 64) {
+    const int e = e0 + lane;
+    int first = 0, count = 0;
+    if (e < a.E) {
+      first = min(max(a.offsets[e], 0), a.R);
+      count = max(min(max(a.offsets[e + 1], 0), a.R) - first, 0);
+    }
+    const int n = (int)(((int64_t)count + tm - 1) / tm);
+    const int last = before + mx::wave_inclusive_sum(n);
+    const uint64_t hit = __ballot(idx >= last - n && idx < last);
+    if (hit != 0) {
+      const int l = __builtin_ctzll(hit);
+      const int at = (idx - (__builtin_amdgcn_readlane(last, l) - __builtin_amdgcn_readlane(n, l))) * tm;
+      t.e = e0 + l;
+      t.row0 = __builtin_amdgcn_readlane(first, l) + at;
+      t.rows = min(tm, __builtin_amdgcn_readlane(count, l) - at);
+      return true;
+    }
+    before = __builtin_amdgcn_readlane(last, 63);
+  }
+  return false;
+}
+
+// Block -> (tile, chunk of the other axis): each XCD (blocks are dealt to
+// them round robin) walks a contiguous range with the tile fastest, so that
+// the tiles of an expert read its weights from one XCD's L2.
+__device__ __forceinline__ bool map_block(int tiles, int chunks, int& tile, int& chunk) {
+  const int64_t total = (int64_t)tiles * chunks;
+  const int64_t per = (total + kXcds - 1) / kXcds;
+  const int64_t b = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const int64_t w = (b % kXcds) * per + b / kXcds;
+  if (b / kXcds >= per || w >= total) return false;
+  chunk = (int)(w / tiles);
+  tile = (int)(w - (int64_t)chunk * tiles);
+  return true;
+}
+
+// ---------------------------------------------------------------- few rows
+
+// y for row tiles of at most 16 rows: 16x16x32 MFMA, weights as the A operand
+// (16 weight rows), x rows as B.  A chunk is four groups (128 k): lane (r, q)
+// holds group q of weight row r, one 16-byte load, whose dword s goes to step
+// s with the x values of the same k; any agreed order of k gives the same
+// sums.  The waves of a block split K, kC chunks each at a time (all loads of
+// a wave in flight before the first product), and hold the sums of kG * 16
+// weight rows; x stays in registers for those kG row groups.  The partial
+// sums meet in LDS, added in wave order.  Loads past K, N or the tile's rows
+// return zero from the buffer's bounds.  Bound: the weights' bytes from HBM,
+// and for a single small matrix the latency of one pass.
+constexpr int kFewRows = 16;
+
+template <bool kNv, int kC, int kG>
+__global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs a) {
+  extern __shared__ f32x4 red[];
+  const int n_chunks = (a.N + 16 * kG - 1) / (16 * kG);
+  int ti, nc;
+  if (!map_block(a.max_tiles, n_chunks, ti, nc)) return;  // uniform per block
+  Tile t;
+  if (!find_tile(a, kFewRows, ti, t)) return;
+  const int K = a.K, N = a.N, kgroups = K >> 5, n0 = nc * 16 * kG;
+  const int lane = mx::lane_id(), lr = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const size_t wrow0 = (size_t)t.e * N + n0;
+  const int nrows = min(16 * kG, N - n0);
+  const int kscales = kNv ? K >> 4 : kgroups;
+  const auto rx = buffer(a.x + (size_t)t.row0 * K, (uint32_t)t.rows * K * 2);
+  const auto rw = buffer(a.blocks + wrow0 * (K >> 1), (uint32_t)nrows * (K >> 1));
+  const auto rs = buffer(a.scales + wrow0 * kscales, (uint32_t)nrows * kscales);
+
+  f32x4 acc[kG] = {};
+  const int per = waves * kC;
+  for (int c0 = wave * kC; 4 * c0 < kgroups; c0 += per) {
+    u32x4 xb[kC][4], w[kG][kC];
+    uint32_t sc[kG][kC];
+#pragma unroll
+    for (int j = 0; j < kC; ++j) {
+      const int g = 4 * (c0 + j) + q;
+#pragma unroll
+      for (int i = 0; i < kG; ++i) {
+        const uint32_t row = lr + 16 * i;
+        w[i][j] = __builtin_amdgcn_raw_buffer_load_b128(rw, g < kgroups ? row * (K >> 1) + g * 16 : kDead, 0, 0);
+        if (kNv)
+          sc[i][j] = __builtin_amdgcn_raw_buffer_load_b16(rs, g < kgroups ? row * kscales + g * 2 : kDead, 0, 0);
+        else
+          sc[i][j] = __builtin_amdgcn_raw_buffer_load_b8(rs, g < kgroups ? row * kscales + g : kDead, 0, 0);
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        xb[j][s] = __builtin_amdgcn_raw_buffer_load_b128(
+            rx, g < kgroups ? (uint32_t)lr * K * 2 + g * 64 + 16 * s : kDead, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < kC; ++j)
+#pragma unroll
+      for (int i = 0; i < kG; ++i) {
+        const GroupScale<kNv> gs(sc[i][j] & 255u, sc[i][j] >> 8);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx::as_bf16x8(gs.convert(w[i][j][s], s)),
+                                                           mx::as_bf16x8(xb[j][s]), acc[i], 0, 0, 0);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < kG; ++i) red[(wave * kG + i) * 64 + lane] = acc[i];
+  __syncthreads();
+  const float s2 = kNv ? a.scale2[t.e] : 1.0f;
+  for (int i = wave; i < kG; i += waves) {
+    f32x4 v = red[i * 64 + lane];
+    for (int u = 1; u < waves; ++u) v += red[(u * kG + i) * 64 + lane];
+    const int n = n0 + 16 * i + 4 * q;  // lane (row lr of the tile, q): features n .. n+3
+    if (lr >= t.rows || n >= N) continue;
+    uint16_t* out = a.y + (size_t)(t.row0 + lr) * N + n;
+    const uint16_t* bias = a.bias != nullptr ? a.bias + (size_t)t.e * N + n : nullptr;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      v[c] *= s2;
+      if (bias != nullptr && n + c < N) v[c] += mx::bf16_to_f32(bias[c]);
+    }
+    const uint2 packed = mxgemm::pack_bf16x4(v);
+    if ((N & 3) == 0) {
+      *reinterpret_cast<uint2*>(out) = packed;
+    } else {
+      const uint32_t d[2] = {packed.x, packed.y};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (n + c < N) out[c] = (uint16_t)(d[c >> 1] >> (16 * (c & 1)));
+    }
+  }
+}
+
+// dx for row tiles of at most 16 rows.  The sum runs over weight rows, so the
+// MFMA's A operand is the transposed weights: lane (m, q) loads the dword of
+// eight codes k = 8m .. 8m+7 of eight weight rows n = 8q .. 8q+7, converts
+// each to four pairs of k, and exchanges halves between the rows of a pair
+// (v_perm) into eight operands of eight n, one for each k: operand j
+// multiplies with k = 8m + j as its row m.  Waves split N and add their sums
+// in LDS in wave order.  Bound: as above, the weights' bytes.
+constexpr int kFewK = 128;       // k of a block
+constexpr int kRedStride = 36;   // floats per lane in LDS (32 and padding)
+
+// Eight consecutive dy values of a row from element n on, zeros past N.
+template <bool kAligned>
+__device__ __forceinline__ u32x4 load_dy8(const __amdgpu_buffer_rsrc_t& r, const uint16_t* row, uint32_t row_bytes0,
+                                          int n, int N, bool whole) {
+  if constexpr (kAligned) {
+    return __builtin_amdgcn_raw_buffer_load_b128(r, n < N ? row_bytes0 + n * 2 : kDead, 0, 0);
+  } else {
+    u32x4 v;
+    if (whole) {  // uniform: no lane reaches past N
+      __builtin_memcpy(&v, row + n, 16);
+    } else {
+      uint32_t e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = n + i < N ? row[n + i] : 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = e[2 * i] | (e[2 * i + 1] << 16);
+    }
+    return v;
+  }
+}
+
+template <bool kNv, bool kAligned>
+__global__ __launch_bounds__(512) void linear_backward_few_kernel(LinearArgs a) {
+  extern __shared__ float redf[];
+  const int k_chunks = (a.K + kFewK - 1) / kFewK;
+  int ti, kc;
+  if (!map_block(a.max_tiles, k_chunks, ti, kc)) return;  // uniform per block
+  Tile t;
+  if (!find_tile(a, kFewRows, ti, t)) return;
+  const int K = a.K, N = a.N, k0 = kc * kFewK;
+  const int lane = mx::lane_id(), m = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int kscales = kNv ? K >> 4 : K >> 5;
+  const auto rw = buffer(a.blocks + (size_t)t.e * N * (K >> 1), (uint32_t)N * (K >> 1));
+  const auto rs = buffer(a.scales + (size_t)t.e * N * kscales, (uint32_t)N * kscales);
+  const uint16_t* dy0 = a.x + (size_t)t.row0 * N;
+  const auto rd = buffer(dy0, (uint32_t)t.rows * N * 2);
+  const int row = min(m, t.rows - 1);  // columns past the tile's rows are dropped
+  const uint32_t wcol = (k0 >> 1) + 4 * m, scol = kNv ? (k0 >> 4) + (m >> 1) : (k0 >> 5) + (m >> 2);
+
+  f32x4 acc[8] = {};
+  const int steps = (N + 31) >> 5;
+  for (int s0 = wave; s0 < steps; s0 += 2 * waves) {
+    uint32_t w[2][8], sc[2][8];
+    u32x4 d[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int s = s0 + u * waves;
+      const int n = 32 * s + 8 * q;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[u][i] = __builtin_amdgcn_raw_buffer_load_b32(rw, n + i < N ? (uint32_t)(n + i) * (K >> 1) + wcol : kDead, 0, 0);
+        sc[u][i] = __builtin_amdgcn_raw_buffer_load_b8(rs, n + i < N ? (uint32_t)(n + i) * kscales + scol : kDead, 0, 0);
+      }
+      d[u] = load_dy8<kAligned>(rd, dy0 + (size_t)row * N, (uint32_t)row * N * 2, n, N, 32 * s + 32 <= N);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      u32x4 r[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        r[i] = kNv ? mx::fp4x8_to_bf16x8_any_scale(w[u][i], mx::e4m3x2_operands(sc[u][i]).x)
+                   : mx::fp4x8_to_bf16x8(w[u][i], mx::e8m0_operand(sc[u][i]));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        u32x4 op;
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+          op[p] = __builtin_amdgcn_perm(r[2 * p + 1][j >> 1], r[2 * p][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx::as_bf16x8(op), mx::as_bf16x8(d[u]), acc[j], 0, 0, 0);
+      }
+    }
+  }
+  // lane (row m of the tile, q) holds k = k0 + 32q + 8r + j in acc[j][r]
+  float* mine = redf + (wave * 64 + lane) * kRedStride;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<f32x4*>(mine + 8 * r + 4 * h) =
+          f32x4{acc[4 * h][r], acc[4 * h + 1][r], acc[4 * h + 2][r], acc[4 * h + 3][r]};
+  __syncthreads();
+  const float s2 = kNv ? a.scale2[t.e] : 1.0f;
+  for (int i = threadIdx.x; i < 64 * 8; i += blockDim.x) {
+    const int l = i >> 3, piece = i & 7;
+    f32x4 v = *reinterpret_cast<const f32x4*>(redf + l * kRedStride + 4 * piece);
+    for (int u = 1; u < waves; ++u)
+      v += *reinterpret_cast<const f32x4*>(redf + (u * 64 + l) * kRedStride + 4 * piece);
+    const int k = k0 + 32 * (l >> 4) + 4 * piece, r = l & 15;
+    if (r < t.rows && k < K) *reinterpret_cast<uint2*>(a.y + (size_t)(t.row0 + r) * K + k) = mxgemm::pack_bf16x4(v * s2);
+  }
+}
+
+int max_tiles(const LinearArgs& a, int tm) {
+  const int64_t full = (int64_t)a.R / tm;
+  return (int)(a.offsets == nullptr ? ((int64_t)a.R + tm - 1) / tm : full + (a.E < a.R ? a.E : a.R));
+}
+
+// One block for every tile and chunk, for each XCD the same number; a launch
+// holds fewer than 2^32 threads along x.
+dim3 grid_of(int64_t tiles, int64_t chunks) {
+  constexpr int64_t kMaxX = 1 << 22;
+  const int64_t blocks = (tiles * chunks + kXcds - 1) / kXcds * kXcds;
+  return blocks <= kMaxX ? dim3((unsigned)blocks) : dim3((unsigned)kMaxX, (unsigned)((blocks + kMaxX - 1) / kMaxX));
+}
+
+template <bool kNv, int kC>
+hipError_t launch_few(LinearArgs a, int waves, hipStream_t stream) {
+  // as many row groups to a block (x is read once for all) as leave two blocks for every CU
+  const int64_t groups = ((int64_t)a.N + 15) / 16 * a.max_tiles, want = 2 * mxfp4moe::device_cu_count();
+  const int g = groups >= 4 * want ? 4 : groups >= 2 * want ? 2 : 1;
+  const dim3 grid = grid_of(a.max_tiles, ((int64_t)a.N + 16 * g - 1) / (16 * g));
+  const size_t lds = (size_t)waves * g * 64 * sizeof(f32x4);
+  if (g == 4) linear_few_kernel<kNv, kC, 4><<<grid, waves * 64, lds, stream>>>(a);
+  else if (g == 2) linear_few_kernel<kNv, kC, 2><<<grid, waves * 64, lds, stream>>>(a);
+  else linear_few_kernel<kNv, kC, 1><<<grid, waves * 64, lds, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <bool kNv>
+hipError_t linear(LinearArgs a, hipStream_t stream) {
+  a.max_tiles = max_tiles(a, kFewRows);
+  const int chunks = (a.K + 127) / 128;
+  const int waves = chunks <= 24 ? 4 : 8;
+  const int c = (chunks + waves - 1) / waves;
+  if (c <= 2) return launch_few<kNv, 2>(a, waves, stream);
+  if (c <= 4) return launch_few<kNv, 4>(a, waves, stream);
+  return launch_few<kNv, 6>(a, waves, stream);
+}
+
+template <bool kNv>
+hipError_t linear_backward(LinearArgs a, hipStream_t stream) {
+  a.max_tiles = max_tiles(a, kFewRows);
+  const int steps = (a.N + 31) / 32;
+  const int waves = steps < 8 ? steps : 8;
+  const dim3 grid = grid_of(a.max_tiles, (a.K + kFewK - 1) / kFewK);
+  const size_t lds = (size_t)waves * 64 * kRedStride * sizeof(float);
+  if (a.N % 8 == 0) linear_backward_few_kernel<kNv, true><<<grid, waves * 64, lds, stream>>>(a);
+  else linear_backward_few_kernel<kNv, false><<<grid, waves * 64, lds, stream>>>(a);
+  return hipGetLastError();
+}
+
+LinearArgs args_of(const uint16_t* in, const uint8_t* blocks, const uint8_t* scales, const float* scale2,
+                   const uint16_t* bias, const int32_t* offsets, int64_t R, int64_t K, int64_t N, int64_t E,
+                   uint16_t* out) {
+  return {in, blocks, scales, scale2, bias, offsets, out, (int)R, (int)K, (int)N, (int)E, 0};
+}
+
+}  // namespace
+
+namespace mxfp4moe {
+
+hipError_t launch_linear(const uint16_t* x, const uint8_t* blocks, const uint8_t* scales, const float* scale2,
+                         const uint16_t* bias, const int32_t* offsets, int64_t R, int64_t K, int64_t N, int64_t E,
+                         uint16_t* y, hipStream_t stream) {
+  if (R == 0) return hipSuccess;
+  const LinearArgs a = args_of(x, blocks, scales, scale2, bias, offsets, R, K, N, E, y);
+  ProfileScope prof(kStageLinear, stream);
+  return scale2 != nullptr ? linear<true>(a, stream) : linear<false>(a, stream);
+}
+
+hipError_t launch_linear_backward(const uint16_t* dy, const uint8_t* blocks, const uint8_t* scales,
+                                  const float* scale2, const int32_t* offsets, int64_t R, int64_t K, int64_t N,
+                                  int64_t E, uint16_t* dx, hipStream_t stream) {
+  if (R == 0) return hipSuccess;
+  const LinearArgs a = args_of(dy, blocks, scales, scale2, nullptr, offsets, R, K, N, E, dx);
+  ProfileScope prof(kStageLinearBackward, stream);
+  return scale2 != nullptr ? linear_backward<true>(a, stream) : linear_backward<false>(a, stream);
+}
+
+}  // namespace mxfp4moe

@@ -96,3 +96,44 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         binding.moe_unpermute_backward(x, x, pairs, pairs, w)
     with pytest.raises(ValueError, match="device"):
         binding.moe_route_backward(pairs.view(4, 2), w, w, 8)
+
+
+def _linear_calls(lib):
+    """(call of the pointers and sizes by name, pointer names) of the four linear entry points."""
+    for name in ("moe_mxfp4_linear", "moe_nvfp4_linear", "moe_mxfp4_linear_backward", "moe_nvfp4_linear_backward"):
+        def call(x=A, blocks=A, scales=A, scale2=A, bias=A, offsets=A, y=A, R=8, K=64, N=40, E=4, name=name):
+            args = [x, blocks, scales]
+            args += [scale2] if "nvfp4" in name else []
+            args += [] if "backward" in name else [bias]
+            return getattr(lib, name)(*args, offsets, R, K, N, E, y, None)
+        yield name, call
+
+
+def test_linear_checks(lib):
+    for name, call in _linear_calls(lib):
+        for bad in [dict(R=-1), dict(R=1 << 31), dict(K=48), dict(K=0), dict(K=16), dict(N=0), dict(E=0), dict(E=513),
+                    dict(K=(1 << 20) + 32), dict(N=(1 << 20) + 1), dict(K=1 << 18, N=1 << 14)]:
+            assert call(**bad) == -2, (name, bad)
+        assert call(offsets=None) == -1, name          # more than one expert need offsets
+        for ptr in ("x", "blocks", "scales", "y"):
+            assert call(**{ptr: None}) == -1, (name, ptr)
+            assert call(**{ptr: A + 8}) == -4, (name, ptr)
+        assert call(offsets=A + 2) == -4, name
+        if "nvfp4" in name:
+            assert call(scale2=None) == -1 and call(scale2=A + 2) == -4
+        if "backward" not in name:
+            assert call(bias=A + 1) == -4
+        assert call(x=None, y=None, R=0) == 0
+
+
+def test_linear_binding_refusals():
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    blocks, scales = torch.zeros((40, 32), dtype=torch.uint8), torch.zeros((40, 2), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="device"):
+        binding.moe_mxfp4_linear(x, blocks, scales)
+    with pytest.raises(ValueError, match="blocks has 2 dimensions"):
+        binding.moe_mxfp4_linear(x, blocks, scales, None, torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="blocks has 3 dimensions"):
+        binding.moe_mxfp4_linear_backward(x, blocks[None], scales[None])
+    with pytest.raises(ValueError, match="dimensions"):
+        binding.moe_nvfp4_linear(x[0], blocks, scales, None)
