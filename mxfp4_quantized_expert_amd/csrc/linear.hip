@@ -21,6 +21,7 @@
 namespace {
 
 using mx::bf16x8;
+using mx::f32x16;
 using mx::f32x4;
 using mx::u32x4;
 using mxgemm::GroupScale;
@@ -96,6 +97,42 @@ __device__ __forceinline__ bool map_block(int tiles, int chunks, int& tile, int&
   if (b / kXcds >= per || w >= total) return false;
   chunk = (int)(w / tiles);
   tile = (int)(w - (int64_t)chunk * tiles);
+  return true;
+}
+
+// The row tiles of all experts.
+__device__ int count_tiles(const LinearArgs& a, int tm) {
+  if (a.offsets == nullptr) return (int)(((int64_t)a.R + tm - 1) / tm);
+  int total = 0;
+  for (int e0 = 0; e0 < a.E; e0 += 64) {
+    const int e = e0 + mx::lane_id();
+    int count = 0;
+    if (e < a.E) {
+      const int first = min(max(a.offsets[e], 0), a.R);
+      count = max(min(max(a.offsets[e + 1], 0), a.R) - first, 0);
+    }
+    total += __builtin_amdgcn_readlane(mx::wave_inclusive_sum((int)(((int64_t)count + tm - 1) / tm)), 63);
+  }
+  return min(total, a.max_tiles);
+}
+
+// Block -> (row tile, chunk of the other axis) of a kernel whose blocks share
+// both operands: each XCD walks a contiguous range of the tiles that exist, in
+// groups of kGroup row tiles with the tile fastest, so that the blocks that
+// run together on it share weights and rows through its L2.
+constexpr int kGroup = 4;
+__device__ __forceinline__ bool map_tile(const LinearArgs& a, int tm, int chunks, int& tile, int& chunk) {
+  const int tiles = count_tiles(a, tm);
+  const int64_t total = (int64_t)tiles * chunks;
+  const int64_t per = (total + kXcds - 1) / kXcds;
+  const int64_t b = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const int64_t w = (b % kXcds) * per + b / kXcds;
+  if (b / kXcds >= per || w >= total) return false;
+  const int64_t span = (int64_t)kGroup * chunks;
+  const int g = (int)(w / span), rem = (int)(w - g * span);
+  const int gm = min(kGroup, tiles - g * kGroup);
+  tile = g * kGroup + rem % gm;
+  chunk = rem / gm;
   return true;
 }
 
@@ -297,6 +334,223 @@ __global__ __launch_bounds__(512) void linear_backward_few_kernel(LinearArgs a) 
   }
 }
 
+// --------------------------------------------------------------- many rows
+
+// Scale bytes of one weight row, 16 at a time from byte offset `o` of the
+// expert's scales: aligned dwords and a funnel shift, because a row of scales
+// starts at any byte.  The buffer starts at a dword and ends with the dword
+// that holds its last byte.
+struct ScaleBytes {
+  uint32_t d[5];
+  __device__ __forceinline__ void load(const __amdgpu_buffer_rsrc_t& r, uint32_t o) {
+    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, o & ~3u, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = v[i];
+    d[4] = __builtin_amdgcn_raw_buffer_load_b32(r, (o & ~3u) + 16, 0, 0);
+  }
+  // the next kBytes bytes to the front
+  template <int kBytes>
+  __device__ __forceinline__ void drop() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = kBytes == 4 ? d[i + 1] : __builtin_amdgcn_alignbit(d[i + 1], d[i], 8 * kBytes);
+    if (kBytes != 4) d[4] >>= 8 * kBytes;
+  }
+};
+
+// y for row tiles of 128: 32x32x16 MFMA, a block of four waves makes 256
+// weight rows x 128 rows, each wave 64 x 128.  K runs in chunks of 64: lane
+// half h takes group 2c + h of its weight row, dword s of the group's 16
+// bytes in step s, and the x values of the same k.  Chunks travel from global
+// memory into three LDS stages by the load unit (16 bytes a lane), chunk c+2
+// on its way while chunk c is multiplied; one barrier a chunk.  x rows are
+// 128 bytes a stage, their 16-byte pieces XOR-swizzled so that the 128-bit
+// reads of consecutive rows hit distinct banks.  Scale bytes go straight to
+// registers, a row's next 16 at a time.  Two blocks a CU: one converts and
+// waits while the other multiplies.  Token blocks of 32 without rows are
+// neither read nor multiplied.  Bound: the bf16 MFMA rate (and the
+// conversions beside it).
+constexpr int kTileRows = 128, kTileN = 256;
+constexpr int kXSlots = kTileRows * 8, kWSlots = kTileN * 2, kStageSlots = kXSlots + kWSlots;
+constexpr int kStages = 3;
+constexpr int kChunkLoads = (kXSlots + kWSlots) / 256;  // of a thread
+
+__device__ __forceinline__ int swizzle(int row) { return (row ^ (row >> 3)) & 7; }
+
+__device__ __forceinline__ void load_lds16(const __amdgpu_buffer_rsrc_t& r, u32x4* lds, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0, 0);
+}
+
+// The chunk loop over kLive blocks of 32 rows.
+template <bool kNv, int kLive>
+__device__ __forceinline__ void tile_chunks(f32x16 (&acc)[2][4], u32x4* arena, const __amdgpu_buffer_rsrc_t& rx,
+                                            const __amdgpu_buffer_rsrc_t& rw, const __amdgpu_buffer_rsrc_t& rs,
+                                            int K, uint32_t scale0, int kscales, int wave, bool work) {
+  const int t = threadIdx.x, lane = t & 63, half = lane >> 5, lrow = lane & 31;
+  const int chunks = (K + 63) >> 6;
+  // this thread's pieces of a stage
+  const int xr = t >> 3;
+  const uint32_t xoff = (uint32_t)xr * K * 2 + 16 * ((t & 7) ^ swizzle(xr & 31));
+  const uint32_t woff = (uint32_t)(t >> 1) * (K >> 1) + 16 * (t & 1);
+  auto issue = [&](int c, int st, int k) {
+    c = min(c, chunks - 1);
+    u32x4* dst = arena + st * kStageSlots + wave * 64;
+    if (k < 4) load_lds16(rx, dst + k * 256, xoff + (uint32_t)(k * 32) * K * 2 + c * 128);
+    else load_lds16(rw, dst + kXSlots + (k - 4) * 256, woff + (uint32_t)((k - 4) * 128) * (K >> 1) + c * 32);
+  };
+#pragma unroll
+  for (int k = 0; k < kChunkLoads; ++k) issue(0, 0, k);
+#pragma unroll
+  for (int k = 0; k < kChunkLoads; ++k) issue(1, 1, k);
+
+  // this lane's scale rows: 16 bytes hold the groups of kSpan chunks
+  constexpr int kStep = kNv ? 4 : 2, kSpan = 16 / kStep;
+  ScaleBytes sb[2];
+  const uint32_t so[2] = {scale0 + (uint32_t)(wave * 64 + lrow) * kscales + half * (kStep / 2),
+                          scale0 + (uint32_t)(wave * 64 + 32 + lrow) * kscales + half * (kStep / 2)};
+  int boff[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) boff[s] = lrow * 8 + ((4 * half + s) ^ swizzle(lrow));
+  const int aoff = kXSlots + (wave * 64 + lrow) * 2 + half;
+
+  int st = 0;
+  for (int c = 0; c < chunks; ++c) {
+    if (c % kSpan == 0) {  // uniform
+#pragma unroll
+      for (int rb = 0; rb < 2; ++rb) sb[rb].load(rs, so[rb] + c * kStep);
+#pragma unroll
+      for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sb[rb].d[i] = __builtin_amdgcn_alignbit(sb[rb].d[i + 1], sb[rb].d[i], 8 * (so[rb] & 3u));
+    }
+    mxgemm::wait_loads_then_barrier<kChunkLoads>();
+    const int nst = st == 0 ? 2 : st - 1;  // (c + 2) % 3
+    if (!work) {
+#pragma unroll
+      for (int k = 0; k < kChunkLoads; ++k) issue(c + 2, nst, k);
+      st = st == 2 ? 0 : st + 1;
+      continue;
+    }
+    const u32x4* base = arena + st * kStageSlots;
+    u32x4 w[2];
+    bf16x8 b[4][kLive];
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb) w[rb] = base[aoff + rb * 64];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int cb = 0; cb < kLive; ++cb) b[s][cb] = mx::as_bf16x8(base[boff[s] + cb * 256]);
+    uint32_t s0[2], s1[2];
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb) {
+      s0[rb] = sb[rb].d[0] & 255u;
+      s1[rb] = kNv ? (sb[rb].d[0] >> 8) & 255u : 0u;
+      sb[rb].template drop<kStep>();
+    }
+    if (64 * c + 64 > K) {  // the half chunk past K: zero weights times zero rows
+      const bool dead = half == 1;
+#pragma unroll
+      for (int rb = 0; rb < 2; ++rb) {
+        if (dead) {
+          w[rb] = u32x4{0u, 0u, 0u, 0u};
+          s0[rb] = s1[rb] = 0u;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int cb = 0; cb < kLive; ++cb)
+          if (dead) b[s][cb] = mx::as_bf16x8(u32x4{0u, 0u, 0u, 0u});
+    }
+    const GroupScale<kNv> g0(s0[0], s1[0]), g1(s0[1], s1[1]);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const bf16x8 a0 = mx::as_bf16x8(g0.convert(w[0][s], s)), a1 = mx::as_bf16x8(g1.convert(w[1][s], s));
+#pragma unroll
+      for (int cb = 0; cb < kLive; ++cb) {
+        acc[0][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a0, b[s][cb], acc[0][cb], 0, 0, 0);
+        acc[1][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a1, b[s][cb], acc[1][cb], 0, 0, 0);
+      }
+      if (s < 3) {
+        issue(c + 2, nst, 2 * s);
+        issue(c + 2, nst, 2 * s + 1);
+      }
+    }
+    st = st == 2 ? 0 : st + 1;
+  }
+}
+
+// Rows of the wave's 64 outputs x 32 rows in LDS, before they leave in whole rows.
+constexpr int kOutStride = 72;  // bf16 per row: 64 and padding
+
+template <bool kNv>
+__global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs a) {
+  __shared__ __attribute__((aligned(16))) u32x4 arena[kStages * kStageSlots];
+  const int n_tiles = (a.N + kTileN - 1) / kTileN;
+  int ti, nt;
+  if (!map_tile(a, kTileRows, n_tiles, ti, nt)) return;  // uniform per block
+  Tile t;
+  if (!find_tile(a, kTileRows, ti, t)) return;
+  const int K = a.K, N = a.N, n0 = nt * kTileN;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int nrows = min(kTileN, N - n0), kscales = kNv ? K >> 4 : K >> 5;
+  const size_t wrow0 = (size_t)t.e * N + n0;
+  const auto rx = buffer(a.x + (size_t)t.row0 * K, (uint32_t)t.rows * K * 2);
+  const auto rw = buffer(a.blocks + wrow0 * (K >> 1), (uint32_t)nrows * (K >> 1));
+  const uint8_t* sp = a.scales + wrow0 * kscales;
+  const uint32_t shift = (uint32_t)((uintptr_t)sp & 3u);
+  const auto rs = buffer(sp - shift, (shift + (uint32_t)nrows * kscales + 3u) & ~3u);
+
+  f32x16 acc[2][4] = {};
+  const int live = (t.rows + 31) >> 5;
+  const bool work = n0 + wave * 64 < N;  // uniform: a wave past N only loads its share
+  if (live == 4) tile_chunks<kNv, 4>(acc, arena, rx, rw, rs, K, shift, kscales, wave, work);
+  else if (live == 3) tile_chunks<kNv, 3>(acc, arena, rx, rw, rs, K, shift, kscales, wave, work);
+  else if (live == 2) tile_chunks<kNv, 2>(acc, arena, rx, rw, rs, K, shift, kscales, wave, work);
+  else tile_chunks<kNv, 1>(acc, arena, rx, rw, rs, K, shift, kscales, wave, work);
+
+  // lane (row lane & 31 of the block, half): features 8i + 4 half .. + 3 in acc[.][.][4i ..]
+  mxgemm::wait_loads_then_barrier<0>();  // no load still writes LDS, no wave still reads it
+  const int nw = n0 + wave * 64, half = lane >> 5, lrow = lane & 31;
+  if (!work) return;  // no barrier follows
+  const float s2 = kNv ? a.scale2[t.e] : 1.0f;
+  float bias[2][16];
+#pragma unroll
+  for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int n = min(nw + rb * 32 + 8 * (i >> 2) + 4 * half + (i & 3), N - 1);
+      bias[rb][i] = a.bias != nullptr ? mx::bf16_to_f32(a.bias[(size_t)t.e * N + n]) : 0.f;
+    }
+  uint16_t* out = reinterpret_cast<uint16_t*>(arena) + wave * 32 * kOutStride;
+#pragma unroll
+  for (int cb = 0; cb < 4; ++cb) {
+    if (cb >= live) break;
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f32x4 v;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = acc[rb][cb][4 * i + c] * s2 + bias[rb][4 * i + c];
+        *reinterpret_cast<uint2*>(out + lrow * kOutStride + rb * 32 + 8 * i + 4 * half) = mxgemm::pack_bf16x4(v);
+      }
+    asm volatile("" ::: "memory");  // a wave's own LDS traffic is in order
+    const int rows = min(32, t.rows - cb * 32);
+    uint16_t* y = a.y + (size_t)(t.row0 + cb * 32) * N + nw;
+    if ((N & 7) == 0) {
+      for (int p = lane; p < rows * 8; p += 64) {
+        const int r = p >> 3, col = (p & 7) * 8;
+        if (nw + col < N)
+          *reinterpret_cast<u32x4*>(y + (size_t)r * N + col) = *reinterpret_cast<const u32x4*>(out + r * kOutStride + col);
+      }
+    } else if (nw + lane < N) {
+      for (int r = 0; r < rows; ++r) y[(size_t)r * N + lane] = out[r * kOutStride + lane];
+    }
+    asm volatile("" ::: "memory");
+  }
+}
+
 int max_tiles(const LinearArgs& a, int tm) {
   const int64_t full = (int64_t)a.R / tm;
   return (int)(a.offsets == nullptr ? ((int64_t)a.R + tm - 1) / tm : full + (a.E < a.R ? a.E : a.R));
@@ -309,6 +563,9 @@ dim3 grid_of(int64_t tiles, int64_t chunks) {
   const int64_t blocks = (tiles * chunks + kXcds - 1) / kXcds * kXcds;
   return blocks <= kMaxX ? dim3((unsigned)blocks) : dim3((unsigned)kMaxX, (unsigned)((blocks + kMaxX - 1) / kMaxX));
 }
+
+constexpr int kTileMinRows = 24;     // rows of an expert on average
+constexpr int kTileMinBlocks = 128;
 
 template <bool kNv, int kC>
 hipError_t launch_few(LinearArgs a, int waves, hipStream_t stream) {
@@ -325,6 +582,12 @@ hipError_t launch_few(LinearArgs a, int waves, hipStream_t stream) {
 
 template <bool kNv>
 hipError_t linear(LinearArgs a, hipStream_t stream) {
+  const int64_t n_tiles = (a.N + kTileN - 1) / kTileN, rows = (int64_t)a.R / a.E;
+  if (rows >= kTileMinRows && n_tiles * max_tiles(a, kTileRows) >= kTileMinBlocks) {
+    a.max_tiles = max_tiles(a, kTileRows);
+    linear_tile_kernel<kNv><<<grid_of(a.max_tiles, n_tiles), 256, 0, stream>>>(a);
+    return hipGetLastError();
+  }
   a.max_tiles = max_tiles(a, kFewRows);
   const int chunks = (a.K + 127) / 128;
   const int waves = chunks <= 24 ? 4 : 8;
