@@ -21,6 +21,7 @@
 namespace {
 
 using mx::bf16x8;
+typedef __attribute__((__vector_size__(2 * sizeof(int)))) int i32x2;
 using mx::f32x16;
 using mx::f32x4;
 using mx::u32x4;
@@ -551,6 +552,238 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs a) {
   }
 }
 
+// dx for row tiles of 128: a block of four waves makes 256 k x 128 rows, each
+// wave 64 k x 128, over chunks of 64 weight rows n.  Stages and swizzles as
+// above: dy pieces of 64 n a row, and the chunk's weight rows, 128 bytes of
+// codes each.  The A operand needs eight n of one k, so the codes are read
+// transposed: of a group of 16 lanes each reads eight bytes of one of eight
+// rows (ds_read_b64_tr_b8), and lane c gets byte c of the eight rows, i.e. k
+// = 2c and 2c + 1 of the group's 32 k for eight n.  Each byte is converted
+// with its row's scale and the halves of neighbouring rows are exchanged
+// (v_perm; NVFP4 rounds the pair itself) into an operand for the even and one
+// for the odd k.  The chunk's scales lie transposed in LDS as bf16 (exact),
+// written one chunk ahead from bytes loaded one chunk before that.
+constexpr int kBackK = 256;
+
+template <bool kNv, int kLive, bool kAligned>
+__device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][4], u32x4* arena, uint16_t* table,
+                                                const __amdgpu_buffer_rsrc_t& rd, const uint16_t* dy,
+                                                const __amdgpu_buffer_rsrc_t& rw, const __amdgpu_buffer_rsrc_t& rs,
+                                                int rows, int K, int N, int k0, int wave, bool work) {
+  const int t = threadIdx.x, lane = t & 63, half = lane >> 5, lrow = lane & 31, mg = (lane >> 4) & 1, c16 = lane & 15;
+  const int chunks = (N + 63) >> 6, kscales = kNv ? K >> 4 : K >> 5;
+  constexpr int kGroups = kNv ? 16 : 8;  // of the block's 256 k
+  const int pr = t >> 3, pc = t & 7;     // this thread's row (of 32) and place in a stage
+  const int part = pc ^ swizzle(pr & 31);
+  const uint32_t doff = (uint32_t)pr * N * 2 + 16 * part;
+  // weight rows pr, pr + 32: the swizzle of the code pieces is the row's low bits
+  const uint32_t woff = (uint32_t)pr * (K >> 1) + (k0 >> 1) + 16 * (pc ^ (pr & 7));
+  // aligned dy rows travel by the load unit, others through registers
+  constexpr int kLoads = kAligned ? 6 : 2;
+  u32x4 dreg[4];
+  auto load_dy = [&](int c) {
+    c = min(c, chunks - 1);
+    const int n = 64 * c + 8 * part;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint16_t* row = dy + (size_t)min(pr + 32 * k, rows - 1) * N;
+      dreg[k] = load_dy8<false>(rd, row, 0, n, N, 64 * c + 64 <= N);
+    }
+  };
+  auto store_dy = [&](int st) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) arena[st * kStageSlots + t + k * 256] = dreg[k];
+  };
+  auto issue = [&](int c, int st, int k) {
+    c = min(c, chunks - 1);
+    u32x4* dst = arena + st * kStageSlots + wave * 64;
+    if (k < 2) load_lds16(rw, dst + kXSlots + k * 256, woff + (uint32_t)(64 * c + 32 * k) * (K >> 1));
+    else load_lds16(rd, dst + (k - 2) * 256, doff + (uint32_t)((k - 2) * 32) * N * 2 + c * 128);
+  };
+  // scales: thread -> row t / 4 of the chunk, a quarter of its groups
+  const int sn = t >> 2, sq = t & 3;
+  uint32_t sreg[2];
+  auto load_scales = [&](int c) {
+    const int n = 64 * c + sn;
+    const uint32_t o = (uint32_t)n * kscales + (k0 >> (kNv ? 4 : 5)) + sq * (kGroups / 4);
+    if (kNv) {  // a row holds an even number of them
+      sreg[0] = __builtin_amdgcn_raw_buffer_load_b16(rs, n < N ? o : kDead, 0, 0);
+      sreg[1] = __builtin_amdgcn_raw_buffer_load_b16(rs, n < N ? o + 2 : kDead, 0, 0);
+    } else {
+      sreg[0] = __builtin_amdgcn_raw_buffer_load_b8(rs, n < N ? o : kDead, 0, 0);
+      sreg[1] = __builtin_amdgcn_raw_buffer_load_b8(rs, n < N ? o + 1 : kDead, 0, 0);
+    }
+  };
+  auto store_scales = [&](int c) {
+    uint16_t* dst = table + (c & 1) * kGroups * 64 + sq * (kGroups / 4) * 64 + sn;
+#pragma unroll
+    for (int i = 0; i < (kNv ? 2 : 1); ++i) {
+      uint32_t two;
+      if (kNv) {
+        const mx::f32x2p v = mx::e4m3x2_operands(sreg[i]);
+        two = mx::pack_bf16x2_rne(v.x, v.y);
+      } else {
+        two = (sreg[0] << 7) | (sreg[1] << 23);
+      }
+      dst[2 * i * 64] = (uint16_t)two;
+      dst[(2 * i + 1) * 64] = (uint16_t)(two >> 16);
+    }
+  };
+
+  load_scales(0);
+  if (!kAligned) {
+    load_dy(0);
+    store_dy(0);
+  }
+  store_scales(0);
+  load_scales(1);
+  if (!kAligned) load_dy(1);
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) issue(0, 0, k);
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) issue(1, 1, k);
+
+  int boff[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) boff[s] = lrow * 8 + ((2 * s + half) ^ swizzle(lrow));
+  // codes: this lane's address for row i = c16 / 2 of the eight of a step, byte 8 (c16 & 1) of the wave's piece mg
+  const int ai = c16 >> 1;
+  const int aoff = (8 * half + ai) * 128 + (((wave * 2 + mg) ^ ai) * 16) + 8 * (c16 & 1);
+  const int soff = (kNv ? wave * 4 + mg * 2 + (c16 >> 3) : wave * 2 + mg) * 64 + 8 * half;
+
+  int st = 0;
+  for (int c = 0; c < chunks; ++c) {
+    const int nst = st == 0 ? 2 : st - 1, st1 = st == 2 ? 0 : st + 1;
+    mxgemm::wait_loads_then_barrier<kLoads>();
+    // the next chunk's scales (and unaligned dy) into LDS, the one's after that on their way
+    store_scales(c + 1);
+    load_scales(c + 2);
+    if (!kAligned) {
+      store_dy(st1);
+      load_dy(c + 2);
+    }
+    if (!work) {
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) issue(c + 2, nst, k);
+      st = st1;
+      continue;
+    }
+    const u32x4* base = arena + st * kStageSlots;
+    const uint8_t* codes = reinterpret_cast<const uint8_t*>(base + kXSlots) + aoff;
+    const uint16_t* sc = table + (c & 1) * kGroups * 64 + soff;
+    u32x4 b[4][kLive], sv[4];
+    i32x2 w[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      w[s] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)(codes + s * 16 * 128));
+      sv[s] = *reinterpret_cast<const u32x4*>(sc + 16 * s);
+#pragma unroll
+      for (int cb = 0; cb < kLive; ++cb) b[s][cb] = base[boff[s] + cb * 256];
+    }
+    if (64 * c + 64 > N) {  // rows past N: zero weights times zero dy (unaligned dy came with its zeros)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int left = N - (64 * c + 16 * s + 8 * half);  // of this lane's eight n
+        if (left <= 0) w[s] = i32x2{0, 0};
+        else if (left < 8) {
+          w[s][0] &= left < 4 ? (int)((1u << (8 * left)) - 1u) : -1;
+          w[s][1] &= left > 4 ? (int)((1u << (8 * (left - 4))) - 1u) : 0;
+        }
+#pragma unroll
+        for (int cb = 0; cb < kLive; ++cb)
+          if (kAligned && left <= 0) b[s][cb] = u32x4{0u, 0u, 0u, 0u};
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      u32x4 op[2];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {  // rows 2p, 2p + 1 of the eight
+        const uint32_t d = (uint32_t)w[s][p >> 1];
+        const float f0 = __uint_as_float(sv[s][p] << 16), f1 = __uint_as_float(sv[s][p] & 0xffff0000u);
+        if (kNv) {
+          const mx::f32x2e v0 = (p & 1) ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 2)
+                                        : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 0);
+          const mx::f32x2e v1 = (p & 1) ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 3)
+                                        : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 1);
+          op[0][p] = mx::pack_bf16x2_rne(v0.x * f0, v1.x * f1);
+          op[1][p] = mx::pack_bf16x2_rne(v0.y * f0, v1.y * f1);
+        } else {
+          const uint32_t r0 = (p & 1) ? mx::fp4x2_to_bf16x2<2>(d, f0) : mx::fp4x2_to_bf16x2<0>(d, f0);
+          const uint32_t r1 = (p & 1) ? mx::fp4x2_to_bf16x2<3>(d, f1) : mx::fp4x2_to_bf16x2<1>(d, f1);
+          op[0][p] = __builtin_amdgcn_perm(r1, r0, 0x05040100u);
+          op[1][p] = __builtin_amdgcn_perm(r1, r0, 0x07060302u);
+        }
+      }
+#pragma unroll
+      for (int cb = 0; cb < kLive; ++cb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          acc[e][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(mx::as_bf16x8(op[e]), mx::as_bf16x8(b[s][cb]),
+                                                               acc[e][cb], 0, 0, 0);
+      if (2 * s < kLoads) {
+        issue(c + 2, nst, 2 * s);
+        issue(c + 2, nst, 2 * s + 1);
+      }
+    }
+    st = st1;
+  }
+}
+
+template <bool kNv, bool kAligned>
+__global__ __launch_bounds__(256, 2) void linear_backward_tile_kernel(LinearArgs a) {
+  __shared__ __attribute__((aligned(16))) u32x4 arena[kStages * kStageSlots];
+  __shared__ __attribute__((aligned(16))) uint16_t table[2 * (kNv ? 16 : 8) * 64];
+  const int k_tiles = (a.K + kBackK - 1) / kBackK;
+  int ti, kt;
+  if (!map_tile(a, kTileRows, k_tiles, ti, kt)) return;  // uniform per block
+  Tile t;
+  if (!find_tile(a, kTileRows, ti, t)) return;
+  const int K = a.K, N = a.N, k0 = kt * kBackK;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int kscales = kNv ? K >> 4 : K >> 5;
+  const uint16_t* dy = a.x + (size_t)t.row0 * N;
+  const auto rd = buffer(dy, (uint32_t)t.rows * N * 2);
+  const auto rw = buffer(a.blocks + (size_t)t.e * N * (K >> 1), (uint32_t)N * (K >> 1));
+  const auto rs = buffer(a.scales + (size_t)t.e * N * kscales, (uint32_t)N * kscales);
+
+  f32x16 acc[2][4] = {};
+  const int live = (t.rows + 31) >> 5;
+  const bool work = k0 + wave * 64 < K;  // uniform: a wave past K only loads its share
+  if (live == 4) backward_chunks<kNv, 4, kAligned>(acc, arena, table, rd, dy, rw, rs, t.rows, K, N, k0, wave, work);
+  else if (live == 3) backward_chunks<kNv, 3, kAligned>(acc, arena, table, rd, dy, rw, rs, t.rows, K, N, k0, wave, work);
+  else if (live == 2) backward_chunks<kNv, 2, kAligned>(acc, arena, table, rd, dy, rw, rs, t.rows, K, N, k0, wave, work);
+  else backward_chunks<kNv, 1, kAligned>(acc, arena, table, rd, dy, rw, rs, t.rows, K, N, k0, wave, work);
+
+  // lane (row lane & 31 of the block, half): k = 32 (b / 2) + 16 (b & 1) + 8 half + 2 r + e of the wave's 64 in
+  // acc[e][.][4b + r]
+  mxgemm::wait_loads_then_barrier<0>();  // no load still writes LDS, no wave still reads it
+  if (!work) return;                     // no barrier follows
+  const int kw = k0 + wave * 64, half = lane >> 5, lrow = lane & 31;
+  const float s2 = kNv ? a.scale2[t.e] : 1.0f;
+  uint16_t* out = reinterpret_cast<uint16_t*>(arena) + wave * 32 * kOutStride;
+#pragma unroll
+  for (int cb = 0; cb < 4; ++cb) {
+    if (cb >= live) break;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      u32x4 v;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = mx::pack_bf16x2_rne(acc[0][cb][4 * b + r] * s2, acc[1][cb][4 * b + r] * s2);
+      *reinterpret_cast<u32x4*>(out + lrow * kOutStride + 32 * (b >> 1) + 16 * (b & 1) + 8 * half) = v;
+    }
+    asm volatile("" ::: "memory");  // a wave's own LDS traffic is in order
+    const int rows = min(32, t.rows - cb * 32);
+    uint16_t* dx = a.y + (size_t)(t.row0 + cb * 32) * K + kw;
+    for (int p = lane; p < rows * 8; p += 64) {
+      const int r = p >> 3, col = (p & 7) * 8;
+      if (kw + col < K)
+        *reinterpret_cast<u32x4*>(dx + (size_t)r * K + col) = *reinterpret_cast<const u32x4*>(out + r * kOutStride + col);
+    }
+    asm volatile("" ::: "memory");
+  }
+}
+
 int max_tiles(const LinearArgs& a, int tm) {
   const int64_t full = (int64_t)a.R / tm;
   return (int)(a.offsets == nullptr ? ((int64_t)a.R + tm - 1) / tm : full + (a.E < a.R ? a.E : a.R));
@@ -599,6 +832,14 @@ hipError_t linear(LinearArgs a, hipStream_t stream) {
 
 template <bool kNv>
 hipError_t linear_backward(LinearArgs a, hipStream_t stream) {
+  const int64_t k_tiles = (a.K + kBackK - 1) / kBackK, rows = (int64_t)a.R / a.E;
+  if (rows >= kTileMinRows && k_tiles * max_tiles(a, kTileRows) >= kTileMinBlocks) {
+    a.max_tiles = max_tiles(a, kTileRows);
+    const dim3 tile_grid = grid_of(a.max_tiles, k_tiles);
+    if (a.N % 8 == 0) linear_backward_tile_kernel<kNv, true><<<tile_grid, 256, 0, stream>>>(a);
+    else linear_backward_tile_kernel<kNv, false><<<tile_grid, 256, 0, stream>>>(a);
+    return hipGetLastError();
+  }
   a.max_tiles = max_tiles(a, kFewRows);
   const int steps = (a.N + 31) / 32;
   const int waves = steps < 8 ? steps : 8;

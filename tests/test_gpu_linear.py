@@ -199,6 +199,71 @@ def test_infinite_inputs_stay_in_their_rows(gpu, fmt, R, N, K):
         assert not bool(torch.isfinite(got[0]).any()) and bool(torch.isnan(got[R]).all())
 
 
+# Batches whose size takes the 128-row tiles, at sizes that end inside a chunk, a block of rows or a tile.
+def _many(seed, E=128, mean=40):
+    rng = np.random.default_rng(seed)
+    counts = rng.poisson(mean, E)
+    counts[:12] = [0, 1, 31, 32, 33, 64, 97, 127, 128, 129, 256, 300]
+    return [int(c) for c in rng.permutation(counts)]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("N,K", [(1, 32), (8, 64), (33, 96), (64, 160), (72, 544), (130, 288), (200, 256), (256, 320),
+                                 (257, 32), (321, 224), (264, 1056)])
+def test_many_rows_grouped(gpu, fmt, N, K):
+    counts = _many(N + K)
+    w = Weights(fmt, len(counts), N, K, seed=N)
+    check_both(gpu, w, sum(counts) + 11, offsets_of(counts, 7), bias=N % 2 == 1, label=f"many {fmt}")
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("R,N,K", [(17_000, 40, 96), (2500, 2050, 1568), (4000, 1030, 1088)])
+def test_many_rows_dense(gpu, fmt, R, N, K):
+    w = Weights(fmt, 1, N, K, dense=True, seed=R)
+    check_both(gpu, w, R, label=f"many dense {fmt}")
+
+
+@pytest.mark.parametrize("fmt,nan", [("mxfp4", 0xFF), ("nvfp4", 0x7F)])
+def test_many_rows_nan_scales(gpu, fmt, nan):
+    N, K = 70, 192
+    counts = _many(3)
+    off = offsets_of(counts)
+    e = int(np.argmax(counts))
+    w = Weights(fmt, len(counts), N, K, seed=4)
+    w.s[e, 69, -1] = nan
+    w.s[e, 3, 0] = nan
+    w.upload()
+    rng = np.random.default_rng(6)
+    R, first = sum(counts), int(np.sum(counts[:e]))
+    y, dx = f64(w.linear(gpu, bf16(rng, R, K), None, off)), f64(w.backward(gpu, bf16(rng, R, N), off))
+    bad = np.zeros(y.shape, bool)
+    bad[first:first + counts[e], [[3], [69]]] = True
+    assert np.array_equal(np.isnan(y), bad)
+    bad = np.zeros(dx.shape, bool)
+    bad[first:first + counts[e], :w.group] = bad[first:first + counts[e], K - w.group:] = True
+    assert np.array_equal(np.isnan(dx), bad)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("N,K", [(97, 160), (72, 96), (64, 64)])
+def test_many_rows_infinite_inputs(gpu, fmt, N, K):
+    counts = _many(5)
+    R = sum(counts)
+    w = Weights(fmt, len(counts), N, K, seed=3)
+    rng = np.random.default_rng(7)
+    off = offsets_of(counts)
+    at = np.sort(rng.permutation(R)[:200])
+    rest = np.setdiff1d(np.arange(R), at)
+    for width, call in ((K, lambda v: w.linear(gpu, v, None, off)), (N, lambda v: w.backward(gpu, v, off))):
+        v = bf16(rng, R, width)
+        clean = call(v).clone()
+        v[at[::2]] = float("inf")
+        v[at[1::2]] = float("nan")
+        got = call(v)
+        assert torch.equal(got[rest], clean[rest])
+        assert not bool(torch.isfinite(got[at]).any())
+
+
 def test_offsets_out_of_range_are_clamped(gpu):
     w = Weights("mxfp4", 4, 64, 64, seed=9)
     rng = np.random.default_rng(8)
@@ -206,8 +271,10 @@ def test_offsets_out_of_range_are_clamped(gpu):
     off = torch.tensor([-7, 10, 10, 45, 2 ** 31 - 1], dtype=torch.int32).cuda()
     want, mag, _ = X.linear(f64(x), w.f64, [0, 10, 10, 45, 50])
     assert_sums(w.linear(gpu, x, None, off), want, mag, 64, "clamped")
-    down = torch.tensor([40, 10, 30, 20, 50], dtype=torch.int32).cuda()  # descending in places: in bounds all the same
-    w.linear(gpu, x, None, down), w.backward(gpu, x, down)
+    for scale in (1, 100):  # descending in places: in bounds all the same
+        down = torch.tensor([40, 10, 30, 20, 50], dtype=torch.int32).cuda() * scale
+        x = bf16(rng, 50 * scale, 64)
+        w.linear(gpu, x, None, down), w.backward(gpu, x, down)
     torch.cuda.synchronize()
 
 
@@ -237,7 +304,7 @@ def test_by_differences(gpu):
         assert abs(lhs - rhs) <= tol and tol <= 0.05 * scale
 
 
-@pytest.mark.parametrize("counts", [[3, 0, 1], [40, 17, 0], [300, 129, 5]])
+@pytest.mark.parametrize("counts", [[3, 0, 1], [40, 17, 0], [300, 129, 5], [7000, 5000, 5000]])
 def test_captured_and_replayed(gpu, counts):
     w = Weights("nvfp4", 3, 200, 256, seed=14)
     R = sum(counts)
