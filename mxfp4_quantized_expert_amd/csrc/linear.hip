@@ -14,6 +14,8 @@
 // at most five for NVFP4), so every product of the bf16 MFMA is exact and the
 // sums are its fp32 accumulation; s2 and the bias follow in fp32 and the
 // result is rounded once.
+#include <type_traits>
+
 #include "expert_device.h"
 #include "internal.h"
 #include "mx_device.h"
@@ -337,24 +339,21 @@ __global__ __launch_bounds__(512) void linear_backward_few_kernel(LinearArgs a) 
 
 // --------------------------------------------------------------- many rows
 
-// Scale bytes of one weight row, 16 at a time from byte offset `o` of the
-// expert's scales: aligned dwords and a funnel shift, because a row of scales
-// starts at any byte.  The buffer starts at a dword and ends with the dword
-// that holds its last byte.
+// Scale bytes of one weight row, 32 at a time from byte offset `o` of the
+// buffer: aligned dwords and a funnel shift, because a row of scales starts
+// at any byte.  The buffer starts at a dword and ends with the dword that
+// holds its last byte.
 struct ScaleBytes {
-  uint32_t d[5];
+  uint32_t d[9];
   __device__ __forceinline__ void load(const __amdgpu_buffer_rsrc_t& r, uint32_t o) {
-    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, o & ~3u, 0, 0);
+    o &= ~3u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = v[i];
-    d[4] = __builtin_amdgcn_raw_buffer_load_b32(r, (o & ~3u) + 16, 0, 0);
-  }
-  // the next kBytes bytes to the front
-  template <int kBytes>
-  __device__ __forceinline__ void drop() {
+    for (int h = 0; h < 2; ++h) {
+      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, o + 16 * h, 0, 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = kBytes == 4 ? d[i + 1] : __builtin_amdgcn_alignbit(d[i + 1], d[i], 8 * kBytes);
-    if (kBytes != 4) d[4] >>= 8 * kBytes;
+      for (int i = 0; i < 4; ++i) d[4 * h + i] = v[i];
+    }
+    d[8] = __builtin_amdgcn_raw_buffer_load_b32(r, o + 32, 0, 0);
   }
 };
 
@@ -373,7 +372,7 @@ struct ScaleBytes {
 constexpr int kTileRows = 128, kTileN = 256;
 constexpr int kXSlots = kTileRows * 8, kWSlots = kTileN * 2, kStageSlots = kXSlots + kWSlots;
 constexpr int kStages = 3;
-constexpr int kChunkLoads = (kXSlots + kWSlots) / 256;  // of a thread
+constexpr int kArenaSlots = 5120;  // 16-byte slots of the forward's rings: 80 KB
 
 __device__ __forceinline__ int swizzle(int row) { return (row ^ (row >> 3)) & 7; }
 
@@ -381,103 +380,146 @@ __device__ __forceinline__ void load_lds16(const __amdgpu_buffer_rsrc_t& r, u32x
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0, 0);
 }
 
+// Stages in flight by the number of live row blocks: a block without rows
+// needs no room, and the fewer rows share the weights, the more of them have
+// to be on their way to keep HBM busy.  x stages hold 64 k, weight stages 128
+// k: 64 bytes of a row at a time stream from HBM at 4.7 TB/s, 32 bytes at
+// 3.3 (load-unit reads of 565 MB in this pattern, no arithmetic).  Both rings
+// within 80 KB (two blocks a CU).
+template <int kLive>
+struct Rings {
+  static constexpr int kX = kLive >= 4 ? 3 : kLive >= 2 ? 4 : 6;
+  static constexpr int kW = kLive >= 3 ? 2 : 3;
+  static constexpr int kXStage = kLive * 256, kWStage = kTileN * 4;  // 16-byte slots
+  // Iteration c issues (even c: 4 loads of the weights of chunks c + 2 kW - 2 and the next one, then) kLive loads of
+  // x of chunk c + kX - 1.  Loads that may be in flight when chunk c is read: those issued after its x, and after
+  // its weights.
+  static constexpr int after_x(int odd) {
+    int n = 0;
+    for (int i = 1; i <= kX - 2; ++i) n += kLive + (((odd + i) & 1) == 0 ? 4 : 0);
+    return n;
+  }
+  static constexpr int kAfterW = kLive * 2 * (kW - 1) + 4 * (kW - 2);
+  static constexpr int kAheadOdd = after_x(1), kAheadEven = after_x(0) < kAfterW ? after_x(0) : kAfterW;
+  static_assert(kX * kXStage + kW * kWStage <= kArenaSlots, "rings fit in the arena");
+};
+
 // The chunk loop over kLive blocks of 32 rows.
 template <bool kNv, int kLive>
 __device__ __forceinline__ void tile_chunks(f32x16 (&acc)[2][4], u32x4* arena, const __amdgpu_buffer_rsrc_t& rx,
                                             const __amdgpu_buffer_rsrc_t& rw, const __amdgpu_buffer_rsrc_t& rs,
                                             int K, uint32_t scale0, int kscales, int wave, bool work) {
+  using Ring = Rings<kLive>;
   const int t = threadIdx.x, lane = t & 63, half = lane >> 5, lrow = lane & 31;
-  const int chunks = (K + 63) >> 6;
+  const int chunks = (K + 63) >> 6, pairs = (chunks + 1) >> 1;
+  u32x4* const wring = arena + Ring::kX * Ring::kXStage;
   // this thread's pieces of a stage
   const int xr = t >> 3;
   const uint32_t xoff = (uint32_t)xr * K * 2 + 16 * ((t & 7) ^ swizzle(xr & 31));
-  const uint32_t woff = (uint32_t)(t >> 1) * (K >> 1) + 16 * (t & 1);
-  auto issue = [&](int c, int st, int k) {
-    c = min(c, chunks - 1);
-    u32x4* dst = arena + st * kStageSlots + wave * 64;
-    if (k < 4) load_lds16(rx, dst + k * 256, xoff + (uint32_t)(k * 32) * K * 2 + c * 128);
-    else load_lds16(rw, dst + kXSlots + (k - 4) * 256, woff + (uint32_t)((k - 4) * 128) * (K >> 1) + c * 32);
+  const uint32_t woff = (uint32_t)(t >> 2) * (K >> 1) + 16 * ((t & 3) ^ ((t >> 4) & 3));
+  auto issue_x = [&](int c, int st, int k) {
+    load_lds16(rx, arena + st * Ring::kXStage + wave * 64 + k * 256,
+               xoff + (uint32_t)(k * 32) * K * 2 + min(c, chunks - 1) * 128);
   };
-#pragma unroll
-  for (int k = 0; k < kChunkLoads; ++k) issue(0, 0, k);
-#pragma unroll
-  for (int k = 0; k < kChunkLoads; ++k) issue(1, 1, k);
+  auto issue_w = [&](int s, int st, int k) {
+    load_lds16(rw, wring + st * Ring::kWStage + wave * 64 + k * 256,
+               woff + (uint32_t)(k * 64) * (K >> 1) + min(s, pairs - 1) * 64);
+  };
+  int xs = 0, ws = 0;  // stages of the chunk (pair) being read
 
-  // this lane's scale rows: 16 bytes hold the groups of kSpan chunks
-  constexpr int kStep = kNv ? 4 : 2, kSpan = 16 / kStep;
-  ScaleBytes sb[2];
-  const uint32_t so[2] = {scale0 + (uint32_t)(wave * 64 + lrow) * kscales + half * (kStep / 2),
-                          scale0 + (uint32_t)(wave * 64 + 32 + lrow) * kscales + half * (kStep / 2)};
+  // this lane's scale row (of the wave's 64): 32 bytes hold the groups of kSpan pairs of chunks
+  constexpr int kStep = kNv ? 2 : 1, kSpan = 8 / kStep;  // dwords of a pair
+  const uint32_t so = scale0 + (uint32_t)(wave * 64 + lane) * kscales;
+  ScaleBytes sb, next;
+  next.load(rs, so);
+  constexpr int kPrologue = 2 * (Ring::kW - 1) > Ring::kX - 1 ? 2 * (Ring::kW - 1) : (Ring::kX / 2) * 2;
+#pragma unroll
+  for (int c = -kPrologue; c < 0; ++c) {
+    if (c % 2 == 0 && c / 2 + Ring::kW - 1 >= 0) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) issue_w(c / 2 + Ring::kW - 1, c / 2 + Ring::kW - 1, k);
+    }
+    if (c + Ring::kX - 1 >= 0) {
+#pragma unroll
+      for (int k = 0; k < kLive; ++k) issue_x(c + Ring::kX - 1, c + Ring::kX - 1, k);
+    }
+  }
   int boff[4];
 #pragma unroll
   for (int s = 0; s < 4; ++s) boff[s] = lrow * 8 + ((4 * half + s) ^ swizzle(lrow));
-  const int aoff = kXSlots + (wave * 64 + lrow) * 2 + half;
+  const int arow = (wave * 64 + lrow) * 4, aswz = (lrow >> 2) & 3;
 
-  int st = 0;
-  for (int c = 0; c < chunks; ++c) {
-    if (c % kSpan == 0) {  // uniform
+  // chunk 2s + kOdd, its scale dword(s) in row order: e[0] of the lane's first weight row, e[1] of its second
+  auto chunk = [&](auto odd, int c, int s, uint32_t e0, uint32_t e1) {
+    constexpr int kOdd = decltype(odd)::value;
+    constexpr int kIssue = kLive + (kOdd ? 0 : 4);
+    const int xnext = xs == 0 ? Ring::kX - 1 : xs - 1, wnext = ws == 0 ? Ring::kW - 1 : ws - 1;
+    auto issue = [&](int k) {
+      if (!kOdd && k < 4) issue_w(s + Ring::kW - 1, wnext, k);
+      else issue_x(c + Ring::kX - 1, xnext, k - (kOdd ? 0 : 4));
+    };
+    if (work) {
+      const u32x4* xbase = arena + xs * Ring::kXStage;
+      const u32x4* wbase = wring + ws * Ring::kWStage + arow + ((2 * kOdd + half) ^ aswz);
+      u32x4 w[2];
+      bf16x8 b[4][kLive];
 #pragma unroll
-      for (int rb = 0; rb < 2; ++rb) sb[rb].load(rs, so[rb] + c * kStep);
+      for (int rb = 0; rb < 2; ++rb) w[rb] = wbase[rb * 128];
 #pragma unroll
-      for (int rb = 0; rb < 2; ++rb)
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int cb = 0; cb < kLive; ++cb) b[i][cb] = mx::as_bf16x8(xbase[boff[i] + cb * 256]);
+      if (64 * c + 64 > K && half == 1) {  // the half chunk past K: zero weights times zero rows
+        e0 = e1 = 0u;
+#pragma unroll
+        for (int rb = 0; rb < 2; ++rb) w[rb] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          sb[rb].d[i] = __builtin_amdgcn_alignbit(sb[rb].d[i + 1], sb[rb].d[i], 8 * (so[rb] & 3u));
-    }
-    mxgemm::wait_loads_then_barrier<kChunkLoads>();
-    const int nst = st == 0 ? 2 : st - 1;  // (c + 2) % 3
-    if (!work) {
 #pragma unroll
-      for (int k = 0; k < kChunkLoads; ++k) issue(c + 2, nst, k);
-      st = st == 2 ? 0 : st + 1;
-      continue;
-    }
-    const u32x4* base = arena + st * kStageSlots;
-    u32x4 w[2];
-    bf16x8 b[4][kLive];
+          for (int cb = 0; cb < kLive; ++cb) b[i][cb] = mx::as_bf16x8(u32x4{0u, 0u, 0u, 0u});
+      }
+      const uint32_t sh = kNv ? 16 * half : 16 * kOdd + 8 * half;
+      e0 >>= sh;
+      e1 >>= sh;
+      const GroupScale<kNv> g0(e0 & 255u, (e0 >> 8) & 255u), g1(e1 & 255u, (e1 >> 8) & 255u);
 #pragma unroll
-    for (int rb = 0; rb < 2; ++rb) w[rb] = base[aoff + rb * 64];
+      for (int i = 0; i < 4; ++i) {
+        const bf16x8 a0 = mx::as_bf16x8(g0.convert(w[0][i], i)), a1 = mx::as_bf16x8(g1.convert(w[1][i], i));
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int cb = 0; cb < kLive; ++cb) b[s][cb] = mx::as_bf16x8(base[boff[s] + cb * 256]);
-    uint32_t s0[2], s1[2];
-#pragma unroll
-    for (int rb = 0; rb < 2; ++rb) {
-      s0[rb] = sb[rb].d[0] & 255u;
-      s1[rb] = kNv ? (sb[rb].d[0] >> 8) & 255u : 0u;
-      sb[rb].template drop<kStep>();
-    }
-    if (64 * c + 64 > K) {  // the half chunk past K: zero weights times zero rows
-      const bool dead = half == 1;
-#pragma unroll
-      for (int rb = 0; rb < 2; ++rb) {
-        if (dead) {
-          w[rb] = u32x4{0u, 0u, 0u, 0u};
-          s0[rb] = s1[rb] = 0u;
+        for (int cb = 0; cb < kLive; ++cb) {
+          acc[0][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a0, b[i][cb], acc[0][cb], 0, 0, 0);
+          acc[1][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a1, b[i][cb], acc[1][cb], 0, 0, 0);
         }
+#pragma unroll
+        for (int k = 2 * i; k < 2 * i + 2; ++k)
+          if (k < kIssue) issue(k);
       }
+    } else {
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int cb = 0; cb < kLive; ++cb)
-          if (dead) b[s][cb] = mx::as_bf16x8(u32x4{0u, 0u, 0u, 0u});
+      for (int k = 0; k < kIssue; ++k) issue(k);
     }
-    const GroupScale<kNv> g0(s0[0], s1[0]), g1(s0[1], s1[1]);
+    xs = xs == Ring::kX - 1 ? 0 : xs + 1;
+  };
+  // dword i of the lanes' rows to the rows that the lanes multiply with
+  auto spread = [&](int i) { return __builtin_amdgcn_permlane32_swap(sb.d[i], sb.d[i], false, false); };
+
+  for (int s = 0; s < pairs; ++s) {
+    mxgemm::wait_loads_then_barrier<Ring::kAheadEven>();
+    if (s % kSpan == 0) {  // uniform
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const bf16x8 a0 = mx::as_bf16x8(g0.convert(w[0][s], s)), a1 = mx::as_bf16x8(g1.convert(w[1][s], s));
-#pragma unroll
-      for (int cb = 0; cb < kLive; ++cb) {
-        acc[0][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a0, b[s][cb], acc[0][cb], 0, 0, 0);
-        acc[1][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a1, b[s][cb], acc[1][cb], 0, 0, 0);
-      }
-      if (s < 3) {
-        issue(c + 2, nst, 2 * s);
-        issue(c + 2, nst, 2 * s + 1);
-      }
+      for (int i = 0; i < 8; ++i) sb.d[i] = __builtin_amdgcn_alignbit(next.d[i + 1], next.d[i], 8 * (so & 3u));
     }
-    st = st == 2 ? 0 : st + 1;
+    if (s % kSpan == kSpan - 1) next.load(rs, so + 4 * kStep * (s + 1));
+    const auto e = spread(0);
+    chunk(std::integral_constant<int, 0>{}, 2 * s, s, e[0], e[1]);
+    if (2 * s + 1 < chunks) {  // uniform
+      mxgemm::wait_loads_then_barrier<Ring::kAheadOdd>();
+      const auto o = spread(kStep - 1);
+      chunk(std::integral_constant<int, 1>{}, 2 * s + 1, s, o[0], o[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8 - kStep; ++i) sb.d[i] = sb.d[i + kStep];
+    ws = ws == Ring::kW - 1 ? 0 : ws + 1;
   }
 }
 
@@ -486,7 +528,7 @@ constexpr int kOutStride = 72;  // bf16 per row: 64 and padding
 
 template <bool kNv>
 __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs a) {
-  __shared__ __attribute__((aligned(16))) u32x4 arena[kStages * kStageSlots];
+  __shared__ __attribute__((aligned(16))) u32x4 arena[kArenaSlots];
   const int n_tiles = (a.N + kTileN - 1) / kTileN;
   int ti, nt;
   if (!map_tile(a, kTileRows, n_tiles, ti, nt)) return;  // uniform per block
