@@ -20,6 +20,7 @@
 // is rounded once, and no result depends on the order of blocks.  Every
 // kernel here moves each byte a few flops at most: HBM is the bound, and for
 // a handful of tokens the latency of a launch.
+#include "../../include/mxfp4moe.h"
 #include "internal.h"
 #include "mx_device.h"
 
@@ -54,29 +55,41 @@ constexpr int kPairChunk = 2048;
 __device__ void invert_chunk(const int32_t* __restrict__ sorted_pairs, int64_t R, int64_t P, int chunk,
                              int32_t* __restrict__ pair_rows) {
   __shared__ int32_t lds[kPairChunk];
-  for (int i = threadIdx.x; i < kPairChunk; i += kThreads) lds[i] = -1;
+  for (int i = threadIdx.x; i < kPairChunk; i += blockDim.x) lds[i] = -1;
   __syncthreads();
   const int64_t first = (int64_t)chunk * kPairChunk;
-  for (int64_t i = threadIdx.x; i < R; i += kThreads) {
+#pragma unroll 8
+  for (int64_t i = threadIdx.x; i < R; i += blockDim.x) {
     const int64_t d = (int64_t)sorted_pairs[i] - first;
     if (d >= 0 && d < kPairChunk) atomicMax(&lds[d], (int)i);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < kPairChunk; i += kThreads)
+  for (int i = threadIdx.x; i < kPairChunk; i += blockDim.x)
     if (first + i < P) pair_rows[first + i] = lds[i];
 }
 
+__global__ __launch_bounds__(1024) void invert_kernel(const int32_t* __restrict__ sorted_pairs, int64_t R, int64_t P,
+                                                      int32_t* __restrict__ pair_rows) {
+  invert_chunk(sorted_pairs, R, P, blockIdx.x, pair_rows);
+}
+
 // ... and for a batch of many pairs, where every block reading every row's
-// pair would cost more than a launch: this clears pair_rows, and the copying
-// blocks enter their rows (the larger one wins, whatever the order).
+// pair would cost more than a second launch: clear, then enter the rows (the
+// larger one wins, whatever the order).
 constexpr int64_t kInvertInBlocks = 65536;
 __global__ __launch_bounds__(kThreads) void clear_pair_rows_kernel(int32_t* __restrict__ pair_rows, int64_t P) {
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < P; i += (int64_t)gridDim.x * kThreads)
     pair_rows[i] = -1;
 }
+__global__ __launch_bounds__(kThreads) void enter_pair_rows_kernel(const int32_t* __restrict__ sorted_pairs,
+                                                                   int64_t R, int64_t P,
+                                                                   int32_t* __restrict__ pair_rows) {
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < R; i += (int64_t)gridDim.x * kThreads)
+    if (in_range(sorted_pairs[i], P)) atomicMax(&pair_rows[sorted_pairs[i]], (int)i);
+}
 
-// rows[i] = x[sorted_pairs[i] / top_k]; the blocks before copy_block0 write
-// pair_rows (copy_block0 == 0: it is cleared, and the copying blocks do).
+// Small batches, one launch: rows[i] = x[sorted_pairs[i] / top_k], a piece to
+// a lane; the blocks before copy_block0 write pair_rows meanwhile.
 template <typename V>
 __global__ __launch_bounds__(kThreads) void permute_kernel(const V* __restrict__ x,
                                                            const int32_t* __restrict__ sorted_pairs,
@@ -94,13 +107,72 @@ __global__ __launch_bounds__(kThreads) void permute_kernel(const V* __restrict__
     const unsigned i = (unsigned)g / (unsigned)sp.segs;
     const int32_t p = sorted_pairs[i];
     const bool live = in_range(p, P);
-    if (copy_block0 == 0 && live && (threadIdx.x & (lanes - 1)) == 0 && (unsigned)g % (unsigned)sp.segs == 0)
-      atomicMax(&pair_rows[p], (int)i);
     const V* src = x + (size_t)(live ? p / top_k : 0) * sp.nv;
     V* dst = rows + (size_t)i * sp.nv;
     for (int v = (int)((unsigned)g % (unsigned)sp.segs) * lanes + (threadIdx.x & (lanes - 1)); v < sp.nv;
          v += lanes * sp.segs)
       dst[v] = live ? src[v] : V{};
+  }
+}
+
+// Clears the rows that hold no pair, a wave looking at kZeroRows of them (they
+// lie together behind a rank's share of the rows): block `block` of `blocks`.
+// With x, the earlier row of a pair listed twice gets its token's row instead.
+constexpr int kZeroRows = 4;
+template <typename V>
+__device__ __forceinline__ void clear_empty_rows(V* __restrict__ rows, const V* __restrict__ x, int top_k, const int32_t* __restrict__ sorted_pairs,
+                                                 const int32_t* __restrict__ pair_rows, int64_t R, int64_t P, int nv,
+                                                 int block, int blocks) {
+  const int lane = mx::lane_id();
+  const int64_t waves = (int64_t)blocks * (kThreads / 64);
+  for (int64_t r0 = ((int64_t)block * (kThreads / 64) + (threadIdx.x >> 6)) * kZeroRows; r0 < R;
+       r0 += waves * kZeroRows) {
+    const int64_t r = r0 + lane;
+    bool empty = false;
+    int32_t p = -1;
+    if (lane < kZeroRows && r < R) {
+      p = sorted_pairs[r];
+      empty = !in_range(p, P) || pair_rows[p] != (int32_t)r;
+    }
+    uint64_t todo = __ballot(empty);
+    while (todo != 0) {
+      const int b = __builtin_ctzll(todo);
+      todo &= todo - 1;
+      const int32_t pb = __builtin_amdgcn_readlane(p, b);
+      const V* src = x != nullptr && in_range(pb, P) ? x + (size_t)(pb / top_k) * nv : nullptr;
+      for (int v = lane; v < nv; v += 64) rows[(size_t)(r0 + b) * nv + v] = src != nullptr ? src[v] : V{};
+    }
+  }
+}
+
+// Large batches, with pair_rows written before: a token's pieces are read once
+// and stored to its top_k rows; the blocks from zero_block0 on clear the rows
+// that hold no pair.
+template <typename V>
+__global__ __launch_bounds__(kThreads) void permute_by_token_kernel(const V* __restrict__ x,
+                                                                    const int32_t* __restrict__ sorted_pairs,
+                                                                    V* __restrict__ rows,
+                                                                    const int32_t* __restrict__ pair_rows, int64_t T,
+                                                                    int64_t R, int top_k, RowSplit sp,
+                                                                    int zero_block0) {
+  if ((int)blockIdx.x >= zero_block0) {
+    clear_empty_rows(rows, x, top_k, sorted_pairs, pair_rows, R, T * top_k, sp.nv, blockIdx.x - zero_block0,
+                     gridDim.x - zero_block0);
+    return;
+  }
+  const int lanes = 1 << sp.lg;
+  for (int64_t g = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> sp.lg; g < T * sp.segs;
+       g += ((int64_t)zero_block0 * kThreads) >> sp.lg) {
+    const unsigned t = (unsigned)g / (unsigned)sp.segs;
+    const V* src = x + (size_t)t * sp.nv;
+    for (int v = (int)((unsigned)g % (unsigned)sp.segs) * lanes + (threadIdx.x & (lanes - 1)); v < sp.nv;
+         v += lanes * sp.segs) {
+      const V piece = src[v];
+      for (int j = 0; j < top_k; ++j) {
+        const int32_t r = pair_rows[(size_t)t * top_k + j];
+        if (in_range(r, R)) __builtin_nontemporal_store(piece, rows + (size_t)r * sp.nv + v);
+      }
+    }
   }
 }
 
@@ -120,97 +192,147 @@ __global__ __launch_bounds__(kThreads) void unpermute_kernel(const E* __restrict
     for (int v = (int)((unsigned)g % (unsigned)sp.segs) * lanes + (threadIdx.x & (lanes - 1)); v < sp.nv;
          v += lanes * sp.segs) {
       typename P::fvec sum = {};
-      for (int j = 0; j < top_k; ++j) {
-        const size_t p = (size_t)t * top_k + j;
-        const int32_t r = pair_rows[p];
-        if (!in_range(r, R)) continue;
-        const typename P::fvec z = __builtin_convertvector(src[(size_t)r * sp.nv + v], typename P::fvec);
-        const float w = weights != nullptr ? weights[p] : 1.0f;
+      for (int j0 = 0; j0 < top_k; j0 += 4) {  // four pairs' pieces in flight
+        typename P::vec z[4];
+        float w[4];
+        bool live[4];
 #pragma unroll
-        for (int c = 0; c < P::kN; ++c) sum[c] = __builtin_fmaf(w, z[c], sum[c]);
+        for (int u = 0; u < 4; ++u) {
+          const size_t p = (size_t)t * top_k + min(j0 + u, top_k - 1);
+          const int32_t r = pair_rows[p];
+          live[u] = j0 + u < top_k && in_range(r, R);
+          w[u] = weights != nullptr ? weights[p] : 1.0f;
+          z[u] = live[u] ? src[(size_t)r * sp.nv + v] : typename P::vec{};
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const typename P::fvec f = __builtin_convertvector(z[u], typename P::fvec);
+#pragma unroll
+          for (int c = 0; c < P::kN; ++c) sum[c] = live[u] ? __builtin_fmaf(w[u], f[c], sum[c]) : sum[c];
+        }
       }
       dst[v] = __builtin_convertvector(sum, typename P::vec);
     }
   }
 }
 
-// d_rows and d_w, one wave per token; the blocks from zero_block0 on clear the rows that hold no pair.
-template <typename E, int kBytes>
+// d_rows and d_w, kWaves waves per token (four for a batch too small to fill
+// the chip with one each), four pairs at a time beside one read of dy; the
+// blocks from zero_block0 on clear the rows that hold no pair.
+template <typename E, int kBytes, int kWaves>
 __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
     const E* __restrict__ dy, const E* __restrict__ rows, const int32_t* __restrict__ sorted_pairs,
     const int32_t* __restrict__ pair_rows, const float* __restrict__ weights, E* __restrict__ d_rows,
     float* __restrict__ d_weights, int64_t T, int64_t R, int top_k, int nv, int zero_block0) {
   using P = Piece<E, kBytes>;
+  constexpr int kTokens = kThreads / (64 * kWaves);  // of a block
+  __shared__ float part[4][4];                       // kWaves > 1: [wave][pair]
   const int lane = mx::lane_id();
   typename P::vec* out = reinterpret_cast<typename P::vec*>(d_rows);
   if ((int)blockIdx.x >= zero_block0) {
-    const int64_t step = (int64_t)(gridDim.x - zero_block0) * kThreads;
-    for (int64_t r0 = (int64_t)(blockIdx.x - zero_block0) * kThreads + (threadIdx.x - lane); r0 < R; r0 += step) {
-      const int64_t r = r0 + lane;
-      bool empty = false;
-      if (r < R) {
-        const int32_t p = sorted_pairs[r];
-        empty = !(in_range(p, T * top_k) && pair_rows[p] == (int32_t)r);
-      }
-      uint64_t todo = __ballot(empty);
-      while (todo != 0) {
-        const int b = __builtin_ctzll(todo);
-        todo &= todo - 1;
-        for (int v = lane; v < nv; v += 64) out[(size_t)(r0 + b) * nv + v] = typename P::vec{};
-      }
-    }
+    clear_empty_rows(out, (const typename P::vec*)nullptr, top_k, sorted_pairs, pair_rows, R, T * top_k, nv, blockIdx.x - zero_block0,
+                     gridDim.x - zero_block0);
     return;
   }
   const typename P::vec* z = reinterpret_cast<const typename P::vec*>(rows);
-  for (int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); t < T;
-       t += (int64_t)zero_block0 * (kThreads / 64)) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int64_t t = (int64_t)blockIdx.x * kTokens + wave / kWaves; t < T; t += (int64_t)zero_block0 * kTokens) {
     const typename P::vec* g = reinterpret_cast<const typename P::vec*>(dy) + (size_t)t * nv;
-    for (int j = 0; j < top_k; ++j) {
-      const size_t p = (size_t)t * top_k + j;
-      const int32_t r = pair_rows[p];
-      float dot = 0.f;
-      if (in_range(r, R)) {
-        const bool own = (size_t)sorted_pairs[r] == p;
-        const float w = weights[p];
-        for (int v = lane; v < nv; v += 64) {
-          const typename P::fvec gv = __builtin_convertvector(g[v], typename P::fvec);
-          const typename P::fvec zv = __builtin_convertvector(z[(size_t)r * nv + v], typename P::fvec);
+    for (int j0 = 0; j0 < top_k; j0 += 4) {
+      const typename P::vec* zr[4];
+      typename P::vec* dr[4];
+      float w[4], dot[4];
+      bool live[4], own[4];
 #pragma unroll
-          for (int c = 0; c < P::kN; ++c) dot = __builtin_fmaf(gv[c], zv[c], dot);
-          if (own) out[(size_t)r * nv + v] = __builtin_convertvector(gv * w, typename P::vec);
+      for (int u = 0; u < 4; ++u) {
+        const size_t p = (size_t)t * top_k + min(j0 + u, top_k - 1);
+        const int32_t r = pair_rows[p];
+        live[u] = j0 + u < top_k && in_range(r, R);
+        own[u] = live[u] && (size_t)sorted_pairs[r] == p;
+        w[u] = weights[p];
+        zr[u] = z + (size_t)(live[u] ? r : 0) * nv;
+        dr[u] = out + (size_t)(live[u] ? r : 0) * nv;
+        dot[u] = 0.f;
+      }
+      for (int v = (wave % kWaves) * 64 + lane; v < nv; v += 64 * kWaves) {
+        typename P::vec zv[4];
+        const typename P::fvec gv = __builtin_convertvector(g[v], typename P::fvec);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) zv[u] = live[u] ? zr[u][v] : typename P::vec{};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const typename P::fvec f = __builtin_convertvector(zv[u], typename P::fvec);
+          if (live[u]) {  // uniform
+#pragma unroll
+            for (int c = 0; c < P::kN; ++c) dot[u] = __builtin_fmaf(gv[c], f[c], dot[u]);
+          }
+          if (own[u]) dr[u][v] = __builtin_convertvector(gv * w[u], typename P::vec);
         }
       }
-      dot = mx::wave_sum_f32(dot);
-      if (lane == 0) d_weights[p] = dot;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) dot[u] = mx::wave_sum_f32(dot[u]);
+      if constexpr (kWaves == 1) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (lane == u && j0 + u < top_k) d_weights[t * top_k + j0 + u] = dot[u];
+      } else {
+        if (lane == 0) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) part[wave][u] = dot[u];
+        }
+        __syncthreads();
+        const int u = threadIdx.x;
+        if (u < 4 && j0 + u < top_k)
+          d_weights[t * top_k + j0 + u] = (part[0][u] + part[1][u]) + (part[2][u] + part[3][u]);
+        __syncthreads();
+      }
     }
   }
 }
 
-// kV logits per thread (4 where E allows), a block holding whole tokens.
+// A block takes kRouteTokens tokens: a thread per token forms the gradients of
+// its picks in LDS, then all threads write the rows, kV logits at a time (4
+// where E allows), each compared with its token's ids.  Bound by the bytes
+// written.
+constexpr int kRouteTokens = 32;
 template <int kV>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(const int32_t* __restrict__ ids,
                                                                   const float* __restrict__ weights,
                                                                   const float* __restrict__ d_weights,
                                                                   float* __restrict__ d_logits, int64_t T, int E,
-                                                                  int top_k, int per_token, int tokens_per_block) {
+                                                                  int top_k) {
   typedef float vec __attribute__((ext_vector_type(kV)));
-  const int lt = threadIdx.x / per_token;
-  if (lt >= tokens_per_block) return;
-  for (int64_t t = (int64_t)blockIdx.x * tokens_per_block + lt; t < T; t += (int64_t)gridDim.x * tokens_per_block) {
-    for (int part = threadIdx.x - lt * per_token; part * kV < E; part += per_token) {
-      const int32_t* id = ids + t * top_k;
-      const float* w = weights + t * top_k;
-      const float* dw = d_weights + t * top_k;
+  __shared__ int32_t id[kRouteTokens][MXFP4MOE_MAX_TOPK + 1];
+  __shared__ float grad[kRouteTokens][MXFP4MOE_MAX_TOPK + 1];
+  const int parts = E / kV, lanes = min(parts, kThreads);
+  const int lt = threadIdx.x / lanes, step = kThreads / lanes;  // this thread's first token, tokens at once
+  for (int64_t t0 = (int64_t)blockIdx.x * kRouteTokens; t0 < T; t0 += (int64_t)gridDim.x * kRouteTokens) {
+    const int n = (int)min((int64_t)kRouteTokens, T - t0);
+    if ((int)threadIdx.x < n) {
+      const size_t p0 = (size_t)(t0 + threadIdx.x) * top_k;
       float s = 0.f;
-      for (int j = 0; j < top_k; ++j) s = __builtin_fmaf(w[j], dw[j], s);
-      vec g = {};
+#pragma unroll 4
+      for (int j = 0; j < top_k; ++j) s = __builtin_fmaf(weights[p0 + j], d_weights[p0 + j], s);
+#pragma unroll 4
       for (int j = 0; j < top_k; ++j) {
-        const int at = id[j] - part * kV;
-#pragma unroll
-        for (int c = 0; c < kV; ++c) g[c] += at == c ? w[j] * (dw[j] - s) : 0.f;
+        id[threadIdx.x][j] = ids[p0 + j];
+        grad[threadIdx.x][j] = weights[p0 + j] * (d_weights[p0 + j] - s);
       }
-      *reinterpret_cast<vec*>(d_logits + t * E + part * kV) = g;
     }
+    __syncthreads();
+    if (lt < step) {
+      for (int t = lt; t < n; t += step)
+        for (int part = threadIdx.x - lt * lanes; part < parts; part += lanes) {
+          vec g = {};
+          for (int j = 0; j < top_k; ++j) {
+            const int at = id[t][j] - part * kV;
+#pragma unroll
+            for (int c = 0; c < kV; ++c) g[c] += at == c ? grad[t][j] : 0.f;
+          }
+          *reinterpret_cast<vec*>(d_logits + (t0 + t) * E + part * kV) = g;
+        }
+    }
+    __syncthreads();
   }
 }
 
@@ -224,10 +346,10 @@ int piece_bytes(size_t bytes, size_t element, const void* a, const void* b, cons
   return (int)element;
 }
 
+// One piece a lane while the groups can be counted in 31 bits.
 RowSplit row_split(int64_t rows, int64_t nv) {
   RowSplit s{(int)nv, 0, 1};
   while (s.lg < 6 && (1 << s.lg) < nv) ++s.lg;
-  // one piece per lane while the groups can be counted in 31 bits
   const int64_t segs = (nv + (1 << s.lg) - 1) >> s.lg;
   s.segs = rows * segs <= (int64_t)1 << 24 ? (int)segs : 1;
   return s;
@@ -243,16 +365,32 @@ unsigned block_count(int64_t work, int64_t per_block) {
 
 unsigned split_blocks(int64_t rows, const RowSplit& s) { return block_count(rows * s.segs, kThreads >> s.lg); }
 
+constexpr int64_t kByTokenBytes = 32 << 20;
+
 template <typename V>
-hipError_t permute(const void* x, const int32_t* sorted_pairs, int64_t nv, int64_t R, int64_t P, int top_k,
-                   void* rows, int32_t* pair_rows, hipStream_t stream) {
-  const RowSplit sp = row_split(R, nv);
-  const int chunks = P <= kInvertInBlocks ? (int)((P + kPairChunk - 1) / kPairChunk) : 0;
-  if (P > kInvertInBlocks)
+hipError_t permute(const void* x, const int32_t* sorted_pairs, int64_t nv, int64_t T, int64_t R, int top_k, void* rows,
+                   int32_t* pair_rows, hipStream_t stream) {
+  const int64_t P = T * top_k;
+  const bool in_blocks = P <= kInvertInBlocks;
+  const int chunks = in_blocks ? (int)((P + kPairChunk - 1) / kPairChunk) : 0;
+  if (in_blocks && R * nv * (int64_t)sizeof(V) < kByTokenBytes) {
+    const RowSplit sp = row_split(R, nv);
+    permute_kernel<V><<<chunks + split_blocks(R, sp), kThreads, 0, stream>>>(
+        static_cast<const V*>(x), sorted_pairs, static_cast<V*>(rows), pair_rows, R, P, top_k, sp, chunks);
+    return hipGetLastError();
+  }
+  if (in_blocks) {
+    if (chunks > 0) invert_kernel<<<chunks, 1024, 0, stream>>>(sorted_pairs, R, P, pair_rows);
+  } else {
     clear_pair_rows_kernel<<<block_count(P, kThreads), kThreads, 0, stream>>>(pair_rows, P);
-  if (chunks + R == 0) return hipGetLastError();
-  permute_kernel<V><<<chunks + split_blocks(R, sp), kThreads, 0, stream>>>(
-      static_cast<const V*>(x), sorted_pairs, static_cast<V*>(rows), pair_rows, R, P, top_k, sp, chunks);
+    if (R > 0)
+      enter_pair_rows_kernel<<<block_count(R, kThreads), kThreads, 0, stream>>>(sorted_pairs, R, P, pair_rows);
+  }
+  if (R == 0) return hipGetLastError();
+  const RowSplit sp = row_split(T, nv);
+  const unsigned token_blocks = split_blocks(T, sp);
+  permute_by_token_kernel<V><<<token_blocks + block_count(R, kZeroRows * kThreads / 64), kThreads, 0, stream>>>(
+      static_cast<const V*>(x), sorted_pairs, static_cast<V*>(rows), pair_rows, T, R, top_k, sp, (int)token_blocks);
   return hipGetLastError();
 }
 
@@ -265,15 +403,24 @@ hipError_t unpermute(const void* rows, const int32_t* pair_rows, const float* we
   return hipGetLastError();
 }
 
+constexpr int kManyTokens = 4096;
+
 template <typename E, int kBytes>
 hipError_t unpermute_backward(const void* dy, const void* rows, const int32_t* sorted_pairs,
                               const int32_t* pair_rows, const float* weights, int64_t T, int64_t H, int64_t R,
                               int top_k, void* d_rows, float* d_weights, hipStream_t stream) {
-  const int token_blocks = (int)block_count(T, kThreads / 64);
-  const int row_blocks = (int)block_count(R, kThreads);
-  unpermute_backward_kernel<E, kBytes><<<token_blocks + row_blocks, kThreads, 0, stream>>>(
-      static_cast<const E*>(dy), static_cast<const E*>(rows), sorted_pairs, pair_rows, weights,
-      static_cast<E*>(d_rows), d_weights, T, R, top_k, (int)(H * (int64_t)sizeof(E) / kBytes), token_blocks);
+  const int nv = (int)(H * (int64_t)sizeof(E) / kBytes), row_blocks = (int)block_count(R, kZeroRows * kThreads / 64);
+  if (T < kManyTokens && nv > 64) {
+    const int token_blocks = (int)block_count(T, 1);
+    unpermute_backward_kernel<E, kBytes, 4><<<token_blocks + row_blocks, kThreads, 0, stream>>>(
+        static_cast<const E*>(dy), static_cast<const E*>(rows), sorted_pairs, pair_rows, weights,
+        static_cast<E*>(d_rows), d_weights, T, R, top_k, nv, token_blocks);
+  } else {
+    const int token_blocks = (int)block_count(T, kThreads / 64);
+    unpermute_backward_kernel<E, kBytes, 1><<<token_blocks + row_blocks, kThreads, 0, stream>>>(
+        static_cast<const E*>(dy), static_cast<const E*>(rows), sorted_pairs, pair_rows, weights,
+        static_cast<E*>(d_rows), d_weights, T, R, top_k, nv, token_blocks);
+  }
   return hipGetLastError();
 }
 
@@ -290,9 +437,9 @@ hipError_t launch_permute(const void* x, int dtype, const int32_t* sorted_pairs,
   const size_t bytes = (size_t)H * element_bytes(dtype);
   ProfileScope prof(kStagePermute, stream);
   switch (piece_bytes(bytes, element_bytes(dtype), x, rows, nullptr)) {
-    case 16: return permute<mx::u32x4>(x, sorted_pairs, bytes / 16, R, P, (int)top_k, rows, pair_rows, stream);
-    case 4: return permute<uint32_t>(x, sorted_pairs, bytes / 4, R, P, (int)top_k, rows, pair_rows, stream);
-    default: return permute<uint16_t>(x, sorted_pairs, bytes / 2, R, P, (int)top_k, rows, pair_rows, stream);
+    case 16: return permute<mx::u32x4>(x, sorted_pairs, bytes / 16, T, R, (int)top_k, rows, pair_rows, stream);
+    case 4: return permute<uint32_t>(x, sorted_pairs, bytes / 4, T, R, (int)top_k, rows, pair_rows, stream);
+    default: return permute<uint16_t>(x, sorted_pairs, bytes / 2, T, R, (int)top_k, rows, pair_rows, stream);
   }
 }
 
@@ -336,17 +483,14 @@ hipError_t launch_route_backward(const int32_t* ids, const float* weights, const
                                  int64_t E, int64_t top_k, float* d_logits, hipStream_t stream) {
   if (T == 0) return hipSuccess;
   const bool four = E % 4 == 0 && aligned(d_logits, 16);
-  int per_token = (int)(four ? E / 4 : E);
-  per_token = per_token < kThreads ? per_token : kThreads;
-  const int tokens = kThreads / per_token;
-  const unsigned blocks = block_count(T, tokens);
+  const unsigned blocks = block_count(T, kRouteTokens);
   ProfileScope prof(kStageRouteBackward, stream);
   if (four)
     route_backward_kernel<4><<<blocks, kThreads, 0, stream>>>(ids, weights, d_weights, d_logits, T, (int)E,
-                                                              (int)top_k, per_token, tokens);
+                                                              (int)top_k);
   else
     route_backward_kernel<1><<<blocks, kThreads, 0, stream>>>(ids, weights, d_weights, d_logits, T, (int)E,
-                                                              (int)top_k, per_token, tokens);
+                                                              (int)top_k);
   return hipGetLastError();
 }
 

@@ -153,6 +153,24 @@ def test_pairs_past_those_that_blocks_invert(gpu, seed):
     assert rows.shape == (0, 3) and bool((pair_rows == -1).all())
 
 
+@pytest.mark.parametrize("T,H,k,dtype", [(4000, 2880, 2, "bf16"), (1500, 2881, 4, "f32"), (13000, 2047, 1, "f16"),
+                                         (70000, 512, 1, "bf16")])
+def test_large_batches_by_token(gpu, T, H, k, dtype):
+    """Rows of 32 MiB and more are written token by token; a pair listed twice among them."""
+    b = Batch(T, H, 8, k, dtype, local=6, pad=37, seed=T)
+    pairs = b.pairs_host.copy()
+    twice = np.flatnonzero((pairs >= 0) & (pairs < T * k))[[5, -3]]
+    pairs[twice[0]] = pairs[twice[1]]
+    d = torch.from_numpy(pairs.astype(np.int32)).cuda()
+    assert b.R * H * b.x.element_size() >= 32 << 20
+    rows, pair_rows = gpu.moe_permute(b.x, d, k, out=torch.full((b.R, H), 9.0, dtype=b.dtype, device="cuda"))
+    ok = (pairs >= 0) & (pairs < T * k)
+    want = torch.where(torch.from_numpy(ok).cuda()[:, None], b.x[torch.from_numpy(np.where(ok, pairs, 0) // k).cuda()],
+                       torch.zeros((), dtype=b.dtype, device="cuda"))
+    assert torch.equal(rows, want)
+    assert np.array_equal(pair_rows.cpu().numpy(), X.permute(np.zeros((T, 1)), pairs, k)[1])
+
+
 def test_infinite_rows_reach_their_tokens_only(gpu):
     b = Batch(9, 16, 4, 2, "bf16", seed=7)
     b.z[int(b.pair_rows_host[5])] = float("inf")
