@@ -365,8 +365,8 @@ int moe_nvfp4_forward(const uint16_t* x, const float* router_logits,
  *                value outside [0, R) counts as none).
  *   x, y, dx, dy [T, H];  rows, d_rows [R, H]: all of one element type,
  *                MXFP4MOE_BF16, MXFP4MOE_F16 or MXFP4MOE_F32, aligned to it
- *                (16-byte aligned rows move in 16-byte pieces, others in 4-byte
- *                pieces or single elements).  Outputs alias no input.
+ *                (rows of any H move in 16-byte pieces).  Outputs alias no
+ *                input.
  *   topk_weights, d_weights [T, top_k] float32.
  *   T, R >= 0, 1 <= H <= MXFP4MOE_MAX_ROW, 1 <= top_k <= MXFP4MOE_MAX_TOPK,
  *   T * top_k and R below 2^31.

@@ -28,17 +28,27 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Row pieces: kBytes of a row as one vector of elements.
-template <typename E, int kBytes>
+// Row pieces of kN elements (16 bytes, or one element for rows shorter than
+// that).  A row starts at any element: the loads and stores assume no more
+// alignment than an element's (the hardware takes 16 bytes at any address),
+// and the last piece of a row ends with it, repeating some of the elements of
+// the one before where kN does not divide H (both hold the same values).
+template <typename E, int kN>
 struct Piece {
-  static constexpr int kN = kBytes / (int)sizeof(E);
   typedef E vec __attribute__((ext_vector_type(kN)));
+  typedef vec loose __attribute__((aligned(sizeof(E))));
   typedef float fvec __attribute__((ext_vector_type(kN)));
+  static __device__ __forceinline__ int at(int v, int H) { return min(v * kN, H - kN); }
+  static __device__ __forceinline__ vec load(const E* p) { return *reinterpret_cast<const loose*>(p); }
+  static __device__ __forceinline__ void store(E* p, vec x) { *reinterpret_cast<loose*>(p) = x; }
+  static __device__ __forceinline__ void stream(E* p, vec x) {
+    __builtin_nontemporal_store(x, reinterpret_cast<loose*>(p));
+  }
 };
 
 // How lanes share a row: groups of 2^lg lanes (a power of two up to the
 // wave, so that short rows do not idle most of a wave), `segs` groups to a
-// row, each lane taking `per` pieces, 2^lg apart.
+// row, a piece to a lane where there are enough of them.
 struct RowSplit {
   int nv;    // pieces of a row
   int lg;    // log2 of the lanes of a group
@@ -90,12 +100,13 @@ __global__ __launch_bounds__(kThreads) void enter_pair_rows_kernel(const int32_t
 
 // Small batches, one launch: rows[i] = x[sorted_pairs[i] / top_k], a piece to
 // a lane; the blocks before copy_block0 write pair_rows meanwhile.
-template <typename V>
-__global__ __launch_bounds__(kThreads) void permute_kernel(const V* __restrict__ x,
+template <typename E, int kN>
+__global__ __launch_bounds__(kThreads) void permute_kernel(const E* __restrict__ x,
                                                            const int32_t* __restrict__ sorted_pairs,
-                                                           V* __restrict__ rows, int32_t* __restrict__ pair_rows,
-                                                           int64_t R, int64_t P, int top_k, RowSplit sp,
+                                                           E* __restrict__ rows, int32_t* __restrict__ pair_rows,
+                                                           int64_t R, int64_t P, int H, int top_k, RowSplit sp,
                                                            int copy_block0) {
+  using Pc = Piece<E, kN>;
   if ((int)blockIdx.x < copy_block0) {
     invert_chunk(sorted_pairs, R, P, blockIdx.x, pair_rows);
     return;
@@ -107,11 +118,13 @@ __global__ __launch_bounds__(kThreads) void permute_kernel(const V* __restrict__
     const unsigned i = (unsigned)g / (unsigned)sp.segs;
     const int32_t p = sorted_pairs[i];
     const bool live = in_range(p, P);
-    const V* src = x + (size_t)(live ? p / top_k : 0) * sp.nv;
-    V* dst = rows + (size_t)i * sp.nv;
+    const E* src = x + (size_t)(live ? p / top_k : 0) * H;
+    E* dst = rows + (size_t)i * H;
     for (int v = (int)((unsigned)g % (unsigned)sp.segs) * lanes + (threadIdx.x & (lanes - 1)); v < sp.nv;
-         v += lanes * sp.segs)
-      dst[v] = live ? src[v] : V{};
+         v += lanes * sp.segs) {
+      const int e = Pc::at(v, H);
+      Pc::store(dst + e, live ? Pc::load(src + e) : typename Pc::vec{});
+    }
   }
 }
 
@@ -119,10 +132,12 @@ __global__ __launch_bounds__(kThreads) void permute_kernel(const V* __restrict__
 // lie together behind a rank's share of the rows): block `block` of `blocks`.
 // With x, the earlier row of a pair listed twice gets its token's row instead.
 constexpr int kZeroRows = 4;
-template <typename V>
-__device__ __forceinline__ void clear_empty_rows(V* __restrict__ rows, const V* __restrict__ x, int top_k, const int32_t* __restrict__ sorted_pairs,
-                                                 const int32_t* __restrict__ pair_rows, int64_t R, int64_t P, int nv,
-                                                 int block, int blocks) {
+template <typename E, int kN>
+__device__ __forceinline__ void clear_empty_rows(E* __restrict__ rows, const E* __restrict__ x, int top_k,
+                                                 const int32_t* __restrict__ sorted_pairs,
+                                                 const int32_t* __restrict__ pair_rows, int64_t R, int64_t P, int H,
+                                                 int nv, int block, int blocks) {
+  using Pc = Piece<E, kN>;
   const int lane = mx::lane_id();
   const int64_t waves = (int64_t)blocks * (kThreads / 64);
   for (int64_t r0 = ((int64_t)block * (kThreads / 64) + (threadIdx.x >> 6)) * kZeroRows; r0 < R;
@@ -139,8 +154,11 @@ __device__ __forceinline__ void clear_empty_rows(V* __restrict__ rows, const V* 
       const int b = __builtin_ctzll(todo);
       todo &= todo - 1;
       const int32_t pb = __builtin_amdgcn_readlane(p, b);
-      const V* src = x != nullptr && in_range(pb, P) ? x + (size_t)(pb / top_k) * nv : nullptr;
-      for (int v = lane; v < nv; v += 64) rows[(size_t)(r0 + b) * nv + v] = src != nullptr ? src[v] : V{};
+      const E* src = x != nullptr && in_range(pb, P) ? x + (size_t)(pb / top_k) * H : nullptr;
+      for (int v = lane; v < nv; v += 64) {
+        const int e = Pc::at(v, H);
+        Pc::store(rows + (size_t)(r0 + b) * H + e, src != nullptr ? Pc::load(src + e) : typename Pc::vec{});
+      }
     }
   }
 }
@@ -148,52 +166,53 @@ __device__ __forceinline__ void clear_empty_rows(V* __restrict__ rows, const V* 
 // Large batches, with pair_rows written before: a token's pieces are read once
 // and stored to its top_k rows; the blocks from zero_block0 on clear the rows
 // that hold no pair.
-template <typename V>
-__global__ __launch_bounds__(kThreads) void permute_by_token_kernel(const V* __restrict__ x,
+template <typename E, int kN>
+__global__ __launch_bounds__(kThreads) void permute_by_token_kernel(const E* __restrict__ x,
                                                                     const int32_t* __restrict__ sorted_pairs,
-                                                                    V* __restrict__ rows,
+                                                                    E* __restrict__ rows,
                                                                     const int32_t* __restrict__ pair_rows, int64_t T,
-                                                                    int64_t R, int top_k, RowSplit sp,
+                                                                    int64_t R, int H, int top_k, RowSplit sp,
                                                                     int zero_block0) {
+  using Pc = Piece<E, kN>;
   if ((int)blockIdx.x >= zero_block0) {
-    clear_empty_rows(rows, x, top_k, sorted_pairs, pair_rows, R, T * top_k, sp.nv, blockIdx.x - zero_block0,
-                     gridDim.x - zero_block0);
+    clear_empty_rows<E, kN>(rows, x, top_k, sorted_pairs, pair_rows, R, T * top_k, H, sp.nv, blockIdx.x - zero_block0,
+                            gridDim.x - zero_block0);
     return;
   }
   const int lanes = 1 << sp.lg;
   for (int64_t g = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> sp.lg; g < T * sp.segs;
        g += ((int64_t)zero_block0 * kThreads) >> sp.lg) {
     const unsigned t = (unsigned)g / (unsigned)sp.segs;
-    const V* src = x + (size_t)t * sp.nv;
+    const E* src = x + (size_t)t * H;
     for (int v = (int)((unsigned)g % (unsigned)sp.segs) * lanes + (threadIdx.x & (lanes - 1)); v < sp.nv;
          v += lanes * sp.segs) {
-      const V piece = src[v];
+      const int e = Pc::at(v, H);
+      const typename Pc::vec piece = Pc::load(src + e);
       for (int j = 0; j < top_k; ++j) {
         const int32_t r = pair_rows[(size_t)t * top_k + j];
-        if (in_range(r, R)) __builtin_nontemporal_store(piece, rows + (size_t)r * sp.nv + v);
+        if (in_range(r, R)) Pc::stream(rows + (size_t)r * H + e, piece);
       }
     }
   }
 }
 
 // y[t] = sum_j w[t, j] rows[pair_rows[t, j]] (w == nullptr: 1), j ascending.
-template <typename E, int kBytes>
+template <typename E, int kN>
 __global__ __launch_bounds__(kThreads) void unpermute_kernel(const E* __restrict__ rows,
                                                              const int32_t* __restrict__ pair_rows,
                                                              const float* __restrict__ weights, E* __restrict__ y,
-                                                             int64_t T, int64_t R, int top_k, RowSplit sp) {
-  using P = Piece<E, kBytes>;
+                                                             int64_t T, int64_t R, int H, int top_k, RowSplit sp) {
+  using Pc = Piece<E, kN>;
   const int lanes = 1 << sp.lg;
-  const typename P::vec* src = reinterpret_cast<const typename P::vec*>(rows);
   for (int64_t g = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> sp.lg; g < T * sp.segs;
        g += ((int64_t)gridDim.x * kThreads) >> sp.lg) {
     const unsigned t = (unsigned)g / (unsigned)sp.segs;
-    typename P::vec* dst = reinterpret_cast<typename P::vec*>(y) + (size_t)t * sp.nv;
     for (int v = (int)((unsigned)g % (unsigned)sp.segs) * lanes + (threadIdx.x & (lanes - 1)); v < sp.nv;
          v += lanes * sp.segs) {
-      typename P::fvec sum = {};
+      const int e = Pc::at(v, H);
+      typename Pc::fvec sum = {};
       for (int j0 = 0; j0 < top_k; j0 += 4) {  // four pairs' pieces in flight
-        typename P::vec z[4];
+        typename Pc::vec z[4];
         float w[4];
         bool live[4];
 #pragma unroll
@@ -202,16 +221,16 @@ __global__ __launch_bounds__(kThreads) void unpermute_kernel(const E* __restrict
           const int32_t r = pair_rows[p];
           live[u] = j0 + u < top_k && in_range(r, R);
           w[u] = weights != nullptr ? weights[p] : 1.0f;
-          z[u] = live[u] ? src[(size_t)r * sp.nv + v] : typename P::vec{};
+          z[u] = live[u] ? Pc::load(rows + (size_t)r * H + e) : typename Pc::vec{};
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const typename P::fvec f = __builtin_convertvector(z[u], typename P::fvec);
+          const typename Pc::fvec f = __builtin_convertvector(z[u], typename Pc::fvec);
 #pragma unroll
-          for (int c = 0; c < P::kN; ++c) sum[c] = live[u] ? __builtin_fmaf(w[u], f[c], sum[c]) : sum[c];
+          for (int c = 0; c < kN; ++c) sum[c] = live[u] ? __builtin_fmaf(w[u], f[c], sum[c]) : sum[c];
         }
       }
-      dst[v] = __builtin_convertvector(sum, typename P::vec);
+      Pc::store(y + (size_t)t * H + e, __builtin_convertvector(sum, typename Pc::vec));
     }
   }
 }
@@ -219,28 +238,25 @@ __global__ __launch_bounds__(kThreads) void unpermute_kernel(const E* __restrict
 // d_rows and d_w, kWaves waves per token (four for a batch too small to fill
 // the chip with one each), four pairs at a time beside one read of dy; the
 // blocks from zero_block0 on clear the rows that hold no pair.
-template <typename E, int kBytes, int kWaves>
+template <typename E, int kN, int kWaves>
 __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
     const E* __restrict__ dy, const E* __restrict__ rows, const int32_t* __restrict__ sorted_pairs,
     const int32_t* __restrict__ pair_rows, const float* __restrict__ weights, E* __restrict__ d_rows,
-    float* __restrict__ d_weights, int64_t T, int64_t R, int top_k, int nv, int zero_block0) {
-  using P = Piece<E, kBytes>;
+    float* __restrict__ d_weights, int64_t T, int64_t R, int H, int top_k, int nv, int zero_block0) {
+  using Pc = Piece<E, kN>;
   constexpr int kTokens = kThreads / (64 * kWaves);  // of a block
   __shared__ float part[4][4];                       // kWaves > 1: [wave][pair]
   const int lane = mx::lane_id();
-  typename P::vec* out = reinterpret_cast<typename P::vec*>(d_rows);
   if ((int)blockIdx.x >= zero_block0) {
-    clear_empty_rows(out, (const typename P::vec*)nullptr, top_k, sorted_pairs, pair_rows, R, T * top_k, nv, blockIdx.x - zero_block0,
-                     gridDim.x - zero_block0);
+    clear_empty_rows<E, kN>(d_rows, nullptr, top_k, sorted_pairs, pair_rows, R, T * top_k, H, nv,
+                            blockIdx.x - zero_block0, gridDim.x - zero_block0);
     return;
   }
-  const typename P::vec* z = reinterpret_cast<const typename P::vec*>(rows);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int64_t t = (int64_t)blockIdx.x * kTokens + wave / kWaves; t < T; t += (int64_t)zero_block0 * kTokens) {
-    const typename P::vec* g = reinterpret_cast<const typename P::vec*>(dy) + (size_t)t * nv;
+    const E* g = dy + (size_t)t * H;
     for (int j0 = 0; j0 < top_k; j0 += 4) {
-      const typename P::vec* zr[4];
-      typename P::vec* dr[4];
+      size_t at[4];
       float w[4], dot[4];
       bool live[4], own[4];
 #pragma unroll
@@ -250,23 +266,33 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
         live[u] = j0 + u < top_k && in_range(r, R);
         own[u] = live[u] && (size_t)sorted_pairs[r] == p;
         w[u] = weights[p];
-        zr[u] = z + (size_t)(live[u] ? r : 0) * nv;
-        dr[u] = out + (size_t)(live[u] ? r : 0) * nv;
+        at[u] = (size_t)(live[u] ? r : 0) * H;
         dot[u] = 0.f;
       }
       for (int v = (wave % kWaves) * 64 + lane; v < nv; v += 64 * kWaves) {
-        typename P::vec zv[4];
-        const typename P::fvec gv = __builtin_convertvector(g[v], typename P::fvec);
+        const int e = Pc::at(v, H), again = v * kN - e;  // `again`: elements that the piece before this one has too
+        typename Pc::vec zv[4];
+        const typename Pc::fvec gv = __builtin_convertvector(Pc::load(g + e), typename Pc::fvec);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) zv[u] = live[u] ? zr[u][v] : typename P::vec{};
+        for (int u = 0; u < 4; ++u) zv[u] = live[u] ? Pc::load(rows + at[u] + e) : typename Pc::vec{};
+        typename Pc::fvec gd = gv;
+        if (again > 0) {
+#pragma unroll
+          for (int c = 0; c < kN; ++c)
+            if (c < again) {
+              gd[c] = 0.f;
+#pragma unroll
+              for (int u = 0; u < 4; ++u) zv[u][c] = (E)0.f;
+            }
+        }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const typename P::fvec f = __builtin_convertvector(zv[u], typename P::fvec);
+          const typename Pc::fvec f = __builtin_convertvector(zv[u], typename Pc::fvec);
           if (live[u]) {  // uniform
 #pragma unroll
-            for (int c = 0; c < P::kN; ++c) dot[u] = __builtin_fmaf(gv[c], f[c], dot[u]);
+            for (int c = 0; c < kN; ++c) dot[u] = __builtin_fmaf(gd[c], f[c], dot[u]);
           }
-          if (own[u]) dr[u][v] = __builtin_convertvector(gv * w[u], typename P::vec);
+          if (own[u]) Pc::store(d_rows + at[u] + e, __builtin_convertvector(gv * w[u], typename Pc::vec));
         }
       }
 #pragma unroll
@@ -338,14 +364,6 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const int32_t*
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// The widest piece that divides a row of `bytes` and the alignment of every
-// tensor: 16 or 4 bytes, or one element.
-int piece_bytes(size_t bytes, size_t element, const void* a, const void* b, const void* c) {
-  for (size_t v : {(size_t)16, (size_t)4})
-    if (v >= element && bytes % v == 0 && aligned(a, v) && aligned(b, v) && aligned(c, v)) return (int)v;
-  return (int)element;
-}
-
 // One piece a lane while the groups can be counted in 31 bits.
 RowSplit row_split(int64_t rows, int64_t nv) {
   RowSplit s{(int)nv, 0, 1};
@@ -367,16 +385,16 @@ unsigned split_blocks(int64_t rows, const RowSplit& s) { return block_count(rows
 
 constexpr int64_t kByTokenBytes = 32 << 20;
 
-template <typename V>
-hipError_t permute(const void* x, const int32_t* sorted_pairs, int64_t nv, int64_t T, int64_t R, int top_k, void* rows,
+template <typename E, int kN>
+hipError_t permute(const void* x, const int32_t* sorted_pairs, int64_t T, int64_t H, int64_t R, int top_k, void* rows,
                    int32_t* pair_rows, hipStream_t stream) {
-  const int64_t P = T * top_k;
+  const int64_t P = T * top_k, nv = (H + kN - 1) / kN;
   const bool in_blocks = P <= kInvertInBlocks;
   const int chunks = in_blocks ? (int)((P + kPairChunk - 1) / kPairChunk) : 0;
-  if (in_blocks && R * nv * (int64_t)sizeof(V) < kByTokenBytes) {
+  if (in_blocks && R * H * (int64_t)sizeof(E) < kByTokenBytes) {
     const RowSplit sp = row_split(R, nv);
-    permute_kernel<V><<<chunks + split_blocks(R, sp), kThreads, 0, stream>>>(
-        static_cast<const V*>(x), sorted_pairs, static_cast<V*>(rows), pair_rows, R, P, top_k, sp, chunks);
+    permute_kernel<E, kN><<<chunks + split_blocks(R, sp), kThreads, 0, stream>>>(
+        static_cast<const E*>(x), sorted_pairs, static_cast<E*>(rows), pair_rows, R, P, (int)H, top_k, sp, chunks);
     return hipGetLastError();
   }
   if (in_blocks) {
@@ -389,38 +407,34 @@ hipError_t permute(const void* x, const int32_t* sorted_pairs, int64_t nv, int64
   if (R == 0) return hipGetLastError();
   const RowSplit sp = row_split(T, nv);
   const unsigned token_blocks = split_blocks(T, sp);
-  permute_by_token_kernel<V><<<token_blocks + block_count(R, kZeroRows * kThreads / 64), kThreads, 0, stream>>>(
-      static_cast<const V*>(x), sorted_pairs, static_cast<V*>(rows), pair_rows, T, R, top_k, sp, (int)token_blocks);
+  permute_by_token_kernel<E, kN><<<token_blocks + block_count(R, kZeroRows * kThreads / 64), kThreads, 0, stream>>>(
+      static_cast<const E*>(x), sorted_pairs, static_cast<E*>(rows), pair_rows, T, R, (int)H, top_k, sp,
+      (int)token_blocks);
   return hipGetLastError();
 }
 
-template <typename E, int kBytes>
+template <typename E, int kN>
 hipError_t unpermute(const void* rows, const int32_t* pair_rows, const float* weights, int64_t T, int64_t H,
                      int64_t R, int top_k, void* y, hipStream_t stream) {
-  const RowSplit sp = row_split(T, H * (int64_t)sizeof(E) / kBytes);
-  unpermute_kernel<E, kBytes><<<split_blocks(T, sp), kThreads, 0, stream>>>(
-      static_cast<const E*>(rows), pair_rows, weights, static_cast<E*>(y), T, R, top_k, sp);
+  const RowSplit sp = row_split(T, (H + kN - 1) / kN);
+  unpermute_kernel<E, kN><<<split_blocks(T, sp), kThreads, 0, stream>>>(
+      static_cast<const E*>(rows), pair_rows, weights, static_cast<E*>(y), T, R, (int)H, top_k, sp);
   return hipGetLastError();
 }
 
 constexpr int kManyTokens = 4096;
 
-template <typename E, int kBytes>
+template <typename E, int kN>
 hipError_t unpermute_backward(const void* dy, const void* rows, const int32_t* sorted_pairs,
                               const int32_t* pair_rows, const float* weights, int64_t T, int64_t H, int64_t R,
                               int top_k, void* d_rows, float* d_weights, hipStream_t stream) {
-  const int nv = (int)(H * (int64_t)sizeof(E) / kBytes), row_blocks = (int)block_count(R, kZeroRows * kThreads / 64);
-  if (T < kManyTokens && nv > 64) {
-    const int token_blocks = (int)block_count(T, 1);
-    unpermute_backward_kernel<E, kBytes, 4><<<token_blocks + row_blocks, kThreads, 0, stream>>>(
-        static_cast<const E*>(dy), static_cast<const E*>(rows), sorted_pairs, pair_rows, weights,
-        static_cast<E*>(d_rows), d_weights, T, R, top_k, nv, token_blocks);
-  } else {
-    const int token_blocks = (int)block_count(T, kThreads / 64);
-    unpermute_backward_kernel<E, kBytes, 1><<<token_blocks + row_blocks, kThreads, 0, stream>>>(
-        static_cast<const E*>(dy), static_cast<const E*>(rows), sorted_pairs, pair_rows, weights,
-        static_cast<E*>(d_rows), d_weights, T, R, top_k, nv, token_blocks);
-  }
+  const int nv = (int)((H + kN - 1) / kN), row_blocks = (int)block_count(R, kZeroRows * kThreads / 64);
+  const bool split = T < kManyTokens && nv > 64;
+  const int token_blocks = (int)block_count(T, split ? 1 : kThreads / 64);
+  const auto kernel = split ? unpermute_backward_kernel<E, kN, 4> : unpermute_backward_kernel<E, kN, 1>;
+  kernel<<<token_blocks + row_blocks, kThreads, 0, stream>>>(
+      static_cast<const E*>(dy), static_cast<const E*>(rows), sorted_pairs, pair_rows, weights,
+      static_cast<E*>(d_rows), d_weights, T, R, (int)H, top_k, nv, token_blocks);
   return hipGetLastError();
 }
 
@@ -430,54 +444,40 @@ namespace mxfp4moe {
 
 size_t element_bytes(int dtype) { return dtype == kF32 ? 4 : 2; }
 
+// The call on 16-byte pieces, or on single elements for shorter rows.
+#define MX_BY_PIECE(FN, E, ...) (H * (int64_t)sizeof(E) >= 16 ? FN<E, 16 / (int)sizeof(E)>(__VA_ARGS__) : FN<E, 1>(__VA_ARGS__))
+#define MX_BY_TYPE(FN, ...)                               \
+  (dtype == kF32   ? MX_BY_PIECE(FN, float, __VA_ARGS__)    \
+   : dtype == kF16 ? MX_BY_PIECE(FN, _Float16, __VA_ARGS__) \
+                   : MX_BY_PIECE(FN, __bf16, __VA_ARGS__))
+
 hipError_t launch_permute(const void* x, int dtype, const int32_t* sorted_pairs, int64_t T, int64_t H, int64_t top_k,
                           int64_t R, void* rows, int32_t* pair_rows, hipStream_t stream) {
-  const int64_t P = T * top_k;
-  if (R == 0 && P == 0) return hipSuccess;
-  const size_t bytes = (size_t)H * element_bytes(dtype);
+  if (R == 0 && T == 0) return hipSuccess;
+  const int k = (int)top_k;
   ProfileScope prof(kStagePermute, stream);
-  switch (piece_bytes(bytes, element_bytes(dtype), x, rows, nullptr)) {
-    case 16: return permute<mx::u32x4>(x, sorted_pairs, bytes / 16, T, R, (int)top_k, rows, pair_rows, stream);
-    case 4: return permute<uint32_t>(x, sorted_pairs, bytes / 4, T, R, (int)top_k, rows, pair_rows, stream);
-    default: return permute<uint16_t>(x, sorted_pairs, bytes / 2, T, R, (int)top_k, rows, pair_rows, stream);
-  }
+  return dtype == kF32 ? MX_BY_PIECE(permute, uint32_t, x, sorted_pairs, T, H, R, k, rows, pair_rows, stream)
+                       : MX_BY_PIECE(permute, uint16_t, x, sorted_pairs, T, H, R, k, rows, pair_rows, stream);
 }
 
 hipError_t launch_unpermute(const void* rows, int dtype, const int32_t* pair_rows, const float* weights, int64_t T,
                             int64_t H, int64_t top_k, int64_t R, void* y, hipStream_t stream) {
   if (T == 0) return hipSuccess;
-  const size_t el = element_bytes(dtype);
-  const int piece = piece_bytes((size_t)H * el, el, rows, y, nullptr);
-  const int k = (int)top_k;
   ProfileScope prof(kStageUnpermute, stream);
-  if (dtype == kF32)
-    return piece == 16 ? unpermute<float, 16>(rows, pair_rows, weights, T, H, R, k, y, stream)
-                       : unpermute<float, 4>(rows, pair_rows, weights, T, H, R, k, y, stream);
-  if (dtype == kF16)
-    return piece == 16  ? unpermute<_Float16, 16>(rows, pair_rows, weights, T, H, R, k, y, stream)
-           : piece == 4 ? unpermute<_Float16, 4>(rows, pair_rows, weights, T, H, R, k, y, stream)
-                        : unpermute<_Float16, 2>(rows, pair_rows, weights, T, H, R, k, y, stream);
-  return piece == 16  ? unpermute<__bf16, 16>(rows, pair_rows, weights, T, H, R, k, y, stream)
-         : piece == 4 ? unpermute<__bf16, 4>(rows, pair_rows, weights, T, H, R, k, y, stream)
-                      : unpermute<__bf16, 2>(rows, pair_rows, weights, T, H, R, k, y, stream);
+  return MX_BY_TYPE(unpermute, rows, pair_rows, weights, T, H, R, (int)top_k, y, stream);
 }
 
 hipError_t launch_unpermute_backward(const void* dy, const void* rows, int dtype, const int32_t* sorted_pairs,
                                      const int32_t* pair_rows, const float* weights, int64_t T, int64_t H,
                                      int64_t top_k, int64_t R, void* d_rows, float* d_weights, hipStream_t stream) {
   if (T == 0 && R == 0) return hipSuccess;
-  const size_t el = element_bytes(dtype);
-  const int piece = piece_bytes((size_t)H * el, el, dy, rows, d_rows);
-  const int k = (int)top_k;
   ProfileScope prof(kStageUnpermuteBackward, stream);
-#define MX_BACKWARD(E, B) \
-  unpermute_backward<E, B>(dy, rows, sorted_pairs, pair_rows, weights, T, H, R, k, d_rows, d_weights, stream)
-  if (dtype == kF32) return piece == 16 ? MX_BACKWARD(float, 16) : MX_BACKWARD(float, 4);
-  if (dtype == kF16)
-    return piece == 16 ? MX_BACKWARD(_Float16, 16) : piece == 4 ? MX_BACKWARD(_Float16, 4) : MX_BACKWARD(_Float16, 2);
-  return piece == 16 ? MX_BACKWARD(__bf16, 16) : piece == 4 ? MX_BACKWARD(__bf16, 4) : MX_BACKWARD(__bf16, 2);
-#undef MX_BACKWARD
+  return MX_BY_TYPE(unpermute_backward, dy, rows, sorted_pairs, pair_rows, weights, T, H, R, (int)top_k, d_rows,
+                    d_weights, stream);
 }
+
+#undef MX_BY_TYPE
+#undef MX_BY_PIECE
 
 hipError_t launch_route_backward(const int32_t* ids, const float* weights, const float* d_weights, int64_t T,
                                  int64_t E, int64_t top_k, float* d_logits, hipStream_t stream) {

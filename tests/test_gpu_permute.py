@@ -178,6 +178,19 @@ def test_infinite_rows_reach_their_tokens_only(gpu):
     assert bool(torch.isinf(y[2]).all()) and bool(torch.isfinite(y[torch.arange(9) != 2]).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinite_element_is_counted_once(gpu, dtype):
+    """An infinity among the elements that the last two pieces of a row share (H no multiple of a
+    piece): its dot product with positive values is infinite, not NaN."""
+    H = 13 if dtype == "bf16" else 7
+    b = Batch(6, H, 4, 2, dtype, seed=9)
+    b.dy.copy_(b.dy.abs() + 0.1)
+    b.z[int(b.pair_rows_host[3]), H - 6 if dtype == "f32" else 6] = float("inf")
+    d_rows, d_w = gpu.moe_unpermute_backward(b.dy, b.z, b.pairs, b.pair_rows, b.w)
+    want = f64(b.dy)[:, None] * f64(b.z)[b.pair_rows_host].reshape(6, 2, H)
+    assert bool(torch.isposinf(d_w[1, 1])) and np.array_equal(np.isfinite(f64(d_w)), np.isfinite(want.sum(2)))
+
+
 def test_out_of_range_rows_are_no_rows(gpu):
     b = Batch(9, 16, 4, 2, "f32", seed=8)
     host = b.pair_rows_host.copy()
