@@ -153,6 +153,24 @@ __device__ __forceinline__ bool map_tile(const LinearArgs& a, int tm, int chunks
 // and for a single small matrix the latency of one pass.
 constexpr int kFewRows = 16;
 
+// Four consecutive outputs: s2 * v + bias, `n` of them in range (`whole`: always four, 8-byte aligned).
+__device__ __forceinline__ void store4(uint16_t* out, f32x4 v, float s2, const uint16_t* bias, int n, bool whole) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    v[c] *= s2;
+    if (bias != nullptr && c < n) v[c] += mx::bf16_to_f32(bias[c]);
+  }
+  const uint2 packed = mxgemm::pack_bf16x4(v);
+  if (whole) {
+    *reinterpret_cast<uint2*>(out) = packed;
+    return;
+  }
+  const uint32_t d[2] = {packed.x, packed.y};
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (c < n) out[c] = (uint16_t)(d[c >> 1] >> (16 * (c & 1)));
+}
+
 template <bool kNv, int kC, int kG>
 __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs a) {
   extern __shared__ f32x4 red[];
@@ -216,19 +234,140 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs a) {
     if (lr >= t.rows || n >= N) continue;
     uint16_t* out = a.y + (size_t)(t.row0 + lr) * N + n;
     const uint16_t* bias = a.bias != nullptr ? a.bias + (size_t)t.e * N + n : nullptr;
+    store4(out, v, s2, bias, min(4, N - n), (N & 3) == 0);
+  }
+}
+
+// y for row tiles of at most 4 rows (decode: one token, or a few over many
+// experts), where the weights' bytes and the latency of a pass are all there
+// is.  4x4x4 MFMA, sixteen independent 4 x 4 products at once: lane (b, i) is
+// weight row i of four and group 16u + b of unit u (512 k: a wave reads 256
+// contiguous bytes of each row at a time), and row i of x for the same k, so
+// that x takes a quarter of the registers that 16 columns would.  x of a
+// wave's kU units stays in registers while it streams the weights of its row
+// groups (four weight rows each), the next group's loads in flight behind the
+// current one's products.  The sixteen blocks' sums are added across lanes;
+// lane block b keeps row group b of up to sixteen, which leave together.  A
+// block's waves split K where it exceeds one wave's units and add their sums
+// through LDS in wave order.  Row groups are dealt to the blocks in equal
+// contiguous ranges.
+constexpr int kOneRows = 4;
+constexpr int kBatch = 16;  // row groups that leave together
+
+template <bool kNv, int kU>
+__global__ __launch_bounds__(512) void linear_one_kernel(LinearArgs a) {
+  typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
+  extern __shared__ f32x4 red[];  // [waves][64], only with more than one wave
+  const int K = a.K, N = a.N, kgroups = K >> 5;
+  const int lane = mx::lane_id(), b = lane >> 2, i4 = lane & 3;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int kscales = kNv ? K >> 4 : kgroups;
+  const int groups = (N + 3) >> 2;  // of a tile
+  const int64_t total = (int64_t)count_tiles(a, kOneRows) * groups;
+  int64_t job = total * blockIdx.x / gridDim.x;
+  const int64_t last = total * (blockIdx.x + 1) / gridDim.x;
+
+  while (job < last) {  // uniform: the jobs of one tile at a time
+    const int ti = (int)(job / groups);
+    Tile t;
+    if (!find_tile(a, kOneRows, ti, t)) return;  // uniform, not reached: job < total
+    const int g0 = (int)(job - (int64_t)ti * groups), g1 = (int)min((int64_t)groups, g0 + (last - job));
+    job += g1 - g0;
+    const auto rx = buffer(a.x + (size_t)t.row0 * K, (uint32_t)t.rows * K * 2);
+    const size_t row0 = (size_t)t.e * N + 4 * (size_t)g0;
+    const uint32_t nrows = min(4 * g1, N) - 4 * g0;
+    const auto rw = buffer(a.blocks + row0 * (K >> 1), nrows * (K >> 1));
+    const auto rs = buffer(a.scales + row0 * kscales, nrows * kscales);
+
+    u32x4 x[kU][4];
+    uint32_t woff[kU], soff[kU];
+    bool dead[kU];  // groups past K: zero x and zero weights
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      v[c] *= s2;
-      if (bias != nullptr && n + c < N) v[c] += mx::bf16_to_f32(bias[c]);
+    for (int u = 0; u < kU; ++u) {
+      const int g = 16 * (wave * kU + u) + b;
+      dead[u] = g >= kgroups;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        x[u][s] = __builtin_amdgcn_raw_buffer_load_b128(rx, dead[u] ? kDead : (uint32_t)i4 * K * 2 + g * 64 + 16 * s, 0, 0);
+      woff[u] = (uint32_t)i4 * (K >> 1) + g * 16;
+      soff[u] = (uint32_t)i4 * kscales + g * (kNv ? 2 : 1);
     }
-    const uint2 packed = mxgemm::pack_bf16x4(v);
-    if ((N & 3) == 0) {
-      *reinterpret_cast<uint2*>(out) = packed;
-    } else {
-      const uint32_t d[2] = {packed.x, packed.y};
+    const float s2 = kNv ? a.scale2[t.e] : 1.0f;
+
+    struct Group {
+      u32x4 w[kU];
+      uint32_t sc[kU];
+    };
+    auto load = [&](Group& r, int g) {  // past the last group: zeros
+      const uint32_t wrow = (uint32_t)(4 * (g - g0)) * (K >> 1), srow = (uint32_t)(4 * (g - g0)) * kscales;
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (n + c < N) out[c] = (uint16_t)(d[c >> 1] >> (16 * (c & 1)));
+      for (int u = 0; u < kU; ++u) {
+        r.w[u] = __builtin_amdgcn_raw_buffer_load_b128(rw, dead[u] ? kDead : woff[u] + wrow, 0, 0);
+        const uint32_t so = dead[u] ? kDead : soff[u] + srow;
+        r.sc[u] = kNv ? __builtin_amdgcn_raw_buffer_load_b16(rs, so, 0, 0) : __builtin_amdgcn_raw_buffer_load_b8(rs, so, 0, 0);
+      }
+    };
+    f32x4 kept = {};
+    auto multiply = [&](const Group& r, int g) {
+      f32x4 acc[2] = {};
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const GroupScale<kNv> gs(r.sc[u] & 255u, r.sc[u] >> 8);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const u32x4 wv = gs.convert(r.w[u][s], s);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint2 av{wv[2 * h], wv[2 * h + 1]}, bv{x[u][s][2 * h], x[u][s][2 * h + 1]};
+            acc[h] = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4, av), __builtin_bit_cast(s16x4, bv),
+                                                            acc[h], 0, 0, 0);
+          }
+        }
+      }
+      // lane (b, j): weight rows 0..3 of x row j over block b's k; add the blocks
+      f32x4 v = acc[0] + acc[1];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float f = v[c];
+        f += __int_as_float(mx::dpp_i32<mx::kDppRowRor4>(__float_as_int(f)));
+        f += __int_as_float(mx::dpp_i32<mx::kDppRowRor8>(__float_as_int(f)));
+        const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(f), __float_as_uint(f), false, false);
+        f = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+        const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(f), __float_as_uint(f), false, false);
+        f = __uint_as_float(q[0]) + __uint_as_float(q[1]);
+        if (b == ((g - g0) & (kBatch - 1))) kept[c] = f;
+      }
+    };
+    auto leave = [&](int gb, int ge) {  // row groups gb .. ge - 1, at most kBatch
+      f32x4 v = kept;
+      if (waves > 1) {  // uniform
+        red[wave * 64 + lane] = v;
+        __syncthreads();
+        v = red[lane];
+        for (int u = 1; u < waves; ++u) v += red[u * 64 + lane];
+        __syncthreads();
+        if (wave > 0) return;
+      }
+      const int n = 4 * (gb + b);
+      if (gb + b >= ge || i4 >= t.rows) return;
+      uint16_t* out = a.y + (size_t)(t.row0 + i4) * N + n;
+      const uint16_t* bias = a.bias != nullptr ? a.bias + (size_t)t.e * N + n : nullptr;
+      store4(out, v, s2, bias, min(4, N - n), (N & 3) == 0);
+    };
+
+    Group r0, r1;
+    load(r0, g0);
+    for (int gb = g0; gb < g1; gb += kBatch) {
+      const int ge = min(gb + kBatch, g1);
+      for (int g = gb; g < ge; g += 2) {
+        load(r1, g + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(r0, g);
+        load(r0, g + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        if (g + 1 < ge) multiply(r1, g + 1);  // uniform
+      }
+      leave(gb, ge);
     }
   }
 }
@@ -855,6 +994,29 @@ hipError_t launch_few(LinearArgs a, int waves, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Rows of an expert on average up to which tiles of 4 rows are taken.
+constexpr int kOneMeanRows = 1;
+constexpr int kOneWaves = 8;  // of a CU: what the registers hold (two for each SIMD)
+
+template <bool kNv>
+hipError_t launch_one(LinearArgs a, int units, hipStream_t stream) {
+  a.max_tiles = max_tiles(a, kOneRows);
+  const int waves = (units + 5) / 6, u = (units + waves - 1) / waves;
+  const int64_t jobs = (int64_t)a.max_tiles * ((a.N + 3) / 4);
+  const int64_t most = (int64_t)mxfp4moe::device_cu_count() * (kOneWaves / waves);
+  const unsigned grid = (unsigned)(jobs < most ? jobs : most);
+  const size_t lds = waves > 1 ? (size_t)waves * 64 * sizeof(f32x4) : 0;
+  switch (u) {
+    case 1: linear_one_kernel<kNv, 1><<<grid, waves * 64, lds, stream>>>(a); break;
+    case 2: linear_one_kernel<kNv, 2><<<grid, waves * 64, lds, stream>>>(a); break;
+    case 3: linear_one_kernel<kNv, 3><<<grid, waves * 64, lds, stream>>>(a); break;
+    case 4: linear_one_kernel<kNv, 4><<<grid, waves * 64, lds, stream>>>(a); break;
+    case 5: linear_one_kernel<kNv, 5><<<grid, waves * 64, lds, stream>>>(a); break;
+    default: linear_one_kernel<kNv, 6><<<grid, waves * 64, lds, stream>>>(a); break;
+  }
+  return hipGetLastError();
+}
+
 template <bool kNv>
 hipError_t linear(LinearArgs a, hipStream_t stream) {
   const int64_t n_tiles = (a.N + kTileN - 1) / kTileN, rows = (int64_t)a.R / a.E;
@@ -863,6 +1025,8 @@ hipError_t linear(LinearArgs a, hipStream_t stream) {
     linear_tile_kernel<kNv><<<grid_of(a.max_tiles, n_tiles), 256, 0, stream>>>(a);
     return hipGetLastError();
   }
+  const int units = (a.K + 511) / 512;
+  if (a.R <= (a.offsets == nullptr ? kOneRows : kOneMeanRows * a.E) && units <= 6 * 8) return launch_one<kNv>(a, units, stream);
   a.max_tiles = max_tiles(a, kFewRows);
   const int chunks = (a.K + 127) / 128;
   const int waves = chunks <= 24 ? 4 : 8;

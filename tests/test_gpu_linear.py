@@ -97,6 +97,8 @@ def check_both(gpu, w, R, offsets=None, bias=True, seed=1, label=""):
 
 
 DENSE = [  # R, N, K
+    (1, 4, 512), (1, 3, 544), (2, 66, 3104), (4, 131, 2592), (3, 1030, 7 * 512 + 96), (4, 65, 30 * 512 + 64),
+    (1, 50000, 96), (4, 9, 49 * 512),
     (1, 1, 32), (1, 2880, 2880), (1, 64, 4096), (2, 33, 64), (3, 17, 96), (16, 100, 160), (17, 130, 736),
     (40, 257, 288), (64, 256, 512), (100, 1000, 736), (129, 203, 608), (200, 513, 320), (300, 96, 2880),
     (257, 5, 32), (5, 7, 9 * 128 * 8), (130, 640, 1088),
@@ -110,6 +112,9 @@ def test_dense(gpu, fmt, R, N, K):
 
 
 GROUPED = [  # rows of every expert, N, K
+    ([1, 0, 4, 0, 0, 3, 0, 0, 2], 2880, 2880),
+    ([0, 9, 0, 0, 0, 0, 0, 0, 0, 0, 1, 0], 67, 1184),
+    ([0] * 200 + [5] + [0] * 50, 130, 4096),
     ([1], 32, 32),
     ([0, 0, 0], 32, 32),
     ([4, 0, 1, 0, 0, 11], 96, 128),
