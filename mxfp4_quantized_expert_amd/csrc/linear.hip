@@ -238,12 +238,13 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs a) {
   }
 }
 
-// y for row tiles of at most 4 rows (decode: one token, or a few over many
+// y for row tiles of at most 4 kT rows (decode: one token, or a few over many
 // experts), where the weights' bytes and the latency of a pass are all there
 // is.  4x4x4 MFMA, sixteen independent 4 x 4 products at once: lane (b, i) is
 // weight row i of four and group 16u + b of unit u (512 k: a wave reads 256
-// contiguous bytes of each row at a time), and row i of x for the same k, so
-// that x takes a quarter of the registers that 16 columns would.  x of a
+// contiguous bytes of each row at a time), and row i of x (of each of kT
+// times four) for the same k, so that x takes no registers for columns that
+// 16 of them would leave empty.  x of a
 // wave's kU units stays in registers while it streams the weights of its row
 // groups (four weight rows each), the next group's loads in flight behind the
 // current one's products.  The sixteen blocks' sums are added across lanes;
@@ -254,23 +255,23 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs a) {
 constexpr int kOneRows = 4;
 constexpr int kBatch = 16;  // row groups that leave together
 
-template <bool kNv, int kU>
-__global__ __launch_bounds__(512) void linear_one_kernel(LinearArgs a) {
+template <bool kNv, int kU, int kT>
+__global__ __launch_bounds__(512, 2) void linear_one_kernel(LinearArgs a) {
   typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
-  extern __shared__ f32x4 red[];  // [waves][64], only with more than one wave
+  extern __shared__ f32x4 red[];  // [waves][kT][64], only with more than one wave
   const int K = a.K, N = a.N, kgroups = K >> 5;
   const int lane = mx::lane_id(), b = lane >> 2, i4 = lane & 3;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int kscales = kNv ? K >> 4 : kgroups;
   const int groups = (N + 3) >> 2;  // of a tile
-  const int64_t total = (int64_t)count_tiles(a, kOneRows) * groups;
+  const int64_t total = (int64_t)count_tiles(a, kOneRows * kT) * groups;
   int64_t job = total * blockIdx.x / gridDim.x;
   const int64_t last = total * (blockIdx.x + 1) / gridDim.x;
 
   while (job < last) {  // uniform: the jobs of one tile at a time
     const int ti = (int)(job / groups);
     Tile t;
-    if (!find_tile(a, kOneRows, ti, t)) return;  // uniform, not reached: job < total
+    if (!find_tile(a, kOneRows * kT, ti, t)) return;  // uniform, not reached: job < total
     const int g0 = (int)(job - (int64_t)ti * groups), g1 = (int)min((int64_t)groups, g0 + (last - job));
     job += g1 - g0;
     const auto rx = buffer(a.x + (size_t)t.row0 * K, (uint32_t)t.rows * K * 2);
@@ -279,7 +280,7 @@ __global__ __launch_bounds__(512) void linear_one_kernel(LinearArgs a) {
     const auto rw = buffer(a.blocks + row0 * (K >> 1), nrows * (K >> 1));
     const auto rs = buffer(a.scales + row0 * kscales, nrows * kscales);
 
-    u32x4 x[kU][4];
+    u32x4 x[kT][kU][4];
     uint32_t woff[kU], soff[kU];
     bool dead[kU];  // groups past K: zero x and zero weights
 #pragma unroll
@@ -287,8 +288,11 @@ __global__ __launch_bounds__(512) void linear_one_kernel(LinearArgs a) {
       const int g = 16 * (wave * kU + u) + b;
       dead[u] = g >= kgroups;
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        x[u][s] = __builtin_amdgcn_raw_buffer_load_b128(rx, dead[u] ? kDead : (uint32_t)i4 * K * 2 + g * 64 + 16 * s, 0, 0);
+      for (int p = 0; p < kT; ++p)
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          x[p][u][s] = __builtin_amdgcn_raw_buffer_load_b128(
+              rx, dead[u] ? kDead : (uint32_t)(4 * p + i4) * K * 2 + g * 64 + 16 * s, 0, 0);
       woff[u] = (uint32_t)i4 * (K >> 1) + g * 16;
       soff[u] = (uint32_t)i4 * kscales + g * (kNv ? 2 : 1);
     }
@@ -307,9 +311,9 @@ __global__ __launch_bounds__(512) void linear_one_kernel(LinearArgs a) {
         r.sc[u] = kNv ? __builtin_amdgcn_raw_buffer_load_b16(rs, so, 0, 0) : __builtin_amdgcn_raw_buffer_load_b8(rs, so, 0, 0);
       }
     };
-    f32x4 kept = {};
+    f32x4 kept[kT] = {};
     auto multiply = [&](const Group& r, int g) {
-      f32x4 acc[2] = {};
+      f32x4 acc[kT][2] = {};
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const GroupScale<kNv> gs(r.sc[u] & 255u, r.sc[u] >> 8);
@@ -318,41 +322,53 @@ __global__ __launch_bounds__(512) void linear_one_kernel(LinearArgs a) {
           const u32x4 wv = gs.convert(r.w[u][s], s);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint2 av{wv[2 * h], wv[2 * h + 1]}, bv{x[u][s][2 * h], x[u][s][2 * h + 1]};
-            acc[h] = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4, av), __builtin_bit_cast(s16x4, bv),
-                                                            acc[h], 0, 0, 0);
+            const uint2 av{wv[2 * h], wv[2 * h + 1]};
+#pragma unroll
+            for (int p = 0; p < kT; ++p) {
+              const uint2 bv{x[p][u][s][2 * h], x[p][u][s][2 * h + 1]};
+              acc[p][h] = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4, av),
+                                                                 __builtin_bit_cast(s16x4, bv), acc[p][h], 0, 0, 0);
+            }
           }
         }
       }
       // lane (b, j): weight rows 0..3 of x row j over block b's k; add the blocks
-      f32x4 v = acc[0] + acc[1];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float f = v[c];
+      for (int i = 0; i < 4 * kT; ++i) {
+        const int p = i >> 2, c = i & 3;
+        float f = acc[p][0][c] + acc[p][1][c];
         f += __int_as_float(mx::dpp_i32<mx::kDppRowRor4>(__float_as_int(f)));
         f += __int_as_float(mx::dpp_i32<mx::kDppRowRor8>(__float_as_int(f)));
-        const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(f), __float_as_uint(f), false, false);
-        f = __uint_as_float(p[0]) + __uint_as_float(p[1]);
-        const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(f), __float_as_uint(f), false, false);
-        f = __uint_as_float(q[0]) + __uint_as_float(q[1]);
-        if (b == ((g - g0) & (kBatch - 1))) kept[c] = f;
+        const auto r16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(f), __float_as_uint(f), false, false);
+        f = __uint_as_float(r16[0]) + __uint_as_float(r16[1]);
+        const auto r32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(f), __float_as_uint(f), false, false);
+        f = __uint_as_float(r32[0]) + __uint_as_float(r32[1]);
+        if (b == ((g - g0) & (kBatch - 1))) kept[p][c] = f;
       }
     };
     auto leave = [&](int gb, int ge) {  // row groups gb .. ge - 1, at most kBatch
-      f32x4 v = kept;
+      f32x4 v[kT];
+#pragma unroll
+      for (int p = 0; p < kT; ++p) v[p] = kept[p];
       if (waves > 1) {  // uniform
-        red[wave * 64 + lane] = v;
+#pragma unroll
+        for (int p = 0; p < kT; ++p) red[(wave * kT + p) * 64 + lane] = kept[p];
         __syncthreads();
-        v = red[lane];
-        for (int u = 1; u < waves; ++u) v += red[u * 64 + lane];
+#pragma unroll
+        for (int p = 0; p < kT; ++p) {
+          v[p] = red[p * 64 + lane];
+          for (int u = 1; u < waves; ++u) v[p] += red[(u * kT + p) * 64 + lane];
+        }
         __syncthreads();
         if (wave > 0) return;
       }
       const int n = 4 * (gb + b);
-      if (gb + b >= ge || i4 >= t.rows) return;
-      uint16_t* out = a.y + (size_t)(t.row0 + i4) * N + n;
+      if (gb + b >= ge) return;
       const uint16_t* bias = a.bias != nullptr ? a.bias + (size_t)t.e * N + n : nullptr;
-      store4(out, v, s2, bias, min(4, N - n), (N & 3) == 0);
+#pragma unroll
+      for (int p = 0; p < kT; ++p)
+        if (4 * p + i4 < t.rows)
+          store4(a.y + (size_t)(t.row0 + 4 * p + i4) * N + n, v[p], s2, bias, min(4, N - n), (N & 3) == 0);
     };
 
     Group r0, r1;
@@ -981,8 +997,15 @@ dim3 grid_of(int64_t tiles, int64_t chunks) {
 constexpr int kTileMinRows = 24;     // rows of an expert on average
 constexpr int kTileMinBlocks = 128;
 
+// Blocks for `jobs` row groups: one each while they are few (one pass, no
+// second latency), else as many as stay resident (per_cu waves to a CU).
+unsigned stream_blocks(int64_t jobs, int waves, int per_cu) {
+  const int64_t most = (int64_t)mxfp4moe::device_cu_count() * (per_cu / waves > 0 ? per_cu / waves : 1);
+  return (unsigned)(jobs < 2 * most ? jobs : most);
+}
+
 template <bool kNv, int kC>
-hipError_t launch_few(LinearArgs a, int waves, hipStream_t stream) {
+hipError_t launch_few_groups(const LinearArgs& a, int waves, hipStream_t stream) {
   // as many row groups to a block (x is read once for all) as leave two blocks for every CU
   const int64_t groups = ((int64_t)a.N + 15) / 16 * a.max_tiles, want = 2 * mxfp4moe::device_cu_count();
   const int g = groups >= 4 * want ? 4 : groups >= 2 * want ? 2 : 1;
@@ -994,28 +1017,35 @@ hipError_t launch_few(LinearArgs a, int waves, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Rows of an expert on average up to which tiles of 4 rows are taken.
-constexpr int kOneMeanRows = 1;
-constexpr int kOneWaves = 8;  // of a CU: what the registers hold (two for each SIMD)
-
 template <bool kNv>
-hipError_t launch_one(LinearArgs a, int units, hipStream_t stream) {
-  a.max_tiles = max_tiles(a, kOneRows);
-  const int waves = (units + 5) / 6, u = (units + waves - 1) / waves;
-  const int64_t jobs = (int64_t)a.max_tiles * ((a.N + 3) / 4);
-  const int64_t most = (int64_t)mxfp4moe::device_cu_count() * (kOneWaves / waves);
-  const unsigned grid = (unsigned)(jobs < most ? jobs : most);
-  const size_t lds = waves > 1 ? (size_t)waves * 64 * sizeof(f32x4) : 0;
+hipError_t launch_few(LinearArgs a, hipStream_t stream) {
+  a.max_tiles = max_tiles(a, kFewRows);
+  const int chunks = (a.K + 127) / 128;
+  const int waves = chunks <= 2 ? 1 : chunks <= 8 ? 4 : 8;
+  const int c = (chunks + waves - 1) / waves;
+  if (c <= 2) return launch_few_groups<kNv, 2>(a, waves, stream);
+  return launch_few_groups<kNv, 3>(a, waves, stream);
+}
+
+template <bool kNv, int kT>
+hipError_t launch_one(LinearArgs a, hipStream_t stream) {
+  a.max_tiles = max_tiles(a, kOneRows * kT);
+  const int units = (a.K + 511) / 512;
+  const int waves = units <= 24 ? (units + 2) / 3 : 8, u = (units + waves - 1) / waves;
+  const unsigned grid = stream_blocks((int64_t)a.max_tiles * ((a.N + 3) / 4), waves, u >= 3 || kT > 1 ? 8 : 16);
+  const size_t lds = waves > 1 ? (size_t)waves * kT * 64 * sizeof(f32x4) : 0;
   switch (u) {
-    case 1: linear_one_kernel<kNv, 1><<<grid, waves * 64, lds, stream>>>(a); break;
-    case 2: linear_one_kernel<kNv, 2><<<grid, waves * 64, lds, stream>>>(a); break;
-    case 3: linear_one_kernel<kNv, 3><<<grid, waves * 64, lds, stream>>>(a); break;
-    case 4: linear_one_kernel<kNv, 4><<<grid, waves * 64, lds, stream>>>(a); break;
-    case 5: linear_one_kernel<kNv, 5><<<grid, waves * 64, lds, stream>>>(a); break;
-    default: linear_one_kernel<kNv, 6><<<grid, waves * 64, lds, stream>>>(a); break;
+    case 1: linear_one_kernel<kNv, 1, kT><<<grid, waves * 64, lds, stream>>>(a); break;
+    case 2: linear_one_kernel<kNv, 2, kT><<<grid, waves * 64, lds, stream>>>(a); break;
+    default: linear_one_kernel<kNv, 3, kT><<<grid, waves * 64, lds, stream>>>(a); break;
   }
   return hipGetLastError();
 }
+constexpr int kOneMaxK = 3 * 8 * 512;  // three units for each of eight waves
+
+// Rows of an expert on average (dense: rows) up to which tiles of 4 and of 8
+// rows are taken.
+constexpr int kMeanOf4 = 2, kMeanOf8 = 6;
 
 template <bool kNv>
 hipError_t linear(LinearArgs a, hipStream_t stream) {
@@ -1025,15 +1055,12 @@ hipError_t linear(LinearArgs a, hipStream_t stream) {
     linear_tile_kernel<kNv><<<grid_of(a.max_tiles, n_tiles), 256, 0, stream>>>(a);
     return hipGetLastError();
   }
-  const int units = (a.K + 511) / 512;
-  if (a.R <= (a.offsets == nullptr ? kOneRows : kOneMeanRows * a.E) && units <= 6 * 8) return launch_one<kNv>(a, units, stream);
-  a.max_tiles = max_tiles(a, kFewRows);
-  const int chunks = (a.K + 127) / 128;
-  const int waves = chunks <= 24 ? 4 : 8;
-  const int c = (chunks + waves - 1) / waves;
-  if (c <= 2) return launch_few<kNv, 2>(a, waves, stream);
-  if (c <= 4) return launch_few<kNv, 4>(a, waves, stream);
-  return launch_few<kNv, 6>(a, waves, stream);
+  if (a.K <= kOneMaxK) {
+    const bool dense = a.offsets == nullptr;
+    if (dense ? a.R <= 4 : a.R <= kMeanOf4 * a.E) return launch_one<kNv, 1>(a, stream);
+    if (dense ? a.R <= 8 : a.R <= kMeanOf8 * a.E) return launch_one<kNv, 2>(a, stream);
+  }
+  return launch_few<kNv>(a, stream);
 }
 
 template <bool kNv>
