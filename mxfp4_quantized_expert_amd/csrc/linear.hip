@@ -44,6 +44,7 @@ struct LinearArgs {
   uint16_t* y;              // forward: y [R, N]; gradient: dx [R, K]
   int R, K, N, E;
   int max_tiles;            // row tiles, at most
+  int tile_rows;            // rows of a tile (the 128-row kernels: 128, 64 or 32)
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes) {
@@ -686,9 +687,9 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs a) {
   __shared__ __attribute__((aligned(16))) u32x4 arena[kArenaSlots];
   const int n_tiles = (a.N + kTileN - 1) / kTileN;
   int ti, nt;
-  if (!map_tile(a, kTileRows, n_tiles, ti, nt)) return;  // uniform per block
+  if (!map_tile(a, a.tile_rows, n_tiles, ti, nt)) return;  // uniform per block
   Tile t;
-  if (!find_tile(a, kTileRows, ti, t)) return;
+  if (!find_tile(a, a.tile_rows, ti, t)) return;
   const int K = a.K, N = a.N, n0 = nt * kTileN;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int nrows = min(kTileN, N - n0), kscales = kNv ? K >> 4 : K >> 5;
@@ -933,9 +934,9 @@ __global__ __launch_bounds__(256, 2) void linear_backward_tile_kernel(LinearArgs
   __shared__ __attribute__((aligned(16))) uint16_t table[2 * (kNv ? 16 : 8) * 64];
   const int k_tiles = (a.K + kBackK - 1) / kBackK;
   int ti, kt;
-  if (!map_tile(a, kTileRows, k_tiles, ti, kt)) return;  // uniform per block
+  if (!map_tile(a, a.tile_rows, k_tiles, ti, kt)) return;  // uniform per block
   Tile t;
-  if (!find_tile(a, kTileRows, ti, t)) return;
+  if (!find_tile(a, a.tile_rows, ti, t)) return;
   const int K = a.K, N = a.N, k0 = kt * kBackK;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int kscales = kNv ? K >> 4 : K >> 5;
@@ -994,8 +995,38 @@ dim3 grid_of(int64_t tiles, int64_t chunks) {
   return blocks <= kMaxX ? dim3((unsigned)blocks) : dim3((unsigned)kMaxX, (unsigned)((blocks + kMaxX - 1) / kMaxX));
 }
 
-constexpr int kTileMinRows = 24;     // rows of an expert on average
-constexpr int kTileMinBlocks = 128;
+// Whether the tiles of up to 128 rows pay, and their rows: a choice by the
+// sizes alone, from times measured at N, K = 736 .. 2880, 1 to 32 experts and
+// 4 to 256 rows of an expert.
+//
+// A tile block takes a fixed time for each chunk of its loop, whatever few
+// rows it has (us: 0.62, 0.72, 0.9, 1.05 with 1 to 4 live row blocks; the
+// gradient a tenth more), two blocks a CU at once.  So tiles are halved while
+// all blocks still run at once: 1024 dense rows, 2880 x 2880: 47 us as 96
+// blocks of 128 rows, 32 us as 384 of 32.
+//
+// The 16-row kernels read the weights once for each 16 rows: from HBM the
+// first time, at `cold` bytes/us, from the caches then, at `hot`.
+struct TilePlan {
+  bool pays;
+  int rows;
+};
+TilePlan plan_tiles(LinearArgs a, int64_t col_tiles, int chunks, bool nv, double chunk_cost, double cold, double hot) {
+  TilePlan p{false, kTileRows};
+  const int64_t slots = 2 * mxfp4moe::device_cu_count();
+  while (p.rows > 32 && max_tiles(a, p.rows / 2) * col_tiles <= slots) p.rows /= 2;
+  const double chunk_us[5] = {0, 0.62, 0.72, 0.9, 1.05};
+  // half of the experts' last tiles, in the mean
+  const int64_t experts = a.E < a.R ? a.E : a.R;
+  const double blocks = ((double)a.R / p.rows + 0.5 * experts) * col_tiles;
+  const double rounds = blocks > slots ? blocks / slots : 1.0;
+  const double bytes = (double)a.N * a.K * (nv ? 0.5625 : 0.53125);
+  const double tile_us = 4 + rounds * chunks * chunk_cost * chunk_us[p.rows / 32];
+  const double reads = (double)a.R / kFewRows + 0.5 * experts;  // of one expert's weights
+  const double few_us = 4 + experts * bytes / cold + (reads > experts ? reads - experts : 0) * bytes / hot;
+  p.pays = tile_us < few_us;
+  return p;
+}
 
 // Blocks for `jobs` row groups: one each while they are few (one pass, no
 // second latency), else as many as stay resident (per_cu waves to a CU).
@@ -1049,25 +1080,27 @@ constexpr int kMeanOf4 = 2, kMeanOf8 = 6;
 
 template <bool kNv>
 hipError_t linear(LinearArgs a, hipStream_t stream) {
-  const int64_t n_tiles = (a.N + kTileN - 1) / kTileN, rows = (int64_t)a.R / a.E;
-  if (rows >= kTileMinRows && n_tiles * max_tiles(a, kTileRows) >= kTileMinBlocks) {
-    a.max_tiles = max_tiles(a, kTileRows);
-    linear_tile_kernel<kNv><<<grid_of(a.max_tiles, n_tiles), 256, 0, stream>>>(a);
-    return hipGetLastError();
-  }
+  const int64_t n_tiles = (a.N + kTileN - 1) / kTileN;
   if (a.K <= kOneMaxK) {
     const bool dense = a.offsets == nullptr;
     if (dense ? a.R <= 4 : a.R <= kMeanOf4 * a.E) return launch_one<kNv, 1>(a, stream);
     if (dense ? a.R <= 8 : a.R <= kMeanOf8 * a.E) return launch_one<kNv, 2>(a, stream);
   }
-  return launch_few<kNv>(a, stream);
+  const TilePlan plan = plan_tiles(a, n_tiles, (a.K + 63) / 64, kNv, 1.0, 2.9e6, 3.7e6);
+  if (!plan.pays) return launch_few<kNv>(a, stream);
+  a.tile_rows = plan.rows;
+  a.max_tiles = max_tiles(a, plan.rows);
+  linear_tile_kernel<kNv><<<grid_of(a.max_tiles, n_tiles), 256, 0, stream>>>(a);
+  return hipGetLastError();
 }
 
 template <bool kNv>
 hipError_t linear_backward(LinearArgs a, hipStream_t stream) {
-  const int64_t k_tiles = (a.K + kBackK - 1) / kBackK, rows = (int64_t)a.R / a.E;
-  if (rows >= kTileMinRows && k_tiles * max_tiles(a, kTileRows) >= kTileMinBlocks) {
-    a.max_tiles = max_tiles(a, kTileRows);
+  const int64_t k_tiles = (a.K + kBackK - 1) / kBackK;
+  const TilePlan plan = plan_tiles(a, k_tiles, (a.N + 63) / 64, kNv, 1.1, 1.9e6, 6e6);
+  if (plan.pays) {
+    a.tile_rows = plan.rows;
+    a.max_tiles = max_tiles(a, plan.rows);
     const dim3 tile_grid = grid_of(a.max_tiles, k_tiles);
     if (a.N % 8 == 0) linear_backward_tile_kernel<kNv, true><<<tile_grid, 256, 0, stream>>>(a);
     else linear_backward_tile_kernel<kNv, false><<<tile_grid, 256, 0, stream>>>(a);
@@ -1086,7 +1119,7 @@ hipError_t linear_backward(LinearArgs a, hipStream_t stream) {
 LinearArgs args_of(const uint16_t* in, const uint8_t* blocks, const uint8_t* scales, const float* scale2,
                    const uint16_t* bias, const int32_t* offsets, int64_t R, int64_t K, int64_t N, int64_t E,
                    uint16_t* out) {
-  return {in, blocks, scales, scale2, bias, offsets, out, (int)R, (int)K, (int)N, (int)E, 0};
+  return {in, blocks, scales, scale2, bias, offsets, out, (int)R, (int)K, (int)N, (int)E, 0, 0};
 }
 
 }  // namespace

@@ -222,6 +222,58 @@ def test_many_rows_grouped(gpu, fmt, N, K):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("mean,N,K", [(900, 64, 160), (900, 72, 544), (900, 130, 288), (700, 200, 256),
+                                      (600, 256, 320), (900, 257, 96), (500, 321, 224), (150, 264, 1056),
+                                      (900, 97, 160), (900, 40, 1088), (300, 129, 640), (700, 520, 64)])
+def test_long_batches_grouped(gpu, fmt, mean, N, K):
+    """Enough rows that small matrices take the 128-row tiles too."""
+    counts = _many(N + K, mean=mean)
+    w = Weights(fmt, len(counts), N, K, seed=N)
+    check_both(gpu, w, sum(counts) + 11, offsets_of(counts, 7), bias=N % 2 == 1, label=f"long {fmt}")
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("N,K", [(97, 288), (200, 224), (264, 544)])
+def test_long_batches_infinite_inputs(gpu, fmt, N, K):
+    counts = _many(5, mean=700)
+    R = sum(counts)
+    w = Weights(fmt, len(counts), N, K, seed=3)
+    rng = np.random.default_rng(7)
+    off = offsets_of(counts)
+    at = np.sort(rng.permutation(R)[:2000])
+    rest = np.setdiff1d(np.arange(R), at)
+    for width, call in ((K, lambda v: w.linear(gpu, v, None, off)), (N, lambda v: w.backward(gpu, v, off))):
+        v = bf16(rng, R, width)
+        clean = call(v).clone()
+        v[at[::2]] = float("inf")
+        v[at[1::2]] = float("nan")
+        got = call(v)
+        assert torch.equal(got[rest], clean[rest])
+        assert not bool(torch.isfinite(got[at]).any())
+
+
+@pytest.mark.parametrize("fmt,nan", [("mxfp4", 0xFF), ("nvfp4", 0xFF)])
+def test_long_batches_nan_scales(gpu, fmt, nan):
+    N, K = 198, 352
+    counts = _many(3, mean=700)
+    off = offsets_of(counts)
+    e = int(np.argmax(counts))
+    w = Weights(fmt, len(counts), N, K, seed=4)
+    w.s[e, N - 1, -1] = nan
+    w.s[e, 3, 0] = nan
+    w.upload()
+    rng = np.random.default_rng(6)
+    R, first = sum(counts), int(np.sum(counts[:e]))
+    y, dx = w.linear(gpu, bf16(rng, R, K), None, off), w.backward(gpu, bf16(rng, R, N), off)
+    bad = torch.zeros(y.shape, dtype=torch.bool, device="cuda")
+    bad[first:first + counts[e], 3] = bad[first:first + counts[e], N - 1] = True
+    assert torch.equal(torch.isnan(y), bad)
+    bad = torch.zeros(dx.shape, dtype=torch.bool, device="cuda")
+    bad[first:first + counts[e], :w.group] = bad[first:first + counts[e], K - w.group:] = True
+    assert torch.equal(torch.isnan(dx), bad)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 @pytest.mark.parametrize("R,N,K", [(17_000, 40, 96), (2500, 2050, 1568), (4000, 1030, 1088)])
 def test_many_rows_dense(gpu, fmt, R, N, K):
     w = Weights(fmt, 1, N, K, dense=True, seed=R)
