@@ -416,6 +416,7 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 # The current stream's handle without building a torch.cuda.Stream (0.07 against 2.7 us of host
 # time a call; a call of a few tokens is bound by its host time).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # of an initialised runtime
 
 
 def _current_stream(t: torch.Tensor) -> int:
@@ -427,7 +428,13 @@ def _current_stream(t: torch.Tensor) -> int:
 def _elsewhere(t: torch.Tensor, stream) -> bool:
     """Whether a call on t has to be moved to another device or stream than the current ones."""
     return stream is not None or (isinstance(t, torch.Tensor) and t.is_cuda
-                                  and t.get_device() != torch.cuda.current_device())
+                                  and t.get_device() != _current_device())
+
+
+def _fits(t: torch.Tensor, dtype: torch.dtype, shape, device: torch.device) -> bool:
+    """Whether t passes _check_on, in the few steps that every call of a small batch pays for."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.shape == shape
+            and t.is_contiguous())
 
 
 def _place(t: torch.Tensor, stream):
@@ -444,6 +451,8 @@ def _place(t: torch.Tensor, stream):
 
 
 def _check_on(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: torch.device):
+    if _fits(t, dtype, shape, device):
+        return
     _check(t, name, dtype, shape)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -484,11 +493,11 @@ def moe_permute(x: torch.Tensor, sorted_pairs: torch.Tensor, top_k: int, out: Op
     _check(x, "x", x.dtype)
     _check_on(sorted_pairs, "sorted_pairs", torch.int32, (R,), dev)
     if out is None:
-        out = torch.empty((R, H), dtype=x.dtype, device=dev)
+        out = x.new_empty((R, H))
     else:
         _check_on(out, "out", x.dtype, (R, H), dev)
     if pair_rows is None:
-        pair_rows = torch.empty((T * top_k,), dtype=torch.int32, device=dev)
+        pair_rows = sorted_pairs.new_empty((T * top_k,))
     else:
         _check_on(pair_rows, "pair_rows", torch.int32, (T * top_k,), dev)
     st = load().moe_permute(x.data_ptr(), code, sorted_pairs.data_ptr(), T, H, top_k, R, out.data_ptr(),
@@ -513,7 +522,7 @@ def moe_permute_backward(d_rows: torch.Tensor, pair_rows: torch.Tensor, top_k: i
     _check(d_rows, "d_rows", d_rows.dtype)
     _check_on(pair_rows, "pair_rows", torch.int32, (P,), dev)
     if out is None:
-        out = torch.empty((T, H), dtype=d_rows.dtype, device=dev)
+        out = d_rows.new_empty((T, H))
     else:
         _check_on(out, "out", d_rows.dtype, (T, H), dev)
     st = load().moe_permute_backward(d_rows.data_ptr(), code, pair_rows.data_ptr(), T, H, top_k, R, out.data_ptr(),
@@ -539,7 +548,7 @@ def moe_unpermute(rows: torch.Tensor, pair_rows: torch.Tensor, topk_weights: tor
     _check_on(topk_weights, "topk_weights", torch.float32, (T, top_k), dev)
     _check_on(pair_rows, "pair_rows", torch.int32, (T * top_k,), dev)
     if out is None:
-        out = torch.empty((T, H), dtype=rows.dtype, device=dev)
+        out = rows.new_empty((T, H))
     else:
         _check_on(out, "out", rows.dtype, (T, H), dev)
     st = load().moe_unpermute(rows.data_ptr(), code, pair_rows.data_ptr(), topk_weights.data_ptr(), T, H, top_k, R,
@@ -568,11 +577,11 @@ def moe_unpermute_backward(dy: torch.Tensor, rows: torch.Tensor, sorted_pairs: t
     _check_on(pair_rows, "pair_rows", torch.int32, (T * top_k,), dev)
     _check_on(topk_weights, "topk_weights", torch.float32, (T, top_k), dev)
     if d_rows is None:
-        d_rows = torch.empty((R, H), dtype=rows.dtype, device=dev)
+        d_rows = rows.new_empty((R, H))
     else:
         _check_on(d_rows, "d_rows", rows.dtype, (R, H), dev)
     if d_weights is None:
-        d_weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        d_weights = topk_weights.new_empty((T, top_k))
     else:
         _check_on(d_weights, "d_weights", torch.float32, (T, top_k), dev)
     st = load().moe_unpermute_backward(dy.data_ptr(), rows.data_ptr(), code, sorted_pairs.data_ptr(),
@@ -597,7 +606,7 @@ def moe_route_backward(topk_ids: torch.Tensor, topk_weights: torch.Tensor, d_wei
     if num_experts < 1:
         raise ValueError(f"num_experts must be at least 1, got {num_experts}")
     if out is None:
-        out = torch.empty((T, num_experts), dtype=torch.float32, device=dev)
+        out = topk_weights.new_empty((T, num_experts))
     else:
         _check_on(out, "out", torch.float32, (T, num_experts), dev)
     st = load().moe_route_backward(topk_ids.data_ptr(), topk_weights.data_ptr(), d_weights.data_ptr(), T,
@@ -606,68 +615,54 @@ def moe_route_backward(topk_ids: torch.Tensor, topk_weights: torch.Tensor, d_wei
     return out
 
 
-def _linear_sizes(rows: torch.Tensor, name: str, blocks: torch.Tensor, scales: torch.Tensor, group: int,
-                  expert_offsets: Optional[torch.Tensor], scale2: Optional[torch.Tensor],
-                  bias: Optional[torch.Tensor] = None):
+def _linear_sizes(rows, name: str, blocks, scales, group: int, expert_offsets, scale2, bias):
     """(E, N, K) of a linear operator's weights, after the checks of every tensor but the rows' width."""
     if not isinstance(rows, torch.Tensor) or not isinstance(blocks, torch.Tensor):
         raise TypeError(f"{name} and blocks must be torch.Tensors")
     lead = 2 if expert_offsets is None else 3
+    shape = blocks.shape
     if rows.dim() != 2:
         raise ValueError(f"{name} has {rows.dim()} dimensions, expected 2")
-    if blocks.dim() != lead:
-        raise ValueError(f"blocks has {blocks.dim()} dimensions, expected {lead} "
+    if len(shape) != lead:
+        raise ValueError(f"blocks has {len(shape)} dimensions, expected {lead} "
                          f"{'without' if lead == 2 else 'with'} expert_offsets")
-    E = 1 if lead == 2 else blocks.shape[0]
-    N, K = blocks.shape[-2], 2 * blocks.shape[-1]
+    E = 1 if lead == 2 else shape[0]
+    N, K = shape[-2], 2 * shape[-1]
     dev = rows.device
-    _check(rows, name, torch.bfloat16)
-    _check_on(blocks, "blocks", torch.uint8, None, dev)
-    _check_on(scales, "scales", torch.uint8, (*blocks.shape[:-1], K // group), dev)
+    if not (rows.dtype is torch.bfloat16 and rows.is_cuda and rows.is_contiguous()):
+        _check(rows, name, torch.bfloat16)
+    _check_on(blocks, "blocks", torch.uint8, shape, dev)
+    _check_on(scales, "scales", torch.uint8, (*shape[:-1], K // group), dev)
     if expert_offsets is not None:
         _check_on(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev)
     if group == 16:
         _check_on(scale2, "scale2", torch.float32, (E,), dev)
     if bias is not None:
-        _check_on(bias, "bias", torch.bfloat16, tuple(blocks.shape[:-1]), dev)
+        _check_on(bias, "bias", torch.bfloat16, shape[:-1], dev)
     return E, N, K
 
 
-def _address(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _linear(fn: str, x, blocks, scales, scale2, bias, expert_offsets, out):
-    group = 32 if fn == "moe_mxfp4_linear" else 16
-    E, N, K = _linear_sizes(x, "x", blocks, scales, group, expert_offsets, scale2, bias)
-    R = x.shape[0]
-    if x.shape[1] != K:
-        raise ValueError(f"x has rows of {x.shape[1]}, expected {K}")
+def _linear(fn: str, forward: bool, group: int, rows, blocks, scales, scale2, bias, expert_offsets, out):
+    """A linear operator's call: rows [R, K] -> [R, N], or the gradient's [R, N] -> [R, K]."""
+    name = "x" if forward else "dy"
+    E, N, K = _linear_sizes(rows, name, blocks, scales, group, expert_offsets, scale2, bias)
+    R, width = rows.shape
+    have, give = (K, N) if forward else (N, K)
+    if width != have:
+        raise ValueError(f"{name} has rows of {width}, expected {have}")
     if out is None:
-        out = torch.empty((R, N), dtype=torch.bfloat16, device=x.device)
+        out = rows.new_empty((R, give))
     else:
-        _check_on(out, "out", torch.bfloat16, (R, N), x.device)
-    weights = (blocks.data_ptr(), scales.data_ptr()) + ((scale2.data_ptr(),) if group == 16 else ())
-    st = getattr(load(), fn)(x.data_ptr(), *weights, _address(bias), _address(expert_offsets), R, K, N, E,
-                             out.data_ptr(), _current_stream(x))
-    _raise(fn, st)
-    return out
-
-
-def _linear_backward(fn: str, dy, blocks, scales, scale2, expert_offsets, out):
-    group = 32 if fn == "moe_mxfp4_linear_backward" else 16
-    E, N, K = _linear_sizes(dy, "dy", blocks, scales, group, expert_offsets, scale2)
-    R = dy.shape[0]
-    if dy.shape[1] != N:
-        raise ValueError(f"dy has rows of {dy.shape[1]}, expected {N}")
-    if out is None:
-        out = torch.empty((R, K), dtype=torch.bfloat16, device=dy.device)
-    else:
-        _check_on(out, "out", torch.bfloat16, (R, K), dy.device)
-    weights = (blocks.data_ptr(), scales.data_ptr()) + ((scale2.data_ptr(),) if group == 16 else ())
-    st = getattr(load(), fn)(dy.data_ptr(), *weights, _address(expert_offsets), R, K, N, E, out.data_ptr(),
-                             _current_stream(dy))
-    _raise(fn, st)
+        _check_on(out, "out", torch.bfloat16, (R, give), rows.device)
+    args = [rows.data_ptr(), blocks.data_ptr(), scales.data_ptr()]
+    if group == 16:
+        args.append(scale2.data_ptr())
+    if forward:
+        args.append(None if bias is None else bias.data_ptr())
+    st = getattr(load(), fn)(*args, None if expert_offsets is None else expert_offsets.data_ptr(), R, K, N, E,
+                             out.data_ptr(), _current_stream(rows))
+    if st:
+        raise MXFP4MoEError(fn, st)
     return out
 
 
@@ -681,7 +676,7 @@ def moe_mxfp4_linear(x: torch.Tensor, blocks: torch.Tensor, scales: torch.Tensor
     if _elsewhere(x, stream):
         with _place(x, stream):
             return moe_mxfp4_linear(x, blocks, scales, bias, expert_offsets, out)
-    return _linear("moe_mxfp4_linear", x, blocks, scales, None, bias, expert_offsets, out)
+    return _linear("moe_mxfp4_linear", True, 32, x, blocks, scales, None, bias, expert_offsets, out)
 
 
 def moe_nvfp4_linear(x: torch.Tensor, blocks: torch.Tensor, scales: torch.Tensor, scale2: torch.Tensor,
@@ -692,7 +687,7 @@ def moe_nvfp4_linear(x: torch.Tensor, blocks: torch.Tensor, scales: torch.Tensor
     if _elsewhere(x, stream):
         with _place(x, stream):
             return moe_nvfp4_linear(x, blocks, scales, scale2, bias, expert_offsets, out)
-    return _linear("moe_nvfp4_linear", x, blocks, scales, scale2, bias, expert_offsets, out)
+    return _linear("moe_nvfp4_linear", True, 16, x, blocks, scales, scale2, bias, expert_offsets, out)
 
 
 def moe_mxfp4_linear_backward(dy: torch.Tensor, blocks: torch.Tensor, scales: torch.Tensor,
@@ -703,7 +698,7 @@ def moe_mxfp4_linear_backward(dy: torch.Tensor, blocks: torch.Tensor, scales: to
     if _elsewhere(dy, stream):
         with _place(dy, stream):
             return moe_mxfp4_linear_backward(dy, blocks, scales, expert_offsets, out)
-    return _linear_backward("moe_mxfp4_linear_backward", dy, blocks, scales, None, expert_offsets, out)
+    return _linear("moe_mxfp4_linear_backward", False, 32, dy, blocks, scales, None, None, expert_offsets, out)
 
 
 def moe_nvfp4_linear_backward(dy: torch.Tensor, blocks: torch.Tensor, scales: torch.Tensor, scale2: torch.Tensor,
@@ -713,7 +708,7 @@ def moe_nvfp4_linear_backward(dy: torch.Tensor, blocks: torch.Tensor, scales: to
     if _elsewhere(dy, stream):
         with _place(dy, stream):
             return moe_nvfp4_linear_backward(dy, blocks, scales, scale2, expert_offsets, out)
-    return _linear_backward("moe_nvfp4_linear_backward", dy, blocks, scales, scale2, expert_offsets, out)
+    return _linear("moe_nvfp4_linear_backward", False, 16, dy, blocks, scales, scale2, None, expert_offsets, out)
 
 
 def profile_begin(stage: str, max_calls: int) -> None:
