@@ -400,11 +400,15 @@ constexpr int kFewK = 128;       // k of a block
 constexpr int kRedStride = 36;   // floats per lane in LDS (32 and padding)
 
 // Eight consecutive dy values of a row from element n on, zeros past N.
+// kAligned: N is even, so that every row starts at a dword.
 template <bool kAligned>
 __device__ __forceinline__ u32x4 load_dy8(const __amdgpu_buffer_rsrc_t& r, const uint16_t* row, uint32_t row_bytes0,
                                           int n, int N, bool whole) {
   if constexpr (kAligned) {
-    return __builtin_amdgcn_raw_buffer_load_b128(r, n < N ? row_bytes0 + n * 2 : kDead, 0, 0);
+    u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, n < N ? row_bytes0 + n * 2 : kDead, 0, 0);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) v[i] = n + 2 * i < N ? v[i] : 0u;
+    return v;
   } else {
     u32x4 v;
     if (whole) {  // uniform: no lane reaches past N
@@ -776,7 +780,7 @@ __device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][4], u32x4* aren
   const uint32_t doff = (uint32_t)pr * N * 2 + 16 * part;
   // weight rows pr, pr + 32: the swizzle of the code pieces is the row's low bits
   const uint32_t woff = (uint32_t)pr * (K >> 1) + (k0 >> 1) + 16 * (pc ^ (pr & 7));
-  // aligned dy rows travel by the load unit, others through registers
+  // dy rows that start at a dword (N even) travel by the load unit, others through registers
   constexpr int kLoads = kAligned ? 6 : 2;
   u32x4 dreg[4];
   auto load_dy = [&](int c) {
@@ -878,7 +882,7 @@ __device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][4], u32x4* aren
 #pragma unroll
       for (int cb = 0; cb < kLive; ++cb) b[s][cb] = base[boff[s] + cb * 256];
     }
-    if (64 * c + 64 > N) {  // rows past N: zero weights times zero dy (unaligned dy came with its zeros)
+    if (64 * c + 64 > N) {  // rows past N: zero weights times zero dy (dy through registers came with its zeros)
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const int left = N - (64 * c + 16 * s + 8 * half);  // of this lane's eight n
@@ -889,7 +893,10 @@ __device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][4], u32x4* aren
         }
 #pragma unroll
         for (int cb = 0; cb < kLive; ++cb)
-          if (kAligned && left <= 0) b[s][cb] = u32x4{0u, 0u, 0u, 0u};
+          if (kAligned) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[s][cb][i] = 2 * i < left ? b[s][cb][i] : 0u;
+          }
       }
     }
 #pragma unroll
@@ -1102,7 +1109,7 @@ hipError_t linear_backward(LinearArgs a, hipStream_t stream) {
     a.tile_rows = plan.rows;
     a.max_tiles = max_tiles(a, plan.rows);
     const dim3 tile_grid = grid_of(a.max_tiles, k_tiles);
-    if (a.N % 8 == 0) linear_backward_tile_kernel<kNv, true><<<tile_grid, 256, 0, stream>>>(a);
+    if (a.N % 2 == 0) linear_backward_tile_kernel<kNv, true><<<tile_grid, 256, 0, stream>>>(a);
     else linear_backward_tile_kernel<kNv, false><<<tile_grid, 256, 0, stream>>>(a);
     return hipGetLastError();
   }
@@ -1111,7 +1118,7 @@ hipError_t linear_backward(LinearArgs a, hipStream_t stream) {
   const int waves = steps < 8 ? steps : 8;
   const dim3 grid = grid_of(a.max_tiles, (a.K + kFewK - 1) / kFewK);
   const size_t lds = (size_t)waves * 64 * kRedStride * sizeof(float);
-  if (a.N % 8 == 0) linear_backward_few_kernel<kNv, true><<<grid, waves * 64, lds, stream>>>(a);
+  if (a.N % 2 == 0) linear_backward_few_kernel<kNv, true><<<grid, waves * 64, lds, stream>>>(a);
   else linear_backward_few_kernel<kNv, false><<<grid, waves * 64, lds, stream>>>(a);
   return hipGetLastError();
 }
