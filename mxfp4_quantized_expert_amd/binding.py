@@ -15,6 +15,7 @@ from typing import Optional
 import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmxfp4moe.so")
+HOST_PATH = os.path.join(os.path.dirname(LIB_PATH), "_host_calls.so")
 
 STATUS = {
     0: "ok",
@@ -32,6 +33,9 @@ STAGES = {"route": 1, "group": 2, "gate_up": 3, "down": 4, "combine": 5, "dequan
           "unpermute_backward": 16, "route_backward": 17, "linear": 18, "linear_backward": 19}
 
 _lib: Optional[ctypes.CDLL] = None
+# The module of the short host path (csrc/host_calls.cpp), set with _lib; without it every call goes
+# through ctypes.
+_host = None
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -45,7 +49,7 @@ class MXFP4MoEError(RuntimeError):
 
 def load() -> ctypes.CDLL:
     """Load the HIP library; raises if it has not been built (no fallback exists)."""
-    global _lib
+    global _lib, _host
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -106,6 +110,9 @@ def load() -> ctypes.CDLL:
     lib.mxfp4moe_profile_end.argtypes = [ctypes.POINTER(ctypes.c_float), ctypes.c_int]
     lib.mxfp4moe_profile_end.restype = ctypes.c_int
     _lib = lib
+    if os.path.exists(HOST_PATH):
+        from . import _host_calls
+        _host = _host_calls
     return lib
 
 
@@ -481,6 +488,10 @@ def moe_permute(x: torch.Tensor, sorted_pairs: torch.Tensor, top_k: int, out: Op
     float16 or float32) and sorted_pairs [R] int32, as moe_mxfp4_route gives them; an entry
     outside [0, T * top_k) makes an empty row of zeros.  Returns (rows [R, H], pair_rows
     [T * top_k] int32: every pair's row, -1 for none)."""
+    if _host is not None and stream is None and out is None and pair_rows is None:
+        got = _host.permute(x, sorted_pairs, top_k)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
     if _elsewhere(x, stream):
         with _place(x, stream):
             return moe_permute(x, sorted_pairs, top_k, out, pair_rows)
@@ -510,6 +521,10 @@ def moe_permute_backward(d_rows: torch.Tensor, pair_rows: torch.Tensor, top_k: i
                          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of moe_permute: dx[t] = sum_j d_rows[pair_rows[t * top_k + j]] over the pairs
     that have a row; d_rows [R, H], pair_rows [T * top_k].  Returns dx [T, H]."""
+    if _host is not None and stream is None and out is None:
+        got = _host.permute_backward(d_rows, pair_rows, top_k)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
     if _elsewhere(d_rows, stream):
         with _place(d_rows, stream):
             return moe_permute_backward(d_rows, pair_rows, top_k, out)
@@ -537,6 +552,10 @@ def moe_unpermute(rows: torch.Tensor, pair_rows: torch.Tensor, topk_weights: tor
     over the pairs that have a row (fp32, rounded once).  rows [R, H] (bfloat16, float16 or
     float32), pair_rows [T * top_k] int32 of moe_permute, topk_weights [T, top_k] float32.
     Returns y [T, H]."""
+    if _host is not None and stream is None and out is None:
+        got = _host.unpermute(rows, pair_rows, topk_weights)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
     if _elsewhere(rows, stream):
         with _place(rows, stream):
             return moe_unpermute(rows, pair_rows, topk_weights, out)
@@ -564,6 +583,10 @@ def moe_unpermute_backward(dy: torch.Tensor, rows: torch.Tensor, sorted_pairs: t
     """Gradients of moe_unpermute for dy [T, H]: d_rows [R, H] (the pair's weight times its token's
     dy; zeros for empty rows) and d_weights [T, top_k] float32 (dot products of dy[t] and the pairs'
     rows; 0 for a pair without one).  sorted_pairs and pair_rows as moe_permute read and wrote them."""
+    if _host is not None and stream is None and d_rows is None and d_weights is None:
+        got = _host.unpermute_backward(dy, rows, sorted_pairs, pair_rows, topk_weights)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
     if _elsewhere(rows, stream):
         with _place(rows, stream):
             return moe_unpermute_backward(dy, rows, sorted_pairs, pair_rows, topk_weights, d_rows, d_weights)
@@ -595,6 +618,10 @@ def moe_route_backward(topk_ids: torch.Tensor, topk_weights: torch.Tensor, d_wei
                        num_experts: int, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of the softmax over a token's picks: topk_ids [T, top_k] int32, topk_weights and
     d_weights [T, top_k] float32 -> d_logits [T, num_experts] float32, zero at experts not picked."""
+    if _host is not None and stream is None and out is None:
+        got = _host.route_backward(topk_ids, topk_weights, d_weights, num_experts)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
     if _elsewhere(topk_weights, stream):
         with _place(topk_weights, stream):
             return moe_route_backward(topk_ids, topk_weights, d_weights, num_experts, out)
@@ -673,6 +700,10 @@ def moe_mxfp4_linear(x: torch.Tensor, blocks: torch.Tensor, scales: torch.Tensor
     and scales [N, K/32] uint8, bias [N] bfloat16.  Per expert: blocks [E, N, K/2], scales
     [E, N, K/32], bias [E, N] and expert_offsets [E + 1] int32 (expert e has the rows
     [offsets[e], offsets[e + 1]); rows outside them keep what `out` held).  Returns y [R, N]."""
+    if _host is not None and stream is None and out is None:
+        got = _host.linear(False, 32, x, blocks, scales, None, bias, expert_offsets)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
     if _elsewhere(x, stream):
         with _place(x, stream):
             return moe_mxfp4_linear(x, blocks, scales, bias, expert_offsets, out)
@@ -684,6 +715,10 @@ def moe_nvfp4_linear(x: torch.Tensor, blocks: torch.Tensor, scales: torch.Tensor
                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """moe_mxfp4_linear over NVFP4 weights: scales [..., N, K/16] uint8 (E4M3) and scale2 [E]
     float32 ([1] dense), which multiplies the product before the bias."""
+    if _host is not None and stream is None and out is None:
+        got = _host.linear(False, 16, x, blocks, scales, scale2, bias, expert_offsets)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
     if _elsewhere(x, stream):
         with _place(x, stream):
             return moe_nvfp4_linear(x, blocks, scales, scale2, bias, expert_offsets, out)
@@ -695,6 +730,10 @@ def moe_mxfp4_linear_backward(dy: torch.Tensor, blocks: torch.Tensor, scales: to
                               stream=None) -> torch.Tensor:
     """Gradient of moe_mxfp4_linear to its rows: dx = dy W for dy [R, N] bfloat16 (weights and
     offsets as there; the weights are frozen).  Returns dx [R, K]."""
+    if _host is not None and stream is None and out is None:
+        got = _host.linear(True, 32, dy, blocks, scales, None, None, expert_offsets)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
     if _elsewhere(dy, stream):
         with _place(dy, stream):
             return moe_mxfp4_linear_backward(dy, blocks, scales, expert_offsets, out)
@@ -705,6 +744,10 @@ def moe_nvfp4_linear_backward(dy: torch.Tensor, blocks: torch.Tensor, scales: to
                               expert_offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                               stream=None) -> torch.Tensor:
     """Gradient of moe_nvfp4_linear to its rows: dx = scale2 * (dy W).  Returns dx [R, K]."""
+    if _host is not None and stream is None and out is None:
+        got = _host.linear(True, 16, dy, blocks, scales, scale2, None, expert_offsets)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
     if _elsewhere(dy, stream):
         with _place(dy, stream):
             return moe_nvfp4_linear_backward(dy, blocks, scales, scale2, expert_offsets, out)

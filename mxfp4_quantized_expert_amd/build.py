@@ -15,6 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxfp4moe.so")
+HOST_CALLS = os.path.join(PKG, "_host_calls.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -47,8 +48,28 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_host_calls() -> None:
+    """csrc/host_calls.cpp, the Python module of the short host path, beside the library it calls."""
+    import sysconfig
+
+    import torch
+
+    torch_dir = os.path.dirname(torch.__file__)
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(torch_dir, "include"), "-isystem", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "host_calls.cpp"), "-o", HOST_CALLS + ".tmp",
+           f"-L{PKG}", "-lmxfp4moe", "-Wl,-rpath,$ORIGIN",
+           f"-L{os.path.join(torch_dir, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("building host_calls failed:\n" + r.stdout + r.stderr)
+    os.replace(HOST_CALLS + ".tmp", HOST_CALLS)
+
+
 def build(verbose: bool = True) -> str:
-    """Compile every csrc/*.hip for gfx950 and link libmxfp4moe.so next to this file."""
+    """Compile every csrc/*.hip for gfx950 and link libmxfp4moe.so next to this file, then the
+    Python module that calls it."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
@@ -59,6 +80,7 @@ def build(verbose: bool = True) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
     os.replace(tmp, LIB)
+    _build_host_calls()
     if verbose:
         print(f"built {LIB}")
     return LIB
