@@ -15,6 +15,7 @@
 // sums are its fp32 accumulation; s2 and the bias follow in fp32 and the
 // result is rounded once.
 #include <type_traits>
+#include <utility>
 
 #include "expert_device.h"
 #include "internal.h"
@@ -499,40 +500,39 @@ __global__ __launch_bounds__(512) void linear_backward_few_kernel(LinearArgs a) 
 
 // --------------------------------------------------------------- many rows
 
-// Scale bytes of one weight row, 32 at a time from byte offset `o` of the
+// Scale bytes of one weight row, 24 at a time from byte offset `o` of the
 // buffer: aligned dwords and a funnel shift, because a row of scales starts
 // at any byte.  The buffer starts at a dword and ends with the dword that
 // holds its last byte.
+constexpr int kScaleDwords = 6;
 struct ScaleBytes {
-  uint32_t d[9];
+  uint32_t d[kScaleDwords + 1];
   __device__ __forceinline__ void load(const __amdgpu_buffer_rsrc_t& r, uint32_t o) {
     o &= ~3u;
+    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0);
+    const auto u = __builtin_amdgcn_raw_buffer_load_b96(r, o + 16, 0, 0);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, o + 16 * h, 0, 0);
+    for (int i = 0; i < 4; ++i) d[i] = v[i];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d[4 * h + i] = v[i];
-    }
-    d[8] = __builtin_amdgcn_raw_buffer_load_b32(r, o + 32, 0, 0);
+    for (int i = 0; i < 3; ++i) d[4 + i] = u[i];
   }
 };
 
 // y for row tiles of 128: 32x32x16 MFMA, a block of four waves makes 256
 // weight rows x 128 rows, each wave 64 x 128.  K runs in chunks of 64: lane
 // half h takes group 2c + h of its weight row, dword s of the group's 16
-// bytes in step s, and the x values of the same k.  Chunks travel from global
-// memory into three LDS stages by the load unit (16 bytes a lane), chunk c+2
-// on its way while chunk c is multiplied; one barrier a chunk.  x rows are
-// 128 bytes a stage, their 16-byte pieces XOR-swizzled so that the 128-bit
-// reads of consecutive rows hit distinct banks.  Scale bytes go straight to
-// registers, a row's next 16 at a time.  Two blocks a CU: one converts and
-// waits while the other multiplies.  Token blocks of 32 without rows are
-// neither read nor multiplied.  Bound: the bf16 MFMA rate (and the
-// conversions beside it).
+// bytes in step s, and the x values of the same k.  x travels from global
+// memory into a ring of LDS stages of 64 k, the weights into one of stages of
+// 128 k, by the load unit (16 bytes a lane), later chunks on their way while
+// one is multiplied; one barrier a chunk.
+//
+// The stages are arrays of their own and the loop is unrolled over the period
+// of both rings: the compiler waits for every load into an array that an LDS
+// read may touch, so with one array and a stage counted at run time it waited
+// for all loads in flight before each chunk.
 constexpr int kTileRows = 128, kTileN = 256;
 constexpr int kXSlots = kTileRows * 8, kWSlots = kTileN * 2, kStageSlots = kXSlots + kWSlots;
 constexpr int kStages = 3;
-constexpr int kArenaSlots = 5120;  // 16-byte slots of the forward's rings: 80 KB
 
 __device__ __forceinline__ int swizzle(int row) { return (row ^ (row >> 3)) & 7; }
 
@@ -540,155 +540,149 @@ __device__ __forceinline__ void load_lds16(const __amdgpu_buffer_rsrc_t& r, u32x
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0, 0);
 }
 
-// Stages in flight by the number of live row blocks: a block without rows
-// needs no room, and the fewer rows share the weights, the more of them have
-// to be on their way to keep HBM busy.  x stages hold 64 k, weight stages 128
-// k: 64 bytes of a row at a time stream from HBM at 4.7 TB/s, 32 bytes at
-// 3.3 (load-unit reads of 565 MB in this pattern, no arithmetic).  Both rings
-// within 80 KB (two blocks a CU).
-template <int kLive>
+// f(0), f(1), ... as compile-time numbers until one returns false.
+template <typename F, int... kP>
+__device__ __forceinline__ bool each_of(F&& f, std::integer_sequence<int, kP...>) {
+  return (f(std::integral_constant<int, kP>{}) && ...);
+}
+
+// The rings of a kernel for up to kMax blocks of 32 rows: kX stages of x, kW
+// of the weights, 80 KB in all (two blocks a CU).  The fewer rows share the
+// weights, the more of them have to be on their way to keep HBM busy.
+template <int kMax>
 struct Rings {
-  static constexpr int kX = kLive >= 4 ? 3 : kLive >= 2 ? 4 : 6;
-  static constexpr int kW = kLive >= 3 ? 2 : 3;
-  static constexpr int kXStage = kLive * 256, kWStage = kTileN * 4;  // 16-byte slots
-  // Iteration c issues (even c: 4 loads of the weights of chunks c + 2 kW - 2 and the next one, then) kLive loads of
-  // x of chunk c + kX - 1.  Loads that may be in flight when chunk c is read: those issued after its x, and after
-  // its weights.
-  static constexpr int after_x(int odd) {
+  static constexpr int kX = kMax > 2 ? 3 : 4, kW = kMax > 2 ? 2 : 3;
+  static constexpr int kPeriod = 12;  // chunks: a multiple of kX and of 2 kW
+  static_assert(kPeriod % kX == 0 && kPeriod % (2 * kW) == 0, "stages repeat with the period");
+  static constexpr int kXStage = kMax * 256, kWStage = kTileN * 4;  // 16-byte slots
+  static_assert(kX * kXStage + kW * kWStage <= 5120, "two blocks a CU");
+  // Chunk c issues `live` loads of x of chunk c + kX - 1, even c also 4 loads of the weights of chunks c + 2 kW - 2 and
+  // the next one.  Loads that may be in flight when chunk c is read: those of the chunks after the one that issued its
+  // x, and for its weights.  Loads of scales are not counted: a wave without work makes none.
+  static constexpr int after_x(int live, int odd) {
     int n = 0;
-    for (int i = 1; i <= kX - 2; ++i) n += kLive + (((odd + i) & 1) == 0 ? 4 : 0);
+    for (int i = 1; i <= kX - 2; ++i) n += live + (((odd + i) & 1) == 0 ? 4 : 0);
     return n;
   }
-  static constexpr int kAfterW = kLive * 2 * (kW - 1) + 4 * (kW - 2);
-  static constexpr int kAheadOdd = after_x(1), kAheadEven = after_x(0) < kAfterW ? after_x(0) : kAfterW;
-  static_assert(kX * kXStage + kW * kWStage <= kArenaSlots, "rings fit in the arena");
+  static constexpr int ahead(int live, int odd) {
+    const int w = live * 2 * (kW - 1) + 4 * (kW - 2), x = after_x(live, odd);
+    return odd || x < w ? x : w;
+  }
 };
 
 // The chunk loop over kLive blocks of 32 rows.
-template <bool kNv, int kLive>
-__device__ __forceinline__ void tile_chunks(f32x16 (&acc)[2][4], u32x4* arena, const __amdgpu_buffer_rsrc_t& rx,
+template <bool kNv, int kLive, int kMax>
+__device__ __forceinline__ void tile_chunks(f32x16 (&acc)[2][kMax], u32x4* const (&xst)[Rings<kMax>::kX],
+                                            u32x4* const (&wst)[Rings<kMax>::kW], const __amdgpu_buffer_rsrc_t& rx,
                                             const __amdgpu_buffer_rsrc_t& rw, const __amdgpu_buffer_rsrc_t& rs,
                                             int K, uint32_t scale0, int kscales, int wave, bool work) {
-  using Ring = Rings<kLive>;
+  using Ring = Rings<kMax>;
   const int t = threadIdx.x, lane = t & 63, half = lane >> 5, lrow = lane & 31;
   const int chunks = (K + 63) >> 6, pairs = (chunks + 1) >> 1;
-  u32x4* const wring = arena + Ring::kX * Ring::kXStage;
   // this thread's pieces of a stage
-  const int xr = t >> 3;
-  const uint32_t xoff = (uint32_t)xr * K * 2 + 16 * ((t & 7) ^ swizzle(xr & 31));
+  const int xr = t >> 3, xpart = (t & 7) ^ swizzle(xr & 31);
+  const uint32_t xoff = (uint32_t)xr * K * 2 + 16 * xpart;
+  const uint32_t xlast = (K & 32) != 0 && xpart >= 4 ? kDead : 0u;  // the half chunk past K: zeros
   const uint32_t woff = (uint32_t)(t >> 2) * (K >> 1) + 16 * ((t & 3) ^ ((t >> 4) & 3));
-  auto issue_x = [&](int c, int st, int k) {
-    load_lds16(rx, arena + st * Ring::kXStage + wave * 64 + k * 256,
-               xoff + (uint32_t)(k * 32) * K * 2 + min(c, chunks - 1) * 128);
+  auto issue_x = [&](int c, u32x4* st, int k) __attribute__((always_inline)) {
+    const uint32_t o = xoff + (uint32_t)(k * 32) * K * 2 + min(c, chunks - 1) * 128;
+    load_lds16(rx, st + wave * 64 + k * 256, c >= chunks - 1 ? o | xlast : o);
   };
-  auto issue_w = [&](int s, int st, int k) {
-    load_lds16(rw, wring + st * Ring::kWStage + wave * 64 + k * 256,
-               woff + (uint32_t)(k * 64) * (K >> 1) + min(s, pairs - 1) * 64);
+  auto issue_w = [&](int s, u32x4* st, int k) __attribute__((always_inline)) {
+    load_lds16(rw, st + wave * 64 + k * 256, woff + (uint32_t)(k * 64) * (K >> 1) + min(s, pairs - 1) * 64);
   };
-  int xs = 0, ws = 0;  // stages of the chunk (pair) being read
 
-  // this lane's scale row (of the wave's 64): 32 bytes hold the groups of kSpan pairs of chunks
-  constexpr int kStep = kNv ? 2 : 1, kSpan = 8 / kStep;  // dwords of a pair
+  // this lane's scale row (of the wave's 64): 24 bytes hold the groups of kSpan chunks
+  constexpr int kSpan = kNv ? 6 : 12;
   const uint32_t so = scale0 + (uint32_t)(wave * 64 + lane) * kscales;
-  ScaleBytes sb, next;
+  ScaleBytes next;
+  uint32_t sb[kScaleDwords];
   next.load(rs, so);
+  // what chunks before the first would have issued
   constexpr int kPrologue = 2 * (Ring::kW - 1) > Ring::kX - 1 ? 2 * (Ring::kW - 1) : (Ring::kX / 2) * 2;
 #pragma unroll
   for (int c = -kPrologue; c < 0; ++c) {
     if (c % 2 == 0 && c / 2 + Ring::kW - 1 >= 0) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) issue_w(c / 2 + Ring::kW - 1, c / 2 + Ring::kW - 1, k);
+      for (int k = 0; k < 4; ++k) issue_w(c / 2 + Ring::kW - 1, wst[c / 2 + Ring::kW - 1], k);
     }
     if (c + Ring::kX - 1 >= 0) {
 #pragma unroll
-      for (int k = 0; k < kLive; ++k) issue_x(c + Ring::kX - 1, c + Ring::kX - 1, k);
+      for (int k = 0; k < kLive; ++k) issue_x(c + Ring::kX - 1, xst[c + Ring::kX - 1], k);
     }
+    __builtin_amdgcn_sched_barrier(0);  // the waits count on this order
   }
   int boff[4];
 #pragma unroll
   for (int s = 0; s < 4; ++s) boff[s] = lrow * 8 + ((4 * half + s) ^ swizzle(lrow));
   const int arow = (wave * 64 + lrow) * 4, aswz = (lrow >> 2) & 3;
 
-  // chunk 2s + kOdd, its scale dword(s) in row order: e[0] of the lane's first weight row, e[1] of its second
-  auto chunk = [&](auto odd, int c, int s, uint32_t e0, uint32_t e1) {
-    constexpr int kOdd = decltype(odd)::value;
-    constexpr int kIssue = kLive + (kOdd ? 0 : 4);
-    const int xnext = xs == 0 ? Ring::kX - 1 : xs - 1, wnext = ws == 0 ? Ring::kW - 1 : ws - 1;
-    auto issue = [&](int k) {
-      if (!kOdd && k < 4) issue_w(s + Ring::kW - 1, wnext, k);
-      else issue_x(c + Ring::kX - 1, xnext, k - (kOdd ? 0 : 4));
-    };
-    if (work) {
-      const u32x4* xbase = arena + xs * Ring::kXStage;
-      const u32x4* wbase = wring + ws * Ring::kWStage + arow + ((2 * kOdd + half) ^ aswz);
-      u32x4 w[2];
-      bf16x8 b[4][kLive];
+  int c0 = 0;
+  auto chunk = [&](auto at) __attribute__((always_inline)) {
+    constexpr int p = decltype(at)::value, kOdd = p & 1;
+    const int c = c0 + p;
+    mxgemm::wait_loads_then_barrier<Ring::ahead(kLive, kOdd)>();
+    if constexpr (p % kSpan == 0) {
 #pragma unroll
-      for (int rb = 0; rb < 2; ++rb) w[rb] = wbase[rb * 128];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int cb = 0; cb < kLive; ++cb) b[i][cb] = mx::as_bf16x8(xbase[boff[i] + cb * 256]);
-      if (64 * c + 64 > K && half == 1) {  // the half chunk past K: zero weights times zero rows
-        e0 = e1 = 0u;
-#pragma unroll
-        for (int rb = 0; rb < 2; ++rb) w[rb] = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int cb = 0; cb < kLive; ++cb) b[i][cb] = mx::as_bf16x8(u32x4{0u, 0u, 0u, 0u});
-      }
-      const uint32_t sh = kNv ? 16 * half : 16 * kOdd + 8 * half;
-      e0 >>= sh;
-      e1 >>= sh;
-      const GroupScale<kNv> g0(e0 & 255u, (e0 >> 8) & 255u), g1(e1 & 255u, (e1 >> 8) & 255u);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bf16x8 a0 = mx::as_bf16x8(g0.convert(w[0][i], i)), a1 = mx::as_bf16x8(g1.convert(w[1][i], i));
-#pragma unroll
-        for (int cb = 0; cb < kLive; ++cb) {
-          acc[0][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a0, b[i][cb], acc[0][cb], 0, 0, 0);
-          acc[1][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a1, b[i][cb], acc[1][cb], 0, 0, 0);
-        }
-#pragma unroll
-        for (int k = 2 * i; k < 2 * i + 2; ++k)
-          if (k < kIssue) issue(k);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < kIssue; ++k) issue(k);
+      for (int i = 0; i < kScaleDwords; ++i) sb[i] = __builtin_amdgcn_alignbit(next.d[i + 1], next.d[i], 8 * (so & 3u));
+      next.load(rs, so + 4 * kScaleDwords * (c / kSpan + 1));
     }
-    xs = xs == Ring::kX - 1 ? 0 : xs + 1;
+    u32x4* const xnext = xst[(p + Ring::kX - 1) % Ring::kX];
+    u32x4* const wnext = wst[(p / 2 + Ring::kW - 1) % Ring::kW];
+    if constexpr (!kOdd) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) issue_w(c / 2 + Ring::kW - 1, wnext, k);
+    }
+#pragma unroll
+    for (int k = 0; k < kLive; ++k) issue_x(c + Ring::kX - 1, xnext, k);
+    if (!work) return;
+    const u32x4* xbase = xst[p % Ring::kX];
+    const u32x4* wbase = wst[p / 2 % Ring::kW] + arow + ((2 * kOdd + half) ^ aswz);
+    u32x4 w[2];
+    bf16x8 b[4][kLive];
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb) w[rb] = wbase[rb * 128];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int cb = 0; cb < kLive; ++cb) b[i][cb] = mx::as_bf16x8(xbase[boff[i] + cb * 256]);
+    // the chunk's dword of scales, in row order: e[0] of the lane's first weight row, e[1] of its second
+    constexpr int kDword = kNv ? p % kSpan : p % kSpan / 2;
+    const auto e = __builtin_amdgcn_permlane32_swap(sb[kDword], sb[kDword], false, false);
+    const uint32_t sh = kNv ? 16 * half : 16 * kOdd + 8 * half;
+    uint32_t e0 = e[0] >> sh, e1 = e[1] >> sh;
+    if (64 * c + 64 > K && half == 1) e0 = e1 = 0u;  // past K the rows are zeros: no NaN from a scale there
+    const GroupScale<kNv> g0(e0 & 255u, (e0 >> 8) & 255u), g1(e1 & 255u, (e1 >> 8) & 255u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bf16x8 a0 = mx::as_bf16x8(g0.convert(w[0][i], i)), a1 = mx::as_bf16x8(g1.convert(w[1][i], i));
+#pragma unroll
+      for (int cb = 0; cb < kLive; ++cb) {
+        acc[0][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a0, b[i][cb], acc[0][cb], 0, 0, 0);
+        acc[1][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a1, b[i][cb], acc[1][cb], 0, 0, 0);
+      }
+    }
   };
-  // dword i of the lanes' rows to the rows that the lanes multiply with
-  auto spread = [&](int i) { return __builtin_amdgcn_permlane32_swap(sb.d[i], sb.d[i], false, false); };
-
-  for (int s = 0; s < pairs; ++s) {
-    mxgemm::wait_loads_then_barrier<Ring::kAheadEven>();
-    if (s % kSpan == 0) {  // uniform
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sb.d[i] = __builtin_amdgcn_alignbit(next.d[i + 1], next.d[i], 8 * (so & 3u));
-    }
-    if (s % kSpan == kSpan - 1) next.load(rs, so + 4 * kStep * (s + 1));
-    const auto e = spread(0);
-    chunk(std::integral_constant<int, 0>{}, 2 * s, s, e[0], e[1]);
-    if (2 * s + 1 < chunks) {  // uniform
-      mxgemm::wait_loads_then_barrier<Ring::kAheadOdd>();
-      const auto o = spread(kStep - 1);
-      chunk(std::integral_constant<int, 1>{}, 2 * s + 1, s, o[0], o[1]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8 - kStep; ++i) sb.d[i] = sb.d[i + kStep];
-    ws = ws == Ring::kW - 1 ? 0 : ws + 1;
-  }
+  // Whole periods without an exit: from a loop with exits inside, the compiler's waits would count the loads that are
+  // in flight at any of them.
+  for (; c0 + Ring::kPeriod <= chunks; c0 += Ring::kPeriod)
+    each_of([&](auto at) __attribute__((always_inline)) { return chunk(at), true; },
+            std::make_integer_sequence<int, Ring::kPeriod>{});
+  each_of([&](auto at) __attribute__((always_inline)) {
+    if (c0 + decltype(at)::value >= chunks) return false;  // uniform
+    chunk(at);
+    return true;
+  }, std::make_integer_sequence<int, Ring::kPeriod - 1>{});
 }
 
 // Rows of the wave's 64 outputs x 32 rows in LDS, before they leave in whole rows.
 constexpr int kOutStride = 72;  // bf16 per row: 64 and padding
 
-template <bool kNv>
+template <bool kNv, int kMax>
 __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs a) {
-  __shared__ __attribute__((aligned(16))) u32x4 arena[kArenaSlots];
+  using Ring = Rings<kMax>;
+  __shared__ __attribute__((aligned(16))) u32x4 x0[Ring::kXStage], x1[Ring::kXStage], x2[Ring::kXStage];
+  __shared__ __attribute__((aligned(16))) u32x4 w0[Ring::kWStage], w1[Ring::kWStage];
   const int n_tiles = (a.N + kTileN - 1) / kTileN;
   int ti, nt;
   if (!map_tile(a, a.tile_rows, n_tiles, ti, nt)) return;  // uniform per block
@@ -704,13 +698,23 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs a) {
   const uint32_t shift = (uint32_t)((uintptr_t)sp & 3u);
   const auto rs = buffer(sp - shift, (shift + (uint32_t)nrows * kscales + 3u) & ~3u);
 
-  f32x16 acc[2][4] = {};
+  f32x16 acc[2][kMax] = {};
   const int live = (t.rows + 31) >> 5;
   const bool work = n0 + wave * 64 < N;  // uniform: a wave past N only loads its share
-  if (live == 4) tile_chunks<kNv, 4>(acc, arena, rx, rw, rs, K, shift, kscales, wave, work);
-  else if (live == 3) tile_chunks<kNv, 3>(acc, arena, rx, rw, rs, K, shift, kscales, wave, work);
-  else if (live == 2) tile_chunks<kNv, 2>(acc, arena, rx, rw, rs, K, shift, kscales, wave, work);
-  else tile_chunks<kNv, 1>(acc, arena, rx, rw, rs, K, shift, kscales, wave, work);
+  if constexpr (kMax > 2) {
+    u32x4* const xst[] = {x0, x1, x2};
+    u32x4* const wst[] = {w0, w1};
+    if (live == 4) tile_chunks<kNv, 4, kMax>(acc, xst, wst, rx, rw, rs, K, shift, kscales, wave, work);
+    else if (live == 3) tile_chunks<kNv, 3, kMax>(acc, xst, wst, rx, rw, rs, K, shift, kscales, wave, work);
+    else if (live == 2) tile_chunks<kNv, 2, kMax>(acc, xst, wst, rx, rw, rs, K, shift, kscales, wave, work);
+    else tile_chunks<kNv, 1, kMax>(acc, xst, wst, rx, rw, rs, K, shift, kscales, wave, work);
+  } else {
+    __shared__ __attribute__((aligned(16))) u32x4 x3[Ring::kXStage], w2[Ring::kWStage];
+    u32x4* const xst[] = {x0, x1, x2, x3};
+    u32x4* const wst[] = {w0, w1, w2};
+    if (live == 2) tile_chunks<kNv, 2, kMax>(acc, xst, wst, rx, rw, rs, K, shift, kscales, wave, work);
+    else tile_chunks<kNv, 1, kMax>(acc, xst, wst, rx, rw, rs, K, shift, kscales, wave, work);
+  }
 
   // lane (row lane & 31 of the block, half): features 8i + 4 half .. + 3 in acc[.][.][4i ..]
   mxgemm::wait_loads_then_barrier<0>();  // no load still writes LDS, no wave still reads it
@@ -725,9 +729,10 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs a) {
       const int n = min(nw + rb * 32 + 8 * (i >> 2) + 4 * half + (i & 3), N - 1);
       bias[rb][i] = a.bias != nullptr ? mx::bf16_to_f32(a.bias[(size_t)t.e * N + n]) : 0.f;
     }
-  uint16_t* out = reinterpret_cast<uint16_t*>(arena) + wave * 32 * kOutStride;
+  static_assert(2 * 32 * kOutStride * sizeof(uint16_t) <= sizeof(w0), "two waves' rows fit in a stage");
+  uint16_t* out = reinterpret_cast<uint16_t*>(wave < 2 ? w0 : w1) + (wave & 1) * 32 * kOutStride;
 #pragma unroll
-  for (int cb = 0; cb < 4; ++cb) {
+  for (int cb = 0; cb < kMax; ++cb) {
     if (cb >= live) break;
 #pragma unroll
     for (int rb = 0; rb < 2; ++rb)
@@ -1097,7 +1102,9 @@ hipError_t linear(LinearArgs a, hipStream_t stream) {
   if (!plan.pays) return launch_few<kNv>(a, stream);
   a.tile_rows = plan.rows;
   a.max_tiles = max_tiles(a, plan.rows);
-  linear_tile_kernel<kNv><<<grid_of(a.max_tiles, n_tiles), 256, 0, stream>>>(a);
+  const dim3 tile_grid = grid_of(a.max_tiles, n_tiles);
+  if (plan.rows > 64) linear_tile_kernel<kNv, 4><<<tile_grid, 256, 0, stream>>>(a);
+  else linear_tile_kernel<kNv, 2><<<tile_grid, 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
