@@ -531,8 +531,6 @@ struct ScaleBytes {
 // read may touch, so with one array and a stage counted at run time it waited
 // for all loads in flight before each chunk.
 constexpr int kTileRows = 128, kTileN = 256;
-constexpr int kXSlots = kTileRows * 8, kWSlots = kTileN * 2, kStageSlots = kXSlots + kWSlots;
-constexpr int kStages = 3;
 
 __device__ __forceinline__ int swizzle(int row) { return (row ^ (row >> 3)) & 7; }
 
@@ -772,11 +770,21 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs a) {
 // written one chunk ahead from bytes loaded one chunk before that.
 constexpr int kBackK = 256;
 
-template <bool kNv, int kLive, bool kAligned>
-__device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][4], u32x4* arena, uint16_t* table,
+// The ring of a kernel for up to kMax blocks of 32 rows: as many stages as
+// leave two blocks a CU.
+template <int kMax>
+struct BackRing {
+  static constexpr int kStages = kMax > 2 ? 3 : 4;
+  static constexpr int kDStage = kMax * 256, kWStage = 512;  // 16-byte slots
+};
+
+template <bool kNv, int kLive, int kMax, bool kAligned>
+__device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][kMax], u32x4* const (&dst)[BackRing<kMax>::kStages],
+                                                u32x4* const (&wst)[BackRing<kMax>::kStages], uint16_t* table,
                                                 const __amdgpu_buffer_rsrc_t& rd, const uint16_t* dy,
                                                 const __amdgpu_buffer_rsrc_t& rw, const __amdgpu_buffer_rsrc_t& rs,
                                                 int rows, int K, int N, int k0, int wave, bool work) {
+  constexpr int kStages = BackRing<kMax>::kStages;
   const int t = threadIdx.x, lane = t & 63, half = lane >> 5, lrow = lane & 31, mg = (lane >> 4) & 1, c16 = lane & 15;
   const int chunks = (N + 63) >> 6, kscales = kNv ? K >> 4 : K >> 5;
   constexpr int kGroups = kNv ? 16 : 8;  // of the block's 256 k
@@ -786,26 +794,31 @@ __device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][4], u32x4* aren
   // weight rows pr, pr + 32: the swizzle of the code pieces is the row's low bits
   const uint32_t woff = (uint32_t)pr * (K >> 1) + (k0 >> 1) + 16 * (pc ^ (pr & 7));
   // dy rows that start at a dword (N even) travel by the load unit, others through registers
-  constexpr int kLoads = kAligned ? 6 : 2;
-  u32x4 dreg[4];
-  auto load_dy = [&](int c) {
+  constexpr int kLoads = kAligned ? 2 + kLive : 2;
+  u32x4 dreg[kLive];
+  auto load_dy = [&](int c) __attribute__((always_inline)) {
     c = min(c, chunks - 1);
     const int n = 64 * c + 8 * part;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kLive; ++k) {
       const uint16_t* row = dy + (size_t)min(pr + 32 * k, rows - 1) * N;
       dreg[k] = load_dy8<false>(rd, row, 0, n, N, 64 * c + 64 <= N);
     }
   };
-  auto store_dy = [&](int st) {
+  auto store_dy = [&](u32x4* st) __attribute__((always_inline)) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) arena[st * kStageSlots + t + k * 256] = dreg[k];
+    for (int k = 0; k < kLive; ++k) st[t + k * 256] = dreg[k];
   };
-  auto issue = [&](int c, int st, int k) {
+  auto issue = [&](int c, u32x4* d, u32x4* w) __attribute__((always_inline)) {
     c = min(c, chunks - 1);
-    u32x4* dst = arena + st * kStageSlots + wave * 64;
-    if (k < 2) load_lds16(rw, dst + kXSlots + k * 256, woff + (uint32_t)(64 * c + 32 * k) * (K >> 1));
-    else load_lds16(rd, dst + (k - 2) * 256, doff + (uint32_t)((k - 2) * 32) * N * 2 + c * 128);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      load_lds16(rw, w + wave * 64 + k * 256, woff + (uint32_t)(64 * c + 32 * k) * (K >> 1));
+    if constexpr (kAligned) {
+#pragma unroll
+      for (int k = 0; k < kLive; ++k)
+        load_lds16(rd, d + wave * 64 + k * 256, doff + (uint32_t)(k * 32) * N * 2 + c * 128);
+    }
   };
   // scales: thread -> row t / 4 of the chunk, a quarter of its groups
   const int sn = t >> 2, sq = t & 3;
@@ -840,15 +853,16 @@ __device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][4], u32x4* aren
   load_scales(0);
   if (!kAligned) {
     load_dy(0);
-    store_dy(0);
+    store_dy(dst[0]);
   }
   store_scales(0);
   load_scales(1);
   if (!kAligned) load_dy(1);
 #pragma unroll
-  for (int k = 0; k < kLoads; ++k) issue(0, 0, k);
-#pragma unroll
-  for (int k = 0; k < kLoads; ++k) issue(1, 1, k);
+  for (int c = 0; c < kStages - 1; ++c) {
+    __builtin_amdgcn_sched_barrier(0);  // the waits count on this order
+    issue(c, dst[c], wst[c]);
+  }
 
   int boff[4];
 #pragma unroll
@@ -858,25 +872,31 @@ __device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][4], u32x4* aren
   const int aoff = (8 * half + ai) * 128 + (((wave * 2 + mg) ^ ai) * 16) + 8 * (c16 & 1);
   const int soff = (kNv ? wave * 4 + mg * 2 + (c16 >> 3) : wave * 2 + mg) * 64 + 8 * half;
 
-  int st = 0;
-  for (int c = 0; c < chunks; ++c) {
-    const int nst = st == 0 ? 2 : st - 1, st1 = st == 2 ? 0 : st + 1;
-    mxgemm::wait_loads_then_barrier<kLoads>();
+  int c0 = 0;
+  auto chunk = [&](auto at) __attribute__((always_inline)) {
+    constexpr int p = decltype(at)::value;
+    const int c = c0 + p;
+    mxgemm::wait_loads_then_barrier<(kStages - 2) * kLoads>();
     // the next chunk's scales (and unaligned dy) into LDS, the one's after that on their way
     store_scales(c + 1);
     load_scales(c + 2);
     if (!kAligned) {
-      store_dy(st1);
+      store_dy(dst[(p + 1) % kStages]);
       load_dy(c + 2);
     }
-    if (!work) {
-#pragma unroll
-      for (int k = 0; k < kLoads; ++k) issue(c + 2, nst, k);
-      st = st1;
-      continue;
+    __builtin_amdgcn_sched_barrier(0);
+    issue(c + kStages - 1, dst[(p + kStages - 1) % kStages], wst[(p + kStages - 1) % kStages]);
+    if (kAligned && 64 * c + 64 > N) {  // uniform: dy past N, the next row's, becomes zeros as the weights there are
+      uint16_t* stage = reinterpret_cast<uint16_t*>(dst[p]);
+      for (int i = t; i < kLive * 32 * 64; i += 256) {
+        const int r = i >> 6, col = i & 63;
+        if (64 * c + col >= N) stage[r * 64 + 8 * ((col >> 3) ^ swizzle(r & 31)) + (col & 7)] = 0;
+      }
+      mxgemm::lds_reads_then_barrier();
     }
-    const u32x4* base = arena + st * kStageSlots;
-    const uint8_t* codes = reinterpret_cast<const uint8_t*>(base + kXSlots) + aoff;
+    if (!work) return;
+    const u32x4* base = dst[p];
+    const uint8_t* codes = reinterpret_cast<const uint8_t*>(wst[p]) + aoff;
     const uint16_t* sc = table + (c & 1) * kGroups * 64 + soff;
     u32x4 b[4][kLive], sv[4];
     i32x2 w[4];
@@ -886,23 +906,6 @@ __device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][4], u32x4* aren
       sv[s] = *reinterpret_cast<const u32x4*>(sc + 16 * s);
 #pragma unroll
       for (int cb = 0; cb < kLive; ++cb) b[s][cb] = base[boff[s] + cb * 256];
-    }
-    if (64 * c + 64 > N) {  // rows past N: zero weights times zero dy (dy through registers came with its zeros)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int left = N - (64 * c + 16 * s + 8 * half);  // of this lane's eight n
-        if (left <= 0) w[s] = i32x2{0, 0};
-        else if (left < 8) {
-          w[s][0] &= left < 4 ? (int)((1u << (8 * left)) - 1u) : -1;
-          w[s][1] &= left > 4 ? (int)((1u << (8 * (left - 4))) - 1u) : 0;
-        }
-#pragma unroll
-        for (int cb = 0; cb < kLive; ++cb)
-          if (kAligned) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b[s][cb][i] = 2 * i < left ? b[s][cb][i] : 0u;
-          }
-      }
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -931,18 +934,24 @@ __device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][4], u32x4* aren
         for (int e = 0; e < 2; ++e)
           acc[e][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(mx::as_bf16x8(op[e]), mx::as_bf16x8(b[s][cb]),
                                                                acc[e][cb], 0, 0, 0);
-      if (2 * s < kLoads) {
-        issue(c + 2, nst, 2 * s);
-        issue(c + 2, nst, 2 * s + 1);
-      }
     }
-    st = st1;
-  }
+  };
+  // whole periods without an exit, as above
+  for (; c0 + kStages <= chunks; c0 += kStages)
+    each_of([&](auto at) __attribute__((always_inline)) { return chunk(at), true; },
+            std::make_integer_sequence<int, kStages>{});
+  each_of([&](auto at) __attribute__((always_inline)) {
+    if (c0 + decltype(at)::value >= chunks) return false;  // uniform
+    chunk(at);
+    return true;
+  }, std::make_integer_sequence<int, kStages - 1>{});
 }
 
-template <bool kNv, bool kAligned>
+template <bool kNv, int kMax, bool kAligned>
 __global__ __launch_bounds__(256, 2) void linear_backward_tile_kernel(LinearArgs a) {
-  __shared__ __attribute__((aligned(16))) u32x4 arena[kStages * kStageSlots];
+  using Ring = BackRing<kMax>;
+  __shared__ __attribute__((aligned(16))) u32x4 d0[Ring::kDStage], d1[Ring::kDStage], d2[Ring::kDStage];
+  __shared__ __attribute__((aligned(16))) u32x4 w0[Ring::kWStage], w1[Ring::kWStage], w2[Ring::kWStage];
   __shared__ __attribute__((aligned(16))) uint16_t table[2 * (kNv ? 16 : 8) * 64];
   const int k_tiles = (a.K + kBackK - 1) / kBackK;
   int ti, kt;
@@ -957,13 +966,29 @@ __global__ __launch_bounds__(256, 2) void linear_backward_tile_kernel(LinearArgs
   const auto rw = buffer(a.blocks + (size_t)t.e * N * (K >> 1), (uint32_t)N * (K >> 1));
   const auto rs = buffer(a.scales + (size_t)t.e * N * kscales, (uint32_t)N * kscales);
 
-  f32x16 acc[2][4] = {};
+  f32x16 acc[2][kMax] = {};
   const int live = (t.rows + 31) >> 5;
   const bool work = k0 + wave * 64 < K;  // uniform: a wave past K only loads its share
-  if (live == 4) backward_chunks<kNv, 4, kAligned>(acc, arena, table, rd, dy, rw, rs, t.rows, K, N, k0, wave, work);
-  else if (live == 3) backward_chunks<kNv, 3, kAligned>(acc, arena, table, rd, dy, rw, rs, t.rows, K, N, k0, wave, work);
-  else if (live == 2) backward_chunks<kNv, 2, kAligned>(acc, arena, table, rd, dy, rw, rs, t.rows, K, N, k0, wave, work);
-  else backward_chunks<kNv, 1, kAligned>(acc, arena, table, rd, dy, rw, rs, t.rows, K, N, k0, wave, work);
+  if constexpr (kMax > 2) {
+    u32x4* const dst[] = {d0, d1, d2};
+    u32x4* const wst[] = {w0, w1, w2};
+    if (live == 4)
+      backward_chunks<kNv, 4, kMax, kAligned>(acc, dst, wst, table, rd, dy, rw, rs, t.rows, K, N, k0, wave, work);
+    else if (live == 3)
+      backward_chunks<kNv, 3, kMax, kAligned>(acc, dst, wst, table, rd, dy, rw, rs, t.rows, K, N, k0, wave, work);
+    else if (live == 2)
+      backward_chunks<kNv, 2, kMax, kAligned>(acc, dst, wst, table, rd, dy, rw, rs, t.rows, K, N, k0, wave, work);
+    else
+      backward_chunks<kNv, 1, kMax, kAligned>(acc, dst, wst, table, rd, dy, rw, rs, t.rows, K, N, k0, wave, work);
+  } else {
+    __shared__ __attribute__((aligned(16))) u32x4 d3[Ring::kDStage], w3[Ring::kWStage];
+    u32x4* const dst[] = {d0, d1, d2, d3};
+    u32x4* const wst[] = {w0, w1, w2, w3};
+    if (live == 2)
+      backward_chunks<kNv, 2, kMax, kAligned>(acc, dst, wst, table, rd, dy, rw, rs, t.rows, K, N, k0, wave, work);
+    else
+      backward_chunks<kNv, 1, kMax, kAligned>(acc, dst, wst, table, rd, dy, rw, rs, t.rows, K, N, k0, wave, work);
+  }
 
   // lane (row lane & 31 of the block, half): k = 32 (b / 2) + 16 (b & 1) + 8 half + 2 r + e of the wave's 64 in
   // acc[e][.][4b + r]
@@ -971,9 +996,10 @@ __global__ __launch_bounds__(256, 2) void linear_backward_tile_kernel(LinearArgs
   if (!work) return;                     // no barrier follows
   const int kw = k0 + wave * 64, half = lane >> 5, lrow = lane & 31;
   const float s2 = kNv ? a.scale2[t.e] : 1.0f;
-  uint16_t* out = reinterpret_cast<uint16_t*>(arena) + wave * 32 * kOutStride;
+  static_assert(32 * kOutStride * sizeof(uint16_t) <= sizeof(w0), "a wave's rows fit in a stage");
+  uint16_t* out = reinterpret_cast<uint16_t*>(wave == 0 ? w0 : wave == 1 ? w1 : wave == 2 ? w2 : d0);
 #pragma unroll
-  for (int cb = 0; cb < 4; ++cb) {
+  for (int cb = 0; cb < kMax; ++cb) {
     if (cb >= live) break;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -1113,11 +1139,13 @@ hipError_t linear_backward(LinearArgs a, hipStream_t stream) {
   const int64_t k_tiles = (a.K + kBackK - 1) / kBackK;
   const TilePlan plan = plan_tiles(a, k_tiles, (a.N + 63) / 64, kNv, 1.1, 1.9e6, 6e6);
   if (plan.pays) {
-    a.tile_rows = plan.rows;
-    a.max_tiles = max_tiles(a, plan.rows);
+    // odd N: dy through registers, which 128 rows leave none of
+    a.tile_rows = a.N % 2 == 0 || plan.rows < 64 ? plan.rows : 64;
+    a.max_tiles = max_tiles(a, a.tile_rows);
     const dim3 tile_grid = grid_of(a.max_tiles, k_tiles);
-    if (a.N % 2 == 0) linear_backward_tile_kernel<kNv, true><<<tile_grid, 256, 0, stream>>>(a);
-    else linear_backward_tile_kernel<kNv, false><<<tile_grid, 256, 0, stream>>>(a);
+    if (a.tile_rows > 64) linear_backward_tile_kernel<kNv, 4, true><<<tile_grid, 256, 0, stream>>>(a);
+    else if (a.N % 2 == 0) linear_backward_tile_kernel<kNv, 2, true><<<tile_grid, 256, 0, stream>>>(a);
+    else linear_backward_tile_kernel<kNv, 2, false><<<tile_grid, 256, 0, stream>>>(a);
     return hipGetLastError();
   }
   a.max_tiles = max_tiles(a, kFewRows);
