@@ -391,14 +391,18 @@ __global__ __launch_bounds__(512, 2) void linear_one_kernel(LinearArgs a) {
 }
 
 // dx for row tiles of at most 16 rows.  The sum runs over weight rows, so the
-// MFMA's A operand is the transposed weights: lane (m, q) loads the dword of
-// eight codes k = 8m .. 8m+7 of eight weight rows n = 8q .. 8q+7, converts
-// each to four pairs of k, and exchanges halves between the rows of a pair
-// (v_perm) into eight operands of eight n, one for each k: operand j
-// multiplies with k = 8m + j as its row m.  Waves split N and add their sums
-// in LDS in wave order.  Bound: as above, the weights' bytes.
-constexpr int kFewK = 128;       // k of a block
-constexpr int kRedStride = 36;   // floats per lane in LDS (32 and padding)
+// MFMA's A operand is the transposed weights: lane (m, q) loads kCodes codes k
+// = kCodes m .. of eight weight rows n = 8q .. 8q+7, converts each to pairs of
+// k, and exchanges halves between the rows of a pair (v_perm) into kCodes
+// operands of eight n, one for each k: operand j multiplies with k = kCodes m
+// + j as its row m.  Waves split N and add their sums in LDS in wave order.
+// Bound: the weights' bytes, at 1.9 TB/s (128 rows over 32 experts, 2880 x
+// 2880: 74 us, where tiles take 41), and for a small matrix the latency of a
+// pass (300 rows over 8 experts, N = 1000, K = 736: 8.1 us MXFP4, 9.1 NVFP4, of
+// which an empty launch is 2.2).  Not better: codes through LDS by the load
+// unit, a quarter of the load instructions (9.3 and 10.2 us); 16 waves a block
+// (8.6 and 9.6 us); row tiles of 32 (9.3 and 11.4 us).
+constexpr int red_stride(int codes) { return 4 * codes + 4; }  // floats per lane in LDS, with padding
 
 // Eight consecutive dy values of a row from element n on, zeros past N.
 // kAligned: N is even, so that every row starts at a dword.
@@ -425,9 +429,10 @@ __device__ __forceinline__ u32x4 load_dy8(const __amdgpu_buffer_rsrc_t& r, const
   }
 }
 
-template <bool kNv, bool kAligned>
+template <bool kNv, bool kAligned, int kCodes>
 __global__ __launch_bounds__(512) void linear_backward_few_kernel(LinearArgs a) {
   extern __shared__ float redf[];
+  constexpr int kFewK = 16 * kCodes, kRedStride = red_stride(kCodes);
   const int k_chunks = (a.K + kFewK - 1) / kFewK;
   int ti, kc;
   if (!map_block(a.max_tiles, k_chunks, ti, kc)) return;  // uniform per block
@@ -442,9 +447,9 @@ __global__ __launch_bounds__(512) void linear_backward_few_kernel(LinearArgs a) 
   const uint16_t* dy0 = a.x + (size_t)t.row0 * N;
   const auto rd = buffer(dy0, (uint32_t)t.rows * N * 2);
   const int row = min(m, t.rows - 1);  // columns past the tile's rows are dropped
-  const uint32_t wcol = (k0 >> 1) + 4 * m, scol = kNv ? (k0 >> 4) + (m >> 1) : (k0 >> 5) + (m >> 2);
+  const uint32_t wcol = (k0 + kCodes * m) >> 1, scol = (k0 + kCodes * m) >> (kNv ? 4 : 5);
 
-  f32x4 acc[8] = {};
+  f32x4 acc[kCodes] = {};
   const int steps = (N + 31) >> 5;
   for (int s0 = wave; s0 < steps; s0 += 2 * waves) {
     uint32_t w[2][8], sc[2][8];
@@ -455,7 +460,10 @@ __global__ __launch_bounds__(512) void linear_backward_few_kernel(LinearArgs a) 
       const int n = 32 * s + 8 * q;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        w[u][i] = __builtin_amdgcn_raw_buffer_load_b32(rw, n + i < N ? (uint32_t)(n + i) * (K >> 1) + wcol : kDead, 0, 0);
+        const uint32_t o = n + i < N ? (uint32_t)(n + i) * (K >> 1) + wcol : kDead;
+        if constexpr (kCodes == 8) w[u][i] = __builtin_amdgcn_raw_buffer_load_b32(rw, o, 0, 0);
+        else if constexpr (kCodes == 4) w[u][i] = __builtin_amdgcn_raw_buffer_load_b16(rw, o, 0, 0);
+        else w[u][i] = __builtin_amdgcn_raw_buffer_load_b8(rw, o, 0, 0);
         sc[u][i] = __builtin_amdgcn_raw_buffer_load_b8(rs, n + i < N ? (uint32_t)(n + i) * kscales + scol : kDead, 0, 0);
       }
       d[u] = load_dy8<kAligned>(rd, dy0 + (size_t)row * N, (uint32_t)row * N * 2, n, N, 32 * s + 32 <= N);
@@ -469,7 +477,7 @@ __global__ __launch_bounds__(512) void linear_backward_few_kernel(LinearArgs a) 
         r[i] = kNv ? mx::fp4x8_to_bf16x8_any_scale(w[u][i], mx::e4m3x2_operands(sc[u][i]).x)
                    : mx::fp4x8_to_bf16x8(w[u][i], mx::e8m0_operand(sc[u][i]));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < kCodes; ++j) {
         u32x4 op;
 #pragma unroll
         for (int p = 0; p < 4; ++p)
@@ -478,22 +486,23 @@ __global__ __launch_bounds__(512) void linear_backward_few_kernel(LinearArgs a) 
       }
     }
   }
-  // lane (row m of the tile, q) holds k = k0 + 32q + 8r + j in acc[j][r]
+  // lane (row m of the tile, q) holds k = k0 + 4 kCodes q + kCodes r + j in acc[j][r]
   float* mine = redf + (wave * 64 + lane) * kRedStride;
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+  for (int i = 0; i < kCodes; ++i) {
+    f32x4 v;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<f32x4*>(mine + 8 * r + 4 * h) =
-          f32x4{acc[4 * h][r], acc[4 * h + 1][r], acc[4 * h + 2][r], acc[4 * h + 3][r]};
+    for (int c = 0; c < 4; ++c) v[c] = acc[(4 * i + c) % kCodes][(4 * i + c) / kCodes];
+    *reinterpret_cast<f32x4*>(mine + 4 * i) = v;
+  }
   __syncthreads();
   const float s2 = kNv ? a.scale2[t.e] : 1.0f;
-  for (int i = threadIdx.x; i < 64 * 8; i += blockDim.x) {
-    const int l = i >> 3, piece = i & 7;
+  for (int i = threadIdx.x; i < 64 * kCodes; i += blockDim.x) {
+    const int l = i / kCodes, piece = i % kCodes;
     f32x4 v = *reinterpret_cast<const f32x4*>(redf + l * kRedStride + 4 * piece);
     for (int u = 1; u < waves; ++u)
       v += *reinterpret_cast<const f32x4*>(redf + (u * 64 + l) * kRedStride + 4 * piece);
-    const int k = k0 + 32 * (l >> 4) + 4 * piece, r = l & 15;
+    const int k = k0 + 4 * kCodes * (l >> 4) + 4 * piece, r = l & 15;
     if (r < t.rows && k < K) *reinterpret_cast<uint2*>(a.y + (size_t)(t.row0 + r) * K + k) = mxgemm::pack_bf16x4(v * s2);
   }
 }
@@ -1034,32 +1043,49 @@ dim3 grid_of(int64_t tiles, int64_t chunks) {
 }
 
 // Whether the tiles of up to 128 rows pay, and their rows: a choice by the
-// sizes alone, from times measured at N, K = 736 .. 2880, 1 to 32 experts and
-// 4 to 256 rows of an expert.
+// sizes alone, from times measured at N, K = 736 .. 2880, 1 to 128 experts
+// and 4 to 16384 rows.
 //
-// A tile block takes a fixed time for each chunk of its loop, whatever few
-// rows it has (us: 0.62, 0.72, 0.9, 1.05 with 1 to 4 live row blocks; the
-// gradient a tenth more), two blocks a CU at once.  So tiles are halved while
-// all blocks still run at once: 1024 dense rows, 2880 x 2880: 47 us as 96
-// blocks of 128 rows, 32 us as 384 of 32.
+// A tile block takes a fixed time for each chunk of its loop, by its rows and
+// by whether it has its CU to itself or shares it with another.  So few rows
+// take small tiles, for more blocks, and many take large ones, which read
+// fewer bytes of LDS for a product (2880 x 2880, tiles of 128, 64 and 32 rows:
+// 512 dense rows 42, 25 and 19 us; 1024 rows 43, 27 and 30; 8192 rows 120, 136
+// and 174; 16384 rows over 128 experts 365, 374 and 494).
 //
 // The 16-row kernels read the weights once for each 16 rows: from HBM the
 // first time, at `cold` bytes/us, from the caches then, at `hot`.
+struct TileCost {  // us of a chunk of tiles of 32, 64 and 128 rows
+  double alone[3], shared[3];
+};
+constexpr TileCost kForward{{0.32, 0.49, 0.88}, {0.57, 0.83, 1.43}};
+constexpr TileCost kBackward{{0.53, 0.64, 1.02}, {0.78, 1.0, 1.58}};
 struct TilePlan {
   bool pays;
   int rows;
 };
-TilePlan plan_tiles(LinearArgs a, int64_t col_tiles, int chunks, bool nv, double chunk_cost, double cold, double hot) {
-  TilePlan p{false, kTileRows};
-  const int64_t slots = 2 * mxfp4moe::device_cu_count();
-  while (p.rows > 32 && max_tiles(a, p.rows / 2) * col_tiles <= slots) p.rows /= 2;
-  const double chunk_us[5] = {0, 0.62, 0.72, 0.9, 1.05};
-  // half of the experts' last tiles, in the mean
-  const int64_t experts = a.E < a.R ? a.E : a.R;
-  const double blocks = ((double)a.R / p.rows + 0.5 * experts) * col_tiles;
-  const double rounds = blocks > slots ? blocks / slots : 1.0;
-  const double bytes = (double)a.N * a.K * (nv ? 0.5625 : 0.53125);
-  const double tile_us = 4 + rounds * chunks * chunk_cost * chunk_us[p.rows / 32];
+TilePlan plan_tiles(const LinearArgs& a, int most_rows, int64_t col_tiles, int chunks, bool nv, const TileCost& cost,
+                    double cold, double hot) {
+  const double cus = mxfp4moe::device_cu_count();
+  const double experts = a.E < a.R ? a.E : a.R, bytes = (double)a.N * a.K * (nv ? 0.5625 : 0.53125);
+  TilePlan p{false, 0};
+  double best = 0;
+  for (int r = 0; r < 3 && 32 << r <= most_rows; ++r) {
+    // half of the experts' last tiles, in the mean, and those half full
+    const double full = (double)a.R / (32 << r), tiles = a.offsets != nullptr ? full + 0.5 * experts : max_tiles(a, 32 << r);
+    const double load = tiles * col_tiles / cus;  // blocks of a CU
+    double chunk;
+    if (load > 4) {
+      chunk = (full * cost.shared[r] + (tiles - full) * cost.shared[0]) * col_tiles / (2 * cus);
+    } else {  // in rounds of two
+      const int rounds = (int)(load / 2);
+      const double rest = load - 2 * rounds;
+      chunk = rounds * cost.shared[r] + (rest > 1 ? cost.shared[r] : rest > 0 ? cost.alone[r] : 0);
+    }
+    if (p.rows == 0 || chunk < best) p.rows = 32 << r, best = chunk;
+  }
+  const double stream_us = experts * bytes / 3.5e6;  // the weights from HBM
+  const double tile_us = 4 + (best * chunks > stream_us ? best * chunks : stream_us);
   const double reads = (double)a.R / kFewRows + 0.5 * experts;  // of one expert's weights
   const double few_us = 4 + experts * bytes / cold + (reads > experts ? reads - experts : 0) * bytes / hot;
   p.pays = tile_us < few_us;
@@ -1124,7 +1150,7 @@ hipError_t linear(LinearArgs a, hipStream_t stream) {
     if (dense ? a.R <= 4 : a.R <= kMeanOf4 * a.E) return launch_one<kNv, 1>(a, stream);
     if (dense ? a.R <= 8 : a.R <= kMeanOf8 * a.E) return launch_one<kNv, 2>(a, stream);
   }
-  const TilePlan plan = plan_tiles(a, n_tiles, (a.K + 63) / 64, kNv, 1.0, 2.9e6, 3.7e6);
+  const TilePlan plan = plan_tiles(a, kTileRows, n_tiles, (a.K + 63) / 64, kNv, kForward, 2.9e6, 3.7e6);
   if (!plan.pays) return launch_few<kNv>(a, stream);
   a.tile_rows = plan.rows;
   a.max_tiles = max_tiles(a, plan.rows);
@@ -1134,28 +1160,37 @@ hipError_t linear(LinearArgs a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <bool kNv, int kCodes>
+hipError_t launch_backward_few(LinearArgs a, hipStream_t stream) {
+  a.max_tiles = max_tiles(a, kFewRows);
+  const int steps = (a.N + 31) / 32, waves = steps < 8 ? steps : 8;
+  const dim3 grid = grid_of(a.max_tiles, (a.K + 16 * kCodes - 1) / (16 * kCodes));
+  const size_t lds = (size_t)waves * 64 * red_stride(kCodes) * sizeof(float);
+  if (a.N % 2 == 0) linear_backward_few_kernel<kNv, true, kCodes><<<grid, waves * 64, lds, stream>>>(a);
+  else linear_backward_few_kernel<kNv, false, kCodes><<<grid, waves * 64, lds, stream>>>(a);
+  return hipGetLastError();
+}
+
 template <bool kNv>
 hipError_t linear_backward(LinearArgs a, hipStream_t stream) {
   const int64_t k_tiles = (a.K + kBackK - 1) / kBackK;
-  const TilePlan plan = plan_tiles(a, k_tiles, (a.N + 63) / 64, kNv, 1.1, 1.9e6, 6e6);
+  // odd N: dy through registers, which 128 rows leave none of
+  const int most = a.N % 2 == 0 ? kTileRows : 64;
+  const TilePlan plan = plan_tiles(a, most, k_tiles, (a.N + 63) / 64, kNv, kBackward, 1.9e6, 5e6);
   if (plan.pays) {
-    // odd N: dy through registers, which 128 rows leave none of
-    a.tile_rows = a.N % 2 == 0 || plan.rows < 64 ? plan.rows : 64;
-    a.max_tiles = max_tiles(a, a.tile_rows);
+    a.tile_rows = plan.rows;
+    a.max_tiles = max_tiles(a, plan.rows);
     const dim3 tile_grid = grid_of(a.max_tiles, k_tiles);
     if (a.tile_rows > 64) linear_backward_tile_kernel<kNv, 4, true><<<tile_grid, 256, 0, stream>>>(a);
     else if (a.N % 2 == 0) linear_backward_tile_kernel<kNv, 2, true><<<tile_grid, 256, 0, stream>>>(a);
     else linear_backward_tile_kernel<kNv, 2, false><<<tile_grid, 256, 0, stream>>>(a);
     return hipGetLastError();
   }
-  a.max_tiles = max_tiles(a, kFewRows);
-  const int steps = (a.N + 31) / 32;
-  const int waves = steps < 8 ? steps : 8;
-  const dim3 grid = grid_of(a.max_tiles, (a.K + kFewK - 1) / kFewK);
-  const size_t lds = (size_t)waves * 64 * kRedStride * sizeof(float);
-  if (a.N % 2 == 0) linear_backward_few_kernel<kNv, true><<<grid, waves * 64, lds, stream>>>(a);
-  else linear_backward_few_kernel<kNv, false><<<grid, waves * 64, lds, stream>>>(a);
-  return hipGetLastError();
+  // 64 k a block instead of 128 while that leaves them a CU each (16 rows, 2880 x 2880, 24 or 45 blocks: 13.5 and 11 us;
+  // 48 or 92 blocks of N = 2880, K = 736: 16 and 12 us; 184 or 360 blocks: 13.6 and 18 us)
+  const int64_t blocks = (int64_t)max_tiles(a, kFewRows) * ((a.K + 127) / 128);
+  return 2 * blocks <= mxfp4moe::device_cu_count() ? launch_backward_few<kNv, 4>(a, stream)
+                                                   : launch_backward_few<kNv, 8>(a, stream);
 }
 
 LinearArgs args_of(const uint16_t* in, const uint8_t* blocks, const uint8_t* scales, const float* scale2,
