@@ -489,3 +489,42 @@ def test_layer_from_its_operators_and_its_gradients(gpu, fmt, T):
         rel = float((got.double().cpu() - want).norm() / want.norm())
         print(f"[layer] {fmt} T={T} {name}: {rel:.2e}", flush=True)
         assert rel <= 1e-2, (name, rel)
+
+
+# experts, rows of an expert on average, N, K: where each of the kernels and of its variants is taken, with loops over
+# K (the gradient: over N) that pass through every stage of a ring more than once and end in each of them
+VARIANTS = [
+    (16, 5, 100, 704), (32, 7, 530, 2112), (128, 7, 180, 2112), (32, 24, 2002, 800), (32, 24, 1998, 832),
+    (20, 70, 850, 1184), (6, 400, 1057, 1600), (5, 900, 834, 1504), (8, 37, 1001, 736), (3, 12, 2050, 96),
+    (128, 130, 1606, 1568),
+]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("E,mean,N,K", VARIANTS)
+def test_kernel_variants(gpu, fmt, E, mean, N, K):
+    counts = np.random.default_rng(E + N).poisson(mean, E)
+    counts[E // 3] = 0
+    w = Weights(fmt, E, N, K, seed=N + K)
+    check_both(gpu, w, int(counts.sum()) + 3, offsets_of(counts, 2), label=f"variants {fmt}")
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("E,mean,N,K", VARIANTS)
+def test_same_bits_every_time(gpu, fmt, E, mean, N, K):
+    """A product that read a stage before its loads were there would differ from call to call, most of all while
+    another one keeps the caches cold."""
+    counts = np.random.default_rng(E + K).poisson(mean, E)
+    w, other = Weights(fmt, E, N, K, seed=3), Weights(fmt, E, N, K, seed=4)
+    off = offsets_of(counts)
+    rng = np.random.default_rng(5)
+    R = int(counts.sum())
+    x, dy = bf16(rng, R, K), bf16(rng, R, N)
+    spill = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    y, dx = w.linear(gpu, x, None, off), w.backward(gpu, dy, off)
+    for i in range(12):
+        if i % 3 == 0:
+            spill.fill_(i)
+        other.linear(gpu, x, None, off), other.backward(gpu, dy, off)
+        assert torch.equal(w.linear(gpu, x, None, off), y)
+        assert torch.equal(w.backward(gpu, dy, off), dx)
