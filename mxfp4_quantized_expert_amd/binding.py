@@ -1,9 +1,10 @@
-"""ctypes binding of libmxfp4moe.so.
+"""Binding of libmxfp4moe.so.
 
 Argument marshalling only: dtype/device/shape checks, output allocation with
-torch, and the raw C call on torch's current HIP stream.  Every step of the
-computation runs in the library's HIP kernels; there is no other code path.
-The C ABI is declared in include/mxfp4moe.h.
+torch, and the raw C call on torch's current HIP stream, by ctypes or, for plain
+calls of the layer's separate operators, in one step of native code.  Every step
+of the computation runs in the library's HIP kernels; there is no other code
+path.  The C ABI is declared in include/mxfp4moe.h.
 """
 
 from __future__ import annotations
@@ -699,7 +700,8 @@ def moe_mxfp4_linear(x: torch.Tensor, blocks: torch.Tensor, scales: torch.Tensor
     """Rows times MXFP4 weights: y = x W^T (+ bias) for x [R, K] bfloat16.  Dense: blocks [N, K/2]
     and scales [N, K/32] uint8, bias [N] bfloat16.  Per expert: blocks [E, N, K/2], scales
     [E, N, K/32], bias [E, N] and expert_offsets [E + 1] int32 (expert e has the rows
-    [offsets[e], offsets[e + 1]); rows outside them keep what `out` held).  Returns y [R, N]."""
+    [offsets[e], offsets[e + 1]); rows outside them keep what `out` held, and without `out` hold
+    anything).  Returns y [R, N]."""
     if _host is not None and stream is None and out is None:
         got = _host.linear(False, 32, x, blocks, scales, None, bias, expert_offsets)
         if got is not None:  # None: not a plain call, or one to refuse

@@ -11,7 +11,7 @@
 // the weights are frozen, so the rows are all that has a gradient.
 //
 // A code times its scale is exact in bf16 (two significant bits for MXFP4,
-// at most five for NVFP4), so every product of the bf16 MFMA is exact and the
+// at most six for NVFP4), so every product of the bf16 MFMA is exact and the
 // sums are its fp32 accumulation; s2 and the bias follow in fp32 and the
 // result is rounded once.
 #include <type_traits>
@@ -152,7 +152,10 @@ __device__ __forceinline__ bool map_tile(const LinearArgs& a, int tm, int chunks
 // weight rows; x stays in registers for those kG row groups.  The partial
 // sums meet in LDS, added in wave order.  Loads past K, N or the tile's rows
 // return zero from the buffer's bounds.  Bound: the weights' bytes from HBM,
-// and for a single small matrix the latency of one pass.
+// at 2.9 TB/s (224 rows over 32 experts, 2880 x 2880: 56 us, where tiles take
+// 46), and for a single small matrix the latency of one pass (256 rows, N =
+// 1024, K = 736: 4.6 us, of which an empty launch is 2.2; 128 rows, 2880 x
+// 2880: 14.6 us, where tiles take 17.5).
 constexpr int kFewRows = 16;
 
 // Four consecutive outputs: s2 * v + bias, `n` of them in range (`whole`: always four, 8-byte aligned).
@@ -253,7 +256,10 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs a) {
 // lane block b keeps row group b of up to sixteen, which leave together.  A
 // block's waves split K where it exceeds one wave's units and add their sums
 // through LDS in wave order.  Row groups are dealt to the blocks in equal
-// contiguous ranges.
+// contiguous ranges, eight waves a CU.  13 of 32 NVFP4 experts, 5760 x 2880,
+// 16 rows: 28 us = 4.3 TB/s of 121 MB (16-row tiles: 47); one row, 2880 x
+// 4096: 5.7 us, of which an empty launch is 2.2; 128 rows over 32 experts, 2880
+// x 2880: 34 us (50).
 constexpr int kOneRows = 4;
 constexpr int kBatch = 16;  // row groups that leave together
 
@@ -533,12 +539,23 @@ struct ScaleBytes {
 // bytes in step s, and the x values of the same k.  x travels from global
 // memory into a ring of LDS stages of 64 k, the weights into one of stages of
 // 128 k, by the load unit (16 bytes a lane), later chunks on their way while
-// one is multiplied; one barrier a chunk.
+// one is multiplied; one barrier a chunk.  x rows are 128 bytes a stage, their
+// 16-byte pieces XOR-swizzled so that the 128-bit reads of consecutive rows
+// hit distinct banks; scale bytes go straight to registers, 24 of a row at a
+// time.  Two blocks a CU: one converts and waits while the other multiplies.
+// Token blocks of 32 without rows are neither read nor multiplied.  Bound: the
+// bf16 MFMA rate under the card's power limit.  16384 rows, 2880 x 2880: dense
+// 235 us = 1160 TFLOP/s, as a large library product reaches; over 128 experts
+// 365 us = 745 TFLOP/s, with tiles filled to 89 % and the weights from HBM (the
+// clock fell to 1.5 GHz there, 1.7 to 1.9 dense).  Few rows: 512, 2880 x 2880:
+// 19 us; 4096 over 128 experts: 171 us, the weights at 3.4 TB/s.
 //
 // The stages are arrays of their own and the loop is unrolled over the period
 // of both rings: the compiler waits for every load into an array that an LDS
 // read may touch, so with one array and a stage counted at run time it waited
-// for all loads in flight before each chunk.
+// for all loads in flight before each chunk (1024 rows 35 us instead of 30,
+// 4096 over 128 experts 193 instead of 172).  For the same reason loads are
+// issued outside the branch on `work`.
 constexpr int kTileRows = 128, kTileN = 256;
 
 __device__ __forceinline__ int swizzle(int row) { return (row ^ (row >> 3)) & 7; }
@@ -555,7 +572,9 @@ __device__ __forceinline__ bool each_of(F&& f, std::integer_sequence<int, kP...>
 
 // The rings of a kernel for up to kMax blocks of 32 rows: kX stages of x, kW
 // of the weights, 80 KB in all (two blocks a CU).  The fewer rows share the
-// weights, the more of them have to be on their way to keep HBM busy.
+// weights, the more of them have to be on their way to keep HBM busy.  Weight
+// stages hold 128 k because 64 bytes of a row at a time stream from HBM at 4.7
+// TB/s, 32 bytes at 3.3 (565 MB in this pattern, no arithmetic).
 template <int kMax>
 struct Rings {
   static constexpr int kX = kMax > 2 ? 3 : 4, kW = kMax > 2 ? 2 : 3;
@@ -774,9 +793,12 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs a) {
 // rows (ds_read_b64_tr_b8), and lane c gets byte c of the eight rows, i.e. k
 // = 2c and 2c + 1 of the group's 32 k for eight n.  Each byte is converted
 // with its row's scale and the halves of neighbouring rows are exchanged
-// (v_perm; NVFP4 rounds the pair itself) into an operand for the even and one
-// for the odd k.  The chunk's scales lie transposed in LDS as bf16 (exact),
-// written one chunk ahead from bytes loaded one chunk before that.
+// (v_perm; NVFP4 rounds the pair itself, exactly) into an operand for the even
+// and one for the odd k.  The chunk's scales lie transposed in LDS as bf16
+// (exact), written one chunk ahead from bytes loaded one chunk before that.
+// Bound: as the forward tiles.  16384 rows, 2880 x 2880: dense 254 us = 1070
+// TFLOP/s, over 128 experts 365 us = 745; odd N (2883; dy through registers, in
+// tiles of 64 rows) 461; 4096 rows over 128 experts 170 us.
 constexpr int kBackK = 256;
 
 // The ring of a kernel for up to kMax blocks of 32 rows: as many stages as

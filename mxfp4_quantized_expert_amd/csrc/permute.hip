@@ -99,7 +99,8 @@ __global__ __launch_bounds__(kThreads) void enter_pair_rows_kernel(const int32_t
 }
 
 // Small batches, one launch: rows[i] = x[sorted_pairs[i] / top_k], a piece to
-// a lane; the blocks before copy_block0 write pair_rows meanwhile.
+// a lane; the blocks before copy_block0 write pair_rows meanwhile.  Bound by
+// the launch: 4 tokens, top 4, 2880 bf16: 2.4 us.
 template <typename E, int kN>
 __global__ __launch_bounds__(kThreads) void permute_kernel(const E* __restrict__ x,
                                                            const int32_t* __restrict__ sorted_pairs,
@@ -164,8 +165,10 @@ __device__ __forceinline__ void clear_empty_rows(E* __restrict__ rows, const E* 
 }
 
 // Large batches, with pair_rows written before: a token's pieces are read once
-// and stored to its top_k rows; the blocks from zero_block0 on clear the rows
-// that hold no pair.
+// and stored to its top_k rows, past the caches; the blocks from zero_block0 on
+// clear the rows that hold no pair.  4096 tokens, top 4, 2880 bf16: 24 us = 4.9
+// TB/s of 118 MB (row by row, x read four times: 32 us; a copy of 1 GiB reaches
+// 5.2 TB/s).  Two, three or six pieces a lane were slower (37 to 40 us).
 template <typename E, int kN>
 __global__ __launch_bounds__(kThreads) void permute_by_token_kernel(const E* __restrict__ x,
                                                                     const int32_t* __restrict__ sorted_pairs,
@@ -196,7 +199,9 @@ __global__ __launch_bounds__(kThreads) void permute_by_token_kernel(const E* __r
   }
 }
 
-// y[t] = sum_j w[t, j] rows[pair_rows[t, j]] (w == nullptr: 1), j ascending.
+// y[t] = sum_j w[t, j] rows[pair_rows[t, j]] (w == nullptr: 1), j ascending, four
+// pairs' pieces in flight.  Bound by HBM: 4096 tokens, top 4, 2880 bf16: 22 us =
+// 5.3 TB/s of 118 MB.
 template <typename E, int kN>
 __global__ __launch_bounds__(kThreads) void unpermute_kernel(const E* __restrict__ rows,
                                                              const int32_t* __restrict__ pair_rows,
@@ -237,7 +242,9 @@ __global__ __launch_bounds__(kThreads) void unpermute_kernel(const E* __restrict
 
 // d_rows and d_w, kWaves waves per token (four for a batch too small to fill
 // the chip with one each), four pairs at a time beside one read of dy; the
-// blocks from zero_block0 on clear the rows that hold no pair.
+// blocks from zero_block0 on clear the rows that hold no pair.  Bound by HBM:
+// 4096 tokens, top 4, 2880 bf16: 37 us = 5.7 TB/s of 212 MB; 777 tokens, top 2,
+// 1001 float32, 5 of 8 experts: 4.7 us, of which an empty launch is 2.2.
 template <typename E, int kN, int kWaves>
 __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
     const E* __restrict__ dy, const E* __restrict__ rows, const int32_t* __restrict__ sorted_pairs,
@@ -319,7 +326,7 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
 // A block takes kRouteTokens tokens: a thread per token forms the gradients of
 // its picks in LDS, then all threads write the rows, kV logits at a time (4
 // where E allows), each compared with its token's ids.  Bound by the bytes
-// written.
+// written: 32768 tokens, 128 experts, top 4: 6.9 us = 2.7 TB/s of 18 MB.
 constexpr int kRouteTokens = 32;
 template <int kV>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(const int32_t* __restrict__ ids,
