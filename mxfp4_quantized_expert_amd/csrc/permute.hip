@@ -68,10 +68,22 @@ __device__ void invert_chunk(const int32_t* __restrict__ sorted_pairs, int64_t R
   for (int i = threadIdx.x; i < kPairChunk; i += blockDim.x) lds[i] = -1;
   __syncthreads();
   const int64_t first = (int64_t)chunk * kPairChunk;
-#pragma unroll 8
-  for (int64_t i = threadIdx.x; i < R; i += blockDim.x) {
-    const int64_t d = (int64_t)sorted_pairs[i] - first;
-    if (d >= 0 && d < kPairChunk) atomicMax(&lds[d], (int)i);
+  // sixteen pairs of a thread in flight, four to a load
+  typedef int32_t four __attribute__((ext_vector_type(4)));
+  typedef four loose __attribute__((aligned(4)));
+  const int64_t whole = R & ~(int64_t)3;
+#pragma unroll 4
+  for (int64_t i = 4 * (int64_t)threadIdx.x; i < whole; i += 4 * blockDim.x) {
+    const four p = *reinterpret_cast<const loose*>(sorted_pairs + i);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t d = (uint32_t)p[c] - (uint32_t)first;
+      if (d < (uint32_t)kPairChunk) atomicMax(&lds[d], (int)i + c);
+    }
+  }
+  if (threadIdx.x < R - whole) {
+    const uint32_t d = (uint32_t)sorted_pairs[whole + threadIdx.x] - (uint32_t)first;
+    if (d < (uint32_t)kPairChunk) atomicMax(&lds[d], (int)(whole + threadIdx.x));
   }
   __syncthreads();
   for (int i = threadIdx.x; i < kPairChunk; i += blockDim.x)
