@@ -335,24 +335,25 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
   }
 }
 
-// A block takes kRouteTokens tokens: a thread per token forms the gradients of
+// A block takes `tokens` tokens (at most kRouteTokens): a thread per token forms the gradients of
 // its picks in LDS, then all threads write the rows, kV logits at a time (4
 // where E allows), each compared with its token's ids.  Bound by the bytes
-// written: 32768 tokens, 128 experts, top 4: 6.9 us = 2.7 TB/s of 18 MB.
+// written: 32768 tokens, 128 experts, top 4: 7.2 us = 2.5 TB/s of 18 MB, of
+// which an empty launch is 2.2.
 constexpr int kRouteTokens = 32;
 template <int kV>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(const int32_t* __restrict__ ids,
                                                                   const float* __restrict__ weights,
                                                                   const float* __restrict__ d_weights,
                                                                   float* __restrict__ d_logits, int64_t T, int E,
-                                                                  int top_k) {
+                                                                  int top_k, int tokens) {
   typedef float vec __attribute__((ext_vector_type(kV)));
   __shared__ int32_t id[kRouteTokens][MXFP4MOE_MAX_TOPK + 1];
   __shared__ float grad[kRouteTokens][MXFP4MOE_MAX_TOPK + 1];
   const int parts = E / kV, lanes = min(parts, kThreads);
   const int lt = threadIdx.x / lanes, step = kThreads / lanes;  // this thread's first token, tokens at once
-  for (int64_t t0 = (int64_t)blockIdx.x * kRouteTokens; t0 < T; t0 += (int64_t)gridDim.x * kRouteTokens) {
-    const int n = (int)min((int64_t)kRouteTokens, T - t0);
+  for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < T; t0 += (int64_t)gridDim.x * tokens) {
+    const int n = (int)min((int64_t)tokens, T - t0);
     if ((int)threadIdx.x < n) {
       const size_t p0 = (size_t)(t0 + threadIdx.x) * top_k;
       float s = 0.f;
@@ -502,14 +503,19 @@ hipError_t launch_route_backward(const int32_t* ids, const float* weights, const
                                  int64_t E, int64_t top_k, float* d_logits, hipStream_t stream) {
   if (T == 0) return hipSuccess;
   const bool four = E % 4 == 0 && aligned(d_logits, 16);
-  const unsigned blocks = block_count(T, kRouteTokens);
+  // fewer tokens a block while two blocks a CU are not there, or a block writes more than 8 KB (tokens 32, 16 and 8:
+  // T = 4096, E = 128, top 8: 7.3, 5.2 and 4.2 us; T = 32768, E = 128: 7.4, 7.2 and 8.2; E = 32: 4.0, 4.6 and 6.2)
+  int tokens = kRouteTokens;
+  while (tokens > 8 && ((T + tokens - 1) / tokens < 2 * device_cu_count() || (tokens > 16 && tokens * E > 2048)))
+    tokens /= 2;
+  const unsigned blocks = block_count(T, tokens);
   ProfileScope prof(kStageRouteBackward, stream);
   if (four)
     route_backward_kernel<4><<<blocks, kThreads, 0, stream>>>(ids, weights, d_weights, d_logits, T, (int)E,
-                                                              (int)top_k);
+                                                              (int)top_k, tokens);
   else
     route_backward_kernel<1><<<blocks, kThreads, 0, stream>>>(ids, weights, d_weights, d_logits, T, (int)E,
-                                                              (int)top_k);
+                                                              (int)top_k, tokens);
   return hipGetLastError();
 }
 

@@ -528,3 +528,23 @@ def test_same_bits_every_time(gpu, fmt, E, mean, N, K):
         other.linear(gpu, x, None, off), other.backward(gpu, dy, off)
         assert torch.equal(w.linear(gpu, x, None, off), y)
         assert torch.equal(w.backward(gpu, dy, off), dx)
+
+
+def test_two_streams_at_once(gpu):
+    """Calls on two streams share nothing: each gives what it gives alone."""
+    rng = np.random.default_rng(11)
+    jobs = []
+    for i, (fmt, E, mean, N, K) in enumerate([("mxfp4", 32, 24, 2002, 800), ("nvfp4", 64, 100, 1606, 1568)]):
+        counts = rng.poisson(mean, E)
+        w, off, R = Weights(fmt, E, N, K, seed=i), offsets_of(counts), int(counts.sum())
+        x, dy = bf16(rng, R, K), bf16(rng, R, N)
+        jobs.append((w, off, x, dy, w.linear(gpu, x, None, off), w.backward(gpu, dy, off), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(6):
+        got = []
+        for w, off, x, dy, _, _, stream in jobs:
+            with torch.cuda.stream(stream):
+                got.append((w.linear(gpu, x, None, off), w.backward(gpu, dy, off)))
+        torch.cuda.synchronize()
+        for (_, _, _, _, y, dx, _), (a, b) in zip(jobs, got):
+            assert torch.equal(a, y) and torch.equal(b, dx)
