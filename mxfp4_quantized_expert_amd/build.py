@@ -60,7 +60,7 @@ def _build_host_calls() -> None:
            "-isystem", os.path.join(torch_dir, "include"), "-isystem", sysconfig.get_paths()["include"],
            os.path.join(CSRC, "host_calls.cpp"), "-o", HOST_CALLS + ".tmp",
            f"-L{PKG}", "-lmxfp4moe", "-Wl,-rpath,$ORIGIN",
-           f"-L{os.path.join(torch_dir, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+           f"-L{os.path.join(torch_dir, 'lib')}", "-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("building host_calls failed:\n" + r.stdout + r.stderr)

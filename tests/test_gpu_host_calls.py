@@ -124,3 +124,34 @@ def test_another_stream_is_current(gpu):
         got = _list(gpu.moe_permute(d["x"], d["pairs"], k))
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_torch_makes_the_outputs_where_a_mode_looks_at_them(gpu):
+    """New tensors filled under deterministic algorithms, and modes that see every call of torch."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    rng = torch.Generator("cuda").manual_seed(2)
+    blocks = torch.randint(0, 256, (2, 40, 32), generator=rng, device="cuda", dtype=torch.uint8)
+    scales = torch.full((2, 40, 2), 127, dtype=torch.uint8, device="cuda")
+    x = torch.randn((9, 64), generator=rng, device="cuda").bfloat16()
+    offsets = torch.tensor([1, 4, 7], dtype=torch.int32, device="cuda")
+    want = gpu.moe_mxfp4_linear(x, blocks, scales, None, offsets)[1:7].clone()
+    was = torch.are_deterministic_algorithms_enabled()
+    try:
+        torch.use_deterministic_algorithms(True)
+        y = gpu.moe_mxfp4_linear(x, blocks, scales, None, offsets)
+    finally:
+        torch.use_deterministic_algorithms(was)
+    assert torch.equal(y[1:7], want) and bool(torch.isnan(y[[0, 7, 8]]).all())
+
+    class Seen(TorchDispatchMode):
+        names = []
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            self.names.append(str(func))
+            return func(*args, **(kwargs or {}))
+
+    with Seen():
+        y = gpu.moe_mxfp4_linear(x, blocks, scales, None, offsets)
+    assert any("empty" in n for n in Seen.names)
+    assert torch.equal(y[1:7], want)
