@@ -335,54 +335,55 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
   }
 }
 
-// A block takes `tokens` tokens (at most kRouteTokens): a thread per token forms the gradients of
-// its picks in LDS, then all threads write the rows, kV logits at a time (4
-// where E allows), each compared with its token's ids.  Bound by the bytes
-// written: 32768 tokens, 128 experts, top 4: 7.2 us = 2.5 TB/s of 18 MB, of
-// which an empty launch is 2.2.
+// A block takes `tokens` tokens (at most kRouteTokens, a multiple of 4): their
+// rows lie in LDS, zeros into which a thread per token adds the gradients of
+// its picks in order, and leave as one contiguous stretch, 16 bytes a thread.
+// Bound by the bytes written: 32768 tokens, 128 experts, top 4: 6.1 us = 3.0
+// TB/s of 18 MB, of which an empty launch is 2.2 (each logit compared with its
+// token's picks instead: 7.4).
 constexpr int kRouteTokens = 32;
-template <int kV>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(const int32_t* __restrict__ ids,
                                                                   const float* __restrict__ weights,
                                                                   const float* __restrict__ d_weights,
                                                                   float* __restrict__ d_logits, int64_t T, int E,
                                                                   int top_k, int tokens) {
-  typedef float vec __attribute__((ext_vector_type(kV)));
-  __shared__ int32_t id[kRouteTokens][MXFP4MOE_MAX_TOPK + 1];
-  __shared__ float grad[kRouteTokens][MXFP4MOE_MAX_TOPK + 1];
-  const int parts = E / kV, lanes = min(parts, kThreads);
-  const int lt = threadIdx.x / lanes, step = kThreads / lanes;  // this thread's first token, tokens at once
+  using Pc = Piece<float, 4>;
+  extern __shared__ __attribute__((aligned(16))) float rows[];  // [tokens][E]
+  __shared__ int32_t id[kRouteTokens * MXFP4MOE_MAX_TOPK];
+  __shared__ float w[kRouteTokens * MXFP4MOE_MAX_TOPK], dw[kRouteTokens * MXFP4MOE_MAX_TOPK];
   for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < T; t0 += (int64_t)gridDim.x * tokens) {
-    const int n = (int)min((int64_t)tokens, T - t0);
+    const int n = (int)min((int64_t)tokens, T - t0), pairs = n * top_k, floats = n * E;
+    const size_t p0 = (size_t)t0 * top_k;
+    for (int i = threadIdx.x; i < pairs; i += kThreads) {
+      id[i] = ids[p0 + i];
+      w[i] = weights[p0 + i];
+      dw[i] = d_weights[p0 + i];
+    }
+    for (int i = threadIdx.x; 4 * i < floats; i += kThreads) *reinterpret_cast<Pc::vec*>(rows + 4 * i) = Pc::vec{};
+    __syncthreads();
     if ((int)threadIdx.x < n) {
-      const size_t p0 = (size_t)(t0 + threadIdx.x) * top_k;
+      const int q0 = threadIdx.x * top_k;
       float s = 0.f;
 #pragma unroll 4
-      for (int j = 0; j < top_k; ++j) s = __builtin_fmaf(weights[p0 + j], d_weights[p0 + j], s);
+      for (int j = 0; j < top_k; ++j) s = __builtin_fmaf(w[q0 + j], dw[q0 + j], s);
 #pragma unroll 4
       for (int j = 0; j < top_k; ++j) {
-        id[threadIdx.x][j] = ids[p0 + j];
-        grad[threadIdx.x][j] = weights[p0 + j] * (d_weights[p0 + j] - s);
+        const int e = id[q0 + j];
+        if (e >= 0 && e < E) rows[threadIdx.x * E + e] += w[q0 + j] * (dw[q0 + j] - s);
       }
     }
     __syncthreads();
-    if (lt < step) {
-      for (int t = lt; t < n; t += step)
-        for (int part = threadIdx.x - lt * lanes; part < parts; part += lanes) {
-          vec g = {};
-          for (int j = 0; j < top_k; ++j) {
-            const int at = id[t][j] - part * kV;
-#pragma unroll
-            for (int c = 0; c < kV; ++c) g[c] += at == c ? grad[t][j] : 0.f;
-          }
-          *reinterpret_cast<vec*>(d_logits + (t0 + t) * E + part * kV) = g;
-        }
+    float* out = d_logits + t0 * E;
+    for (int i = threadIdx.x; 4 * i < floats; i += kThreads) {
+      if (4 * i + 4 <= floats) {
+        Pc::store(out + 4 * i, *reinterpret_cast<const Pc::vec*>(rows + 4 * i));
+      } else {
+        for (int c = 4 * i; c < floats; ++c) out[c] = rows[c];
+      }
     }
     __syncthreads();
   }
 }
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 // One piece a lane while the groups can be counted in 31 bits.
 RowSplit row_split(int64_t rows, int64_t nv) {
@@ -502,20 +503,14 @@ hipError_t launch_unpermute_backward(const void* dy, const void* rows, int dtype
 hipError_t launch_route_backward(const int32_t* ids, const float* weights, const float* d_weights, int64_t T,
                                  int64_t E, int64_t top_k, float* d_logits, hipStream_t stream) {
   if (T == 0) return hipSuccess;
-  const bool four = E % 4 == 0 && aligned(d_logits, 16);
-  // fewer tokens a block while two blocks a CU are not there, or a block writes more than 8 KB (tokens 32, 16 and 8:
-  // T = 4096, E = 128, top 8: 7.3, 5.2 and 4.2 us; T = 32768, E = 128: 7.4, 7.2 and 8.2; E = 32: 4.0, 4.6 and 6.2)
+  // fewer tokens a block while two blocks a CU are not there, or a block writes more than 8 KB (tokens 32, 16 and 8: T =
+  // 4096, E = 128, top 8: 4.0, 3.7 and 3.6 us; T = 32768, E = 128: 6.3, 6.2 and 7.2; E = 32: 3.8, 4.3 and 5.6)
   int tokens = kRouteTokens;
   while (tokens > 8 && ((T + tokens - 1) / tokens < 2 * device_cu_count() || (tokens > 16 && tokens * E > 2048)))
     tokens /= 2;
-  const unsigned blocks = block_count(T, tokens);
   ProfileScope prof(kStageRouteBackward, stream);
-  if (four)
-    route_backward_kernel<4><<<blocks, kThreads, 0, stream>>>(ids, weights, d_weights, d_logits, T, (int)E,
-                                                              (int)top_k, tokens);
-  else
-    route_backward_kernel<1><<<blocks, kThreads, 0, stream>>>(ids, weights, d_weights, d_logits, T, (int)E,
-                                                              (int)top_k, tokens);
+  route_backward_kernel<<<block_count(T, tokens), kThreads, ((size_t)tokens * E + 3) / 4 * 16, stream>>>(
+      ids, weights, d_weights, d_logits, T, (int)E, (int)top_k, tokens);
   return hipGetLastError();
 }
 
