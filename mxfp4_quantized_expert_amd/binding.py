@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from typing import Optional
 
 import torch
@@ -34,8 +35,8 @@ STAGES = {"route": 1, "group": 2, "gate_up": 3, "down": 4, "combine": 5, "dequan
           "unpermute_backward": 16, "route_backward": 17, "linear": 18, "linear_backward": 19}
 
 _lib: Optional[ctypes.CDLL] = None
-# The module of the short host path (csrc/host_calls.cpp), set with _lib; without it every call goes
-# through ctypes.
+# The module of the short host path (csrc/host_calls.cpp), set with _lib; without it, or with one that
+# cannot be loaded, every call goes through ctypes.
 _host = None
 
 _vp = ctypes.c_void_p
@@ -110,10 +111,14 @@ def load() -> ctypes.CDLL:
     lib.mxfp4moe_profile_begin.restype = ctypes.c_int
     lib.mxfp4moe_profile_end.argtypes = [ctypes.POINTER(ctypes.c_float), ctypes.c_int]
     lib.mxfp4moe_profile_end.restype = ctypes.c_int
-    _lib = lib
     if os.path.exists(HOST_PATH):
-        from . import _host_calls
-        _host = _host_calls
+        try:
+            from . import _host_calls
+            _host = _host_calls
+        except (ImportError, AttributeError) as e:  # built for another Python or torch
+            warnings.warn(f"{HOST_PATH} cannot be loaded, calls take the longer way through ctypes: {e}",
+                          RuntimeWarning, stacklevel=2)
+    _lib = lib
     return lib
 
 
