@@ -48,28 +48,38 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _build_host_calls() -> None:
-    """csrc/host_calls.cpp, the Python module of the short host path, beside the library it calls."""
-    import sysconfig
+def _build_host_calls() -> bool:
+    """csrc/host_calls.cpp, the Python module of the short host path, beside the library it calls.  It needs
+    g++ and the headers of Python and torch; where it cannot be built, none is left (one of an earlier
+    library would call this one), and the binding calls through ctypes."""
+    try:
+        import sysconfig
 
-    import torch
+        import torch
 
-    torch_dir = os.path.dirname(torch.__file__)
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-isystem", os.path.join(torch_dir, "include"), "-isystem", sysconfig.get_paths()["include"],
-           os.path.join(CSRC, "host_calls.cpp"), "-o", HOST_CALLS + ".tmp",
-           f"-L{PKG}", "-lmxfp4moe", "-Wl,-rpath,$ORIGIN",
-           f"-L{os.path.join(torch_dir, 'lib')}", "-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-lc10"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("building host_calls failed:\n" + r.stdout + r.stderr)
+        torch_dir = os.path.dirname(torch.__file__)
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               "-isystem", os.path.join(torch_dir, "include"), "-isystem", sysconfig.get_paths()["include"],
+               os.path.join(CSRC, "host_calls.cpp"), "-o", HOST_CALLS + ".tmp",
+               f"-L{PKG}", "-lmxfp4moe", "-Wl,-rpath,$ORIGIN",
+               f"-L{os.path.join(torch_dir, 'lib')}", "-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-lc10"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        why = "" if r.returncode == 0 else r.stdout + r.stderr or f"{cmd[0]} ended with {r.returncode}"
+    except (ImportError, OSError) as e:
+        why = str(e)
+    if why:
+        if os.path.exists(HOST_CALLS):
+            os.remove(HOST_CALLS)
+        print(f"{HOST_CALLS} was not built, calls take the longer way through ctypes:\n{why}", file=sys.stderr)
+        return False
     os.replace(HOST_CALLS + ".tmp", HOST_CALLS)
+    return True
 
 
 def build(verbose: bool = True) -> str:
-    """Compile every csrc/*.hip for gfx950 and link libmxfp4moe.so next to this file, then the
-    Python module that calls it."""
+    """Compile every csrc/*.hip for gfx950 and link libmxfp4moe.so next to this file, then, where that
+    can be done, the Python module that calls it."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:

@@ -57,3 +57,30 @@ def test_a_module_that_cannot_be_loaded(package):
     pkg, run = package
     (pkg / "_host_calls.so").write_bytes(b"\x7fELF of something else")
     assert run() == ["0 True 1", "1 True 0", "2 True 0"]
+
+
+@pytest.fixture
+def stale(tmp_path, monkeypatch):
+    """A module of an earlier build at the place where the build puts a new one."""
+    from mxfp4_quantized_expert_amd import build
+
+    path = tmp_path / "_host_calls.so"
+    path.write_bytes(b"of an earlier library")
+    monkeypatch.setattr(build, "HOST_CALLS", str(path))
+    return build, path
+
+
+@pytest.mark.parametrize("compiler", ["false", "/nowhere/g++"])
+def test_build_goes_on_without_a_compiler_for_the_module(stale, monkeypatch, capsys, compiler):
+    """hipcc is enough for the library; a module that does not belong to it must not stay beside it."""
+    build, path = stale
+    monkeypatch.setenv("CXX", compiler)
+    build._build_host_calls()
+    assert not path.exists() and "ctypes" in capsys.readouterr().err
+
+
+def test_build_goes_on_without_torch(stale, monkeypatch, capsys):
+    build, path = stale
+    monkeypatch.setitem(sys.modules, "torch", None)  # import torch raises ImportError
+    build._build_host_calls()
+    assert not path.exists() and "ctypes" in capsys.readouterr().err
