@@ -10,6 +10,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <ATen/ATen.h>
+#include <ATen/EmptyTensor.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/core/impl/VirtualGuardImpl.h>
@@ -70,8 +71,9 @@ struct Call {
   }
 
  private:
+  // what stands in for an argument that does not fit: outlives the runtime's end, and so the mode of this call
   static const at::Tensor& dummy() {
-    static const at::Tensor& t = *new at::Tensor(at::empty({0, 0}, at::kFloat));  // outlives the runtime's end
+    static const at::Tensor& t = *new at::Tensor(at::detail::empty_cpu({0, 0}, at::kFloat));
     return t;
   }
 };

@@ -84,3 +84,35 @@ def test_build_goes_on_without_torch(stale, monkeypatch, capsys):
     monkeypatch.setitem(sys.modules, "torch", None)  # import torch raises ImportError
     build._build_host_calls()
     assert not path.exists() and "ctypes" in capsys.readouterr().err
+
+
+REFUSED = """
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+from torch.utils._python_dispatch import TorchDispatchMode
+from mxfp4_quantized_expert_amd import binding
+binding.load()
+host = binding._host
+assert host is not None
+
+class Seen(TorchDispatchMode):
+    names = []
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        self.names.append(str(func))
+        return func(*args, **(kwargs or {}))
+
+x, pairs = torch.zeros((3, 8)), torch.zeros(3, dtype=torch.int32)
+with Seen():  # the first call of the process that is left to the step-by-step path
+    assert host.permute(x, pairs, 1) is None
+print(len(Seen.names))
+"""
+
+
+def test_a_call_left_to_the_longer_way_makes_no_tensor_of_its_own():
+    """What stands in for an unfit argument outlives the call, so no mode that happens to be on may make it."""
+    if not os.path.exists(binding.HOST_PATH):
+        pytest.skip("the module is not built")
+    r = subprocess.run([sys.executable, "-c", REFUSED], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert r.stdout.split() == ["0"]
