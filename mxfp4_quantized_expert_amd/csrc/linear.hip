@@ -938,10 +938,14 @@ __device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][kMax], u32x4* c
 #pragma unroll
       for (int cb = 0; cb < kLive; ++cb) b[s][cb] = base[boff[s] + cb * 256];
     }
-    // before the other block's loads and scales: 2 to 3 % (NVFP4 over 128 experts 472 -> 487 us; forward: none, or worse)
-    if constexpr (!kNv) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
+      // From the second step on before the other block's loads and scales (16384 rows over 128 experts, 2880 x 2880: 356
+      // us, without 380, from the first step on 369 and five registers spilled; dense 240, 262, 260; NVFP4 over 128
+      // experts 472 -> 487; forward: none, or worse).
+      if constexpr (!kNv) {
+        if (s == 1) __builtin_amdgcn_s_setprio(1);
+      }
       u32x4 op[2];
 #pragma unroll
       for (int p = 0; p < 4; ++p) {  // rows 2p, 2p + 1 of the eight
