@@ -19,6 +19,7 @@
 
 #include "expert_device.h"
 #include "internal.h"
+#include "linear_plan.h"
 #include "mx_device.h"
 
 namespace {
@@ -156,7 +157,7 @@ __device__ __forceinline__ bool map_tile(const LinearArgs& a, int tm, int chunks
 // 46), and for a single small matrix the latency of one pass (256 rows, N =
 // 1024, K = 736: 4.6 us, of which an empty launch is 2.2; 128 rows, 2880 x
 // 2880: 14.6 us, where tiles take 17.5).
-constexpr int kFewRows = 16;
+constexpr int kFewRows = mxlinear::kFewTileRows;
 
 // Four consecutive outputs: s2 * v + bias, `n` of them in range (`whole`: always four, 8-byte aligned).
 __device__ __forceinline__ void store4(uint16_t* out, f32x4 v, float s2, const uint16_t* bias, int n, bool whole) {
@@ -1071,55 +1072,7 @@ dim3 grid_of(int64_t tiles, int64_t chunks) {
   return blocks <= kMaxX ? dim3((unsigned)blocks) : dim3((unsigned)kMaxX, (unsigned)((blocks + kMaxX - 1) / kMaxX));
 }
 
-// Whether the tiles of up to 128 rows pay, and their rows: a choice by the
-// sizes alone, from times measured at N, K = 736 .. 2880, 1 to 128 experts
-// and 4 to 16384 rows.
-//
-// A tile block takes a fixed time for each chunk of its loop, by its rows and
-// by whether it has its CU to itself or shares it with another.  So few rows
-// take small tiles, for more blocks, and many take large ones, which read
-// fewer bytes of LDS for a product (2880 x 2880, tiles of 128, 64 and 32 rows:
-// 512 dense rows 42, 25 and 19 us; 1024 rows 43, 27 and 30; 8192 rows 120, 136
-// and 174; 16384 rows over 128 experts 365, 374 and 494).
-//
-// The 16-row kernels read the weights once for each 16 rows: from HBM the
-// first time, at `cold` bytes/us, from the caches then, at `hot`.
-struct TileCost {  // us of a chunk of tiles of 32, 64 and 128 rows
-  double alone[3], shared[3];
-};
-constexpr TileCost kForward{{0.32, 0.49, 0.88}, {0.57, 0.83, 1.43}};
-constexpr TileCost kBackward{{0.53, 0.64, 1.02}, {0.78, 1.0, 1.58}};
-struct TilePlan {
-  bool pays;
-  int rows;
-};
-TilePlan plan_tiles(const LinearArgs& a, int most_rows, int64_t col_tiles, int chunks, bool nv, const TileCost& cost,
-                    double cold, double hot) {
-  const double cus = mxfp4moe::device_cu_count();
-  const double experts = a.E < a.R ? a.E : a.R, bytes = (double)a.N * a.K * (nv ? 0.5625 : 0.53125);
-  TilePlan p{false, 0};
-  double best = 0;
-  for (int r = 0; r < 3 && 32 << r <= most_rows; ++r) {
-    // half of the experts' last tiles, in the mean, and those half full
-    const double full = (double)a.R / (32 << r), tiles = a.offsets != nullptr ? full + 0.5 * experts : max_tiles(a, 32 << r);
-    const double load = tiles * col_tiles / cus;  // blocks of a CU
-    double chunk;
-    if (load > 4) {
-      chunk = (full * cost.shared[r] + (tiles - full) * cost.shared[0]) * col_tiles / (2 * cus);
-    } else {  // in rounds of two
-      const int rounds = (int)(load / 2);
-      const double rest = load - 2 * rounds;
-      chunk = rounds * cost.shared[r] + (rest > 1 ? cost.shared[r] : rest > 0 ? cost.alone[r] : 0);
-    }
-    if (p.rows == 0 || chunk < best) p.rows = 32 << r, best = chunk;
-  }
-  const double stream_us = experts * bytes / 3.5e6;  // the weights from HBM
-  const double tile_us = 4 + (best * chunks > stream_us ? best * chunks : stream_us);
-  const double reads = (double)a.R / kFewRows + 0.5 * experts;  // of one expert's weights
-  const double few_us = 4 + experts * bytes / cold + (reads > experts ? reads - experts : 0) * bytes / hot;
-  p.pays = tile_us < few_us;
-  return p;
-}
+mxlinear::Sizes sizes_of(const LinearArgs& a, bool nv) { return {a.R, a.N, a.K, a.E, a.offsets != nullptr, nv}; }
 
 // Blocks for `jobs` row groups: one each while they are few (one pass, no
 // second latency), else as many as stay resident (per_cu waves to a CU).
@@ -1179,7 +1132,8 @@ hipError_t linear(LinearArgs a, hipStream_t stream) {
     if (dense ? a.R <= 4 : a.R <= kMeanOf4 * a.E) return launch_one<kNv, 1>(a, stream);
     if (dense ? a.R <= 8 : a.R <= kMeanOf8 * a.E) return launch_one<kNv, 2>(a, stream);
   }
-  const TilePlan plan = plan_tiles(a, kTileRows, n_tiles, (a.K + 63) / 64, kNv, kForward, 2.9e6, 3.7e6);
+  const mxlinear::TilePlan plan = mxlinear::plan_tiles(sizes_of(a, kNv), true, kTileRows, n_tiles, (a.K + 63) / 64,
+                                                       mxfp4moe::device_cu_count());
   if (!plan.pays) return launch_few<kNv>(a, stream);
   a.tile_rows = plan.rows;
   a.max_tiles = max_tiles(a, plan.rows);
@@ -1205,7 +1159,8 @@ hipError_t linear_backward(LinearArgs a, hipStream_t stream) {
   const int64_t k_tiles = (a.K + kBackK - 1) / kBackK;
   // odd N: dy through registers, which 128 rows leave none of
   const int most = a.N % 2 == 0 ? kTileRows : 64;
-  const TilePlan plan = plan_tiles(a, most, k_tiles, (a.N + 63) / 64, kNv, kBackward, 1.9e6, 5e6);
+  const mxlinear::TilePlan plan = mxlinear::plan_tiles(sizes_of(a, kNv), false, most, k_tiles, (a.N + 63) / 64,
+                                                       mxfp4moe::device_cu_count());
   if (plan.pays) {
     a.tile_rows = plan.rows;
     a.max_tiles = max_tiles(a, plan.rows);

@@ -1,0 +1,97 @@
+// Which of the linear operators' kernels takes a call, and the rows of its
+// tiles: plain host arithmetic on the sizes alone, from times measured at N,
+// K = 736 .. 2880, 1 to 128 experts, 4 to 16384 rows, even and skewed loads.
+#pragma once
+
+#include <math.h>
+#include <stdint.h>
+
+namespace mxlinear {
+
+struct Sizes {
+  int64_t rows, n, k, experts;
+  bool grouped;  // rows by expert (expert_offsets), else one dense matrix
+  bool nv;       // NVFP4 weights
+};
+
+inline double used_experts(const Sizes& s) { return (double)(s.experts < s.rows ? s.experts : s.rows); }
+
+// Bytes of one expert's codes and scales.
+inline double weight_bytes(const Sizes& s) { return (double)s.n * s.k * (s.nv ? 0.5625 : 0.53125); }
+
+// Row tiles of `tm` rows that a call has.  Evenly routed rows: an expert's
+// count is Poisson distributed, and it has a tile for every multiple of tm that
+// the count passes, one at least.  Where the counts spread over more than a
+// tile, the last ones are half full in the mean.
+inline double expected_tiles(const Sizes& s, int tm) {
+  if (!s.grouped) return (double)((s.rows + tm - 1) / tm);
+  const double experts = used_experts(s), mean = s.rows / experts, spread = sqrt(mean);
+  if (4 * spread > tm) return s.rows / (double)tm + 0.5 * experts;
+  double tiles = 1;
+  for (int j = 1; j * tm < mean + 4 * spread; ++j) tiles += 0.5 * erfc((j * tm + 0.5 - mean) / (spread * sqrt(2.0)));
+  return tiles * experts;
+}
+
+// A tile block takes a fixed time for each chunk of its loop, by its rows and
+// by whether it has its CU to itself or shares it with another.  So few rows
+// take small tiles, for more blocks, and many take large ones, which read
+// fewer bytes of LDS for a product (2880 x 2880, tiles of 128, 64 and 32 rows:
+// 512 dense rows 42, 25 and 19 us; 1024 rows 43, 27 and 30; 8192 rows 120, 136
+// and 174; 16384 rows over 128 experts 365, 374 and 494).
+struct TileCost {  // us of a chunk of tiles of 32, 64 and 128 rows
+  double alone[3], shared[3];
+};
+constexpr TileCost kForward{{0.32, 0.49, 0.88}, {0.57, 0.83, 1.43}};
+constexpr TileCost kBackward{{0.53, 0.64, 1.02}, {0.78, 1.0, 1.58}};
+
+// ... and no tile is faster than its weights arrive, in bytes/us: from HBM for
+// an expert's first tile (forward tiles of 128 rows have fewer stages of them
+// on their way: 832 rows over 128 experts, 5760 x 2880, in tiles of 128, 64 and
+// 32 rows: 292, 279 and 277 us), mostly from the caches for the others (1280
+// rows over 32 experts, 5760 x 2880, 36 tiles of 64 or 60 of 32: 89 and 121 us).
+constexpr double kFirstRead = 3.5e6, kFirstRead128 = 3.3e6, kNextRead = 7e6;
+
+// The 16-row kernels read the weights once for each 16 rows: from HBM the
+// first time, at `cold` bytes/us, from the caches then, at `hot`.
+struct FewCost {
+  double cold, hot;
+};
+constexpr FewCost kForwardFew{2.9e6, 3.7e6}, kBackwardFew{1.9e6, 5e6};
+
+constexpr int kFewTileRows = 16;
+
+struct TilePlan {
+  bool pays;  // tiles, else the 16-row kernels
+  int rows;   // of a tile
+};
+
+// col_tiles, chunks: blocks and loop steps of the other two axes.
+inline TilePlan plan_tiles(const Sizes& s, bool forward, int most_rows, int64_t col_tiles, int chunks, double cus) {
+  const TileCost& cost = forward ? kForward : kBackward;
+  const FewCost& few = forward ? kForwardFew : kBackwardFew;
+  const double experts = used_experts(s), bytes = weight_bytes(s);
+  TilePlan p{false, 0};
+  double best = 0;
+  for (int r = 0; r < 3 && 32 << r <= most_rows; ++r) {
+    const double tiles = expected_tiles(s, 32 << r), load = tiles * col_tiles / cus;  // blocks of a CU
+    double chunk;
+    if (load > 4) {  // full tiles, and an expert's last ones as a block of 32 rows
+      const double even = s.rows / (double)(32 << r), full = even < tiles ? even : tiles;
+      chunk = (full * cost.shared[r] + (tiles - full) * cost.shared[0]) * col_tiles / (2 * cus);
+    } else {  // in rounds of two
+      const int rounds = (int)(load / 2);
+      const double rest = load - 2 * rounds;
+      chunk = rounds * cost.shared[r] + (rest > 1 ? cost.shared[r] : rest > 0 ? cost.alone[r] : 0);
+    }
+    const double first = forward && r == 2 ? kFirstRead128 : kFirstRead;
+    const double read_us = (experts / first + (tiles > experts ? tiles - experts : 0) / kNextRead) * bytes;
+    const double us = chunk * chunks > read_us ? chunk * chunks : read_us;
+    if (p.rows == 0 || us < best) p.rows = 32 << r, best = us;
+  }
+  const double reads = s.rows / (double)kFewTileRows + 0.5 * experts;  // of one expert's weights
+  const double few_us = experts * bytes / few.cold + (reads > experts ? reads - experts : 0) * bytes / few.hot;
+  p.pays = best < few_us;
+  return p;
+}
+
+}  // namespace mxlinear
