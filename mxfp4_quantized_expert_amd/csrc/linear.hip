@@ -155,8 +155,9 @@ __device__ __forceinline__ bool map_tile(const LinearArgs& a, int tm, int chunks
 // return zero from the buffer's bounds.  Bound: the weights' bytes from HBM,
 // at 2.9 TB/s (224 rows over 32 experts, 2880 x 2880: 56 us, where tiles take
 // 46), and for a single small matrix the latency of one pass (256 rows, N =
-// 1024, K = 736: 4.6 us, of which an empty launch is 2.2; 128 rows, 2880 x
-// 2880: 14.6 us, where tiles take 17.5).
+// 1024, K = 736: 4.6 us, of which an empty launch is 2.2; one row, 2880 x 2880:
+// 4.6 us, where tiles of 4 rows take 5.0; 128 rows, 2880 x 2880: 14.6 us, where
+// tiles take 17.5).
 constexpr int kFewRows = mxlinear::kFewTileRows;
 
 // Four consecutive outputs: s2 * v + bias, `n` of them in range (`whole`: always four, 8-byte aligned).
@@ -258,9 +259,9 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs a) {
 // block's waves split K where it exceeds one wave's units and add their sums
 // through LDS in wave order.  Row groups are dealt to the blocks in equal
 // contiguous ranges, eight waves a CU.  13 of 32 NVFP4 experts, 5760 x 2880,
-// 16 rows: 28 us = 4.3 TB/s of 121 MB (16-row tiles: 47); one row, 2880 x
-// 4096: 5.7 us, of which an empty launch is 2.2; 128 rows over 32 experts, 2880
-// x 2880: 34 us (50).
+// 16 rows: 28 us = 4.3 TB/s of 121 MB (16-row tiles: 47); one row, 32768 x
+// 2880: 13.2 us = 3.8 TB/s of 50 MB (23.2); 128 rows over 32 experts, 2880 x
+// 2880: 34 us (50).
 constexpr int kOneRows = 4;
 constexpr int kBatch = 16;  // row groups that leave together
 
@@ -1120,20 +1121,17 @@ hipError_t launch_one(LinearArgs a, hipStream_t stream) {
 }
 constexpr int kOneMaxK = 3 * 8 * 512;  // three units for each of eight waves
 
-// Rows of an expert on average (dense: rows) up to which tiles of 4 and of 8
-// rows are taken.
-constexpr int kMeanOf4 = 2, kMeanOf8 = 6;
-
 template <bool kNv>
 hipError_t linear(LinearArgs a, hipStream_t stream) {
   const int64_t n_tiles = (a.N + kTileN - 1) / kTileN;
+  const mxlinear::Sizes sizes = sizes_of(a, kNv);
   if (a.K <= kOneMaxK) {
-    const bool dense = a.offsets == nullptr;
-    if (dense ? a.R <= 4 : a.R <= kMeanOf4 * a.E) return launch_one<kNv, 1>(a, stream);
-    if (dense ? a.R <= 8 : a.R <= kMeanOf8 * a.E) return launch_one<kNv, 2>(a, stream);
+    const int rows = mxlinear::stream_tile_rows(sizes);
+    if (rows == 4) return launch_one<kNv, 1>(a, stream);
+    if (rows == 8) return launch_one<kNv, 2>(a, stream);
   }
-  const mxlinear::TilePlan plan = mxlinear::plan_tiles(sizes_of(a, kNv), true, kTileRows, n_tiles, (a.K + 63) / 64,
-                                                       mxfp4moe::device_cu_count());
+  const mxlinear::TilePlan plan =
+      mxlinear::plan_tiles(sizes, true, kTileRows, n_tiles, (a.K + 63) / 64, mxfp4moe::device_cu_count());
   if (!plan.pays) return launch_few<kNv>(a, stream);
   a.tile_rows = plan.rows;
   a.max_tiles = max_tiles(a, plan.rows);

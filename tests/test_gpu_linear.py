@@ -548,3 +548,81 @@ def test_two_streams_at_once(gpu):
         torch.cuda.synchronize()
         for (_, _, _, _, y, dx, _), (a, b) in zip(jobs, got):
             assert torch.equal(a, y) and torch.equal(b, dx)
+
+
+# Calls with enough weights (13 MB and more) for few rows that they are streamed past them, in tiles of 4 rows and of 8:
+# every number of units of 512 k a wave and of waves a block, N that ends inside a row group.
+STREAMED = [  # rows of every expert (an int: dense), N, K
+    (1, 100_001, 256), (4, 50_003, 544), (3, 22_010, 1184), (7, 17_003, 1568), (8, 10_013, 2592), (2, 8_001, 3104),
+    (6, 7_002, 3680), (5, 5_003, 5152), (1, 4_007, 7200), (4, 3_001, 9888), (8, 2_501, 12_288), (3, 2_050, 12_256),
+    ([1, 0] * 256, 300, 352), ([0] * 20 + [3, 1, 0, 7] * 3 + [1] * 30, 515, 1184), ([2, 0, 0, 9, 4, 0, 1, 5], 1441, 3104),
+    ([0, 30] + [0, 1, 5, 8, 9] * 12, 290, 2112), ([4] * 64, 736, 736), ([17, 1], 3001, 9888),
+]
+STREAMED_IDS = [f"{c if isinstance(c, int) else len(c)}-{n}-{k}" for c, n, k in STREAMED]
+
+
+def streamed(fmt, counts, N, K, seed):
+    dense = isinstance(counts, int)
+    w = Weights(fmt, 1 if dense else len(counts), N, K, seed=seed, dense=dense)
+    return w, (counts if dense else sum(counts)), None if dense else offsets_of(counts)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("counts,N,K", STREAMED, ids=STREAMED_IDS)
+def test_streamed_weights(gpu, fmt, counts, N, K):
+    w, R, off = streamed(fmt, counts, N, K, seed=N + K)
+    used = 1 if off is None else min(len(counts), R)
+    assert used * N * K * 0.53125 >= 13e6
+    rng = np.random.default_rng(1)
+    x, bias = bf16(rng, R, K), w.bias if N % 2 else None
+    print(f"[streamed] {fmt} R={R} N={N} K={K}", flush=True)
+    want, mag, written = X.linear(f64(x), w.f64, None if off is None else off.cpu().numpy(),
+                                  None if bias is None else f64(bias))
+    assert written.all()
+    y = w.linear(gpu, x, bias, off)
+    assert_sums(y, want, mag, K, f"streamed {fmt}")
+    assert torch.equal(w.linear(gpu, x, bias, off), y)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("counts,N,K", [(4, 50_003, 544), (8, 10_013, 2592), ([2, 0, 0, 9, 4, 0, 1, 5], 1441, 3104)],
+                         ids=["4-rows", "8-rows", "experts"])
+def test_streamed_weights_keep_rows_apart(gpu, fmt, counts, N, K):
+    """Infinities and NaN of a row, and a NaN scale of a weight row, reach their own outputs only."""
+    w, R, off = streamed(fmt, counts, N, K, seed=3)
+    x = bf16(np.random.default_rng(7), R, K)
+    clean = w.linear(gpu, x, None, off)
+    x[0], x[R - 1] = float("inf"), float("nan")
+    got = w.linear(gpu, x, None, off)
+    assert torch.equal(got[1:R - 1], clean[1:R - 1])
+    assert not bool(torch.isfinite(got[0]).any()) and bool(torch.isnan(got[R - 1]).all())
+    x = bf16(np.random.default_rng(7), R, K)
+    w.s.reshape(-1, *w.s.shape[-2:])[-1, N - 1, -1] = 0xFF
+    w.upload()
+    bad = torch.zeros((R, N), dtype=torch.bool, device="cuda")
+    bad[0 if off is None else int(off[-2]):, N - 1] = True
+    got = w.linear(gpu, x, None, off)
+    assert torch.equal(torch.isnan(got), bad) and torch.equal(got[~bad], clean[~bad])
+
+
+def test_streamed_weights_in_a_graph(gpu):
+    counts, N, K = [2, 0, 0, 9, 4, 0, 1, 5], 1441, 3104
+    w, R, off = streamed("mxfp4", counts, N, K, seed=4)
+    x = torch.zeros((R, K), dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        w.linear(gpu, x, w.bias, off)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kept = w.linear(gpu, x, w.bias, off)
+    gen = torch.Generator().manual_seed(15)
+    for rep in range(4):
+        x.copy_(torch.randn(x.shape, generator=gen))
+        off.copy_(offsets_of(counts[rep:] + counts[:rep]))
+        eager = w.linear(gpu, x, w.bias, off).clone()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(kept, eager), rep

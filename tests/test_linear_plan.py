@@ -22,6 +22,9 @@ extern "C" int plan(int64_t rows, int64_t n, int64_t k, int64_t experts, int nv,
   const TilePlan p = plan_tiles(s, forward != 0, 128, cols, (int)(((forward ? k : n) + 63) / 64), 256);
   return p.pays ? p.rows : 0;
 }
+extern "C" int stream(int64_t rows, int64_t n, int64_t k, int64_t experts, int nv) {
+  return stream_tile_rows(Sizes{rows, n, k, experts > 0 ? experts : 1, experts > 0, nv != 0});
+}
 """
 
 
@@ -36,6 +39,7 @@ def plan(tmp_path_factory):
     i64 = ctypes.c_int64
     lib.tiles.argtypes, lib.tiles.restype = [i64, i64, ctypes.c_int], ctypes.c_double
     lib.plan.argtypes = [i64, i64, i64, i64, ctypes.c_int, ctypes.c_int]
+    lib.stream.argtypes = [i64, i64, i64, i64, ctypes.c_int]
     return lib
 
 
@@ -79,3 +83,25 @@ def test_dense_tiles(plan):
 ])
 def test_choices_where_both_sides_were_measured(plan, rows, n, k, experts, forward, good):
     assert plan.plan(rows, n, k, experts, 0, forward) in good
+
+
+@pytest.mark.parametrize("rows,n,k,experts,good", [
+    # us in tiles of 4 and of 8 rows, and through the other kernels
+    (1, 2880, 2880, 0, 0),       # 5.0, 6.0, 4.6
+    (8, 5760, 2880, 0, 0),       # 8.1, 14.3, 7.7
+    (8, 4096, 2880, 0, 0),       # 7.3, 9.9, 5.4
+    (1, 12288, 2880, 0, 4),      # 7.4, 8.7, 10.0
+    (1, 32768, 736, 0, 4),       # 6.8, 7.6, 9.2
+    (8, 32768, 2880, 0, 8),      # 18.8, 17.8, 23.5
+    (9, 32768, 2880, 0, 0),
+    (2, 2880, 2880, 4, 0),       # two experts at most: 8.0, 11.6, 6.9
+    (4, 2880, 2880, 4, 4),       # 7.9, 9.4, 10.8
+    (32, 736, 736, 32, 0),       # 9.7, 7.9, 5.8
+    (64, 736, 736, 64, 4),       # 9.2, 9.6, 10.0
+    (16, 5760, 2880, 32, 4),     # 24, 27, 45
+    (192, 2880, 2880, 32, 8),    # 46, 38, 48
+    (320, 5760, 2880, 32, 0),    # 126, 94, 78
+])
+@pytest.mark.parametrize("nv", [0, 1])
+def test_streaming_where_both_sides_were_measured(plan, rows, n, k, experts, good, nv):
+    assert plan.stream(rows, n, k, experts, nv) == good
