@@ -348,3 +348,44 @@ def test_rows_past_32_bit_offsets(gpu):
     d_rows, d_w = gpu.moe_unpermute_backward(x, rows, pairs, pair_rows, w, d_rows=y)
     assert torch.equal(d_rows[:, -1], (x[:, -1] * 0.5).flip(0))
     assert torch.equal(d_w[:, 0], x[:, 0].float() ** 2 + x[:, -1].float() ** 2)
+
+
+def unpermute_f64(b, dy=None):
+    """y, or with dy the gradients, in float64 on the GPU, each with the sum of its terms' magnitudes."""
+    at = torch.from_numpy(b.pair_rows_host).cuda()
+    here = (at >= 0)[:, None]
+    z = torch.where(here, b.z.double()[at.clamp_min(0)], 0.0).view(b.T, b.k, b.H)
+    w = b.w.double()[..., None]
+    if dy is None:
+        return (w * z).sum(1), (w * z).abs().sum(1)
+    d_rows = torch.zeros((b.R, b.H), dtype=torch.float64, device="cuda")
+    d_rows[at[here[:, 0]]] = (w * dy.double()[:, None]).reshape(-1, b.H)[here[:, 0]]
+    p = z * dy.double()[:, None]
+    return d_rows, p.sum(2), p.abs().sum(2)
+
+
+WIDE = [  # T, H, E, k, dtype, local, pad
+    (200, 2881, 16, 8, "f32", 11, 9),      # four waves a token, two rounds of four pairs
+    (200, 2881, 40, 32, "bf16", 29, 9),    # ... eight rounds
+    (63, 2880, 40, 32, "f16", None, 0),
+    (130, 1030, 12, 5, "bf16", 7, 3),      # ... the second round holds one pair
+    (4096, 2880, 32, 4, "bf16", None, 0),  # a wave a token, several pieces a lane, four pairs
+    (4100, 2883, 32, 4, "bf16", 20, 50),
+    (4100, 1001, 16, 6, "f32", 9, 70),     # ... two rounds
+    (5000, 2880, 16, 3, "f16", 5, 0),
+]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=["-".join(map(str, c)) for c in WIDE])
+def test_unpermute_and_gradients_of_wide_rows(gpu, case):
+    T, H, E, k, dtype, local, pad = case
+    b = Batch(T, H, E, k, dtype, local, pad, seed=T + H + k)
+    print(f"[unpermute wide] {case}", flush=True)
+    want, mag = (v.cpu().numpy() for v in unpermute_f64(b))
+    assert_rounded(gpu.moe_unpermute(b.z, b.pair_rows, b.w), want, k * U32 * mag, b.dtype, "y")
+    d_rows, d_w = gpu.moe_unpermute_backward(b.dy, b.z, b.pairs, b.pair_rows, b.w)
+    want, want_w, mag = (v.cpu().numpy() for v in unpermute_f64(b, b.dy))
+    assert_rounded(d_rows, want, U32 * np.abs(want), b.dtype, "d_rows")
+    assert_rounded(d_w, want_w, (H + 1) * U32 * mag, torch.float32, "d_weights")
+    again = gpu.moe_unpermute_backward(b.dy, b.z, b.pairs, b.pair_rows, b.w)
+    assert torch.equal(again[0], d_rows) and torch.equal(again[1], d_w)
