@@ -97,7 +97,9 @@ __global__ __launch_bounds__(1024) void invert_kernel(const int32_t* __restrict_
 
 // ... and for a batch of many pairs, where every block reading every row's
 // pair would cost more than a second launch: clear, then enter the rows (the
-// larger one wins, whatever the order).
+// larger one wins, whatever the order).  us of a permute of 64 bf16, in blocks
+// and in two launches: 16384 pairs 6.4 and 7.5, 32768 7.8 and 8.4, 65536 11.1
+// and 11.1, 98304 15.2 and 13.7, 262144 44.0 and 29.4.
 constexpr int64_t kInvertInBlocks = 65536;
 __global__ __launch_bounds__(kThreads) void clear_pair_rows_kernel(int32_t* __restrict__ pair_rows, int64_t P) {
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < P; i += (int64_t)gridDim.x * kThreads)
@@ -404,6 +406,12 @@ unsigned block_count(int64_t work, int64_t per_block) {
 
 unsigned split_blocks(int64_t rows, const RowSplit& s) { return block_count(rows * s.segs, kThreads >> s.lg); }
 
+// Bytes of the rows from which a second launch, the pair list's, costs less
+// than reading x once for each pick (us in one launch, and by token with the
+// list before it: 512, 1024, 1456 and 4096 tokens, top 4, 2880 bf16 = 11, 22, 32
+// and 90 MiB: 6.0 and 6.5, 9.2 and 8.8, 11.7 and 11.2, 29.5 and 24.1; 8192
+// tokens, top 8, 512 bf16 = 64 MiB: 31.0 and 25.3; top 1 saves no read: 8192
+// tokens of 2880 = 45 MiB 18.8 and 20.4).
 constexpr int64_t kByTokenBytes = 32 << 20;
 
 template <typename E, int kN>
@@ -443,7 +451,12 @@ hipError_t unpermute(const void* rows, const int32_t* pair_rows, const float* we
   return hipGetLastError();
 }
 
-constexpr int kManyTokens = 4096;
+// Tokens from which a wave each fills the chip; below, four waves take one
+// token (us with four and with one: 256, 1024, 1536, 2048 and 4096 tokens, top
+// 4, 2880 bf16: 6.2 and 8.9, 11.4 and 12.0, 15.2 and 15.9, 22.6 and 21.7, 48.0
+// and 47.7; 1024 bf16, top 2, 512, 1536, 2048 and 4096 tokens: 4.2 and 4.4, 6.2
+// and 6.0, 8.5 and 6.8, 12.3 and 9.7).  Rows of up to 64 pieces are one wave's.
+constexpr int64_t kManyTokens = 2048;
 
 template <typename E, int kN>
 hipError_t unpermute_backward(const void* dy, const void* rows, const int32_t* sorted_pairs,
