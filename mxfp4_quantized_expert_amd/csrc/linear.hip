@@ -944,10 +944,8 @@ __device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][kMax], u32x4* c
     for (int s = 0; s < 4; ++s) {
       // From the second step on before the other block's loads and scales (16384 rows over 128 experts, 2880 x 2880: 356
       // us, without 380, from the first step on 369 and five registers spilled; dense 240, 262, 260; NVFP4 over 128
-      // experts 472 -> 487; forward: none, or worse).
-      if constexpr (!kNv) {
-        if (s == 1) __builtin_amdgcn_s_setprio(1);
-      }
+      // experts 388 and 404, dense 257 and 274; forward: none, or worse).
+      if (s == 1) __builtin_amdgcn_s_setprio(1);
       u32x4 op[2];
 #pragma unroll
       for (int p = 0; p < 4; ++p) {  // rows 2p, 2p + 1 of the eight
@@ -974,7 +972,7 @@ __device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][kMax], u32x4* c
           acc[e][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(mx::as_bf16x8(op[e]), mx::as_bf16x8(b[s][cb]),
                                                                acc[e][cb], 0, 0, 0);
     }
-    if constexpr (!kNv) __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_s_setprio(0);
   };
   // whole periods without an exit, as above
   for (; c0 + kStages <= chunks; c0 += kStages)
