@@ -422,6 +422,10 @@ def moe_nvfp4_forward(x: torch.Tensor, router_logits: torch.Tensor,
 
 
 # ---- the layer's steps as operators of their own
+#
+# They record nothing for autograd: no output requires a gradient, also where an input does.  A caller
+# that trains joins a call and its _backward in a torch.autograd.Function.  An output given as `out`
+# (d_rows, ...) must not overlap an input.
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
@@ -493,7 +497,8 @@ def moe_permute(x: torch.Tensor, sorted_pairs: torch.Tensor, top_k: int, out: Op
     """Token rows in expert order: rows[i] = x[sorted_pairs[i] // top_k] for x [T, H] (bfloat16,
     float16 or float32) and sorted_pairs [R] int32, as moe_mxfp4_route gives them; an entry
     outside [0, T * top_k) makes an empty row of zeros.  Returns (rows [R, H], pair_rows
-    [T * top_k] int32: every pair's row, -1 for none)."""
+    [T * top_k] int32: every pair's row, -1 for none).  The rows
+    never require a gradient: moe_permute_backward computes it."""
     if _host is not None and stream is None and out is None and pair_rows is None:
         got = _host.permute(x, sorted_pairs, top_k)
         if got is not None:  # None: not a plain call, or one to refuse
@@ -557,7 +562,8 @@ def moe_unpermute(rows: torch.Tensor, pair_rows: torch.Tensor, topk_weights: tor
     """The experts' rows summed back: y[t] = sum_j topk_weights[t, j] * rows[pair_rows[t * top_k + j]]
     over the pairs that have a row (fp32, rounded once).  rows [R, H] (bfloat16, float16 or
     float32), pair_rows [T * top_k] int32 of moe_permute, topk_weights [T, top_k] float32.
-    Returns y [T, H]."""
+    Returns y [T, H].  The output
+    never requires a gradient: moe_unpermute_backward computes it."""
     if _host is not None and stream is None and out is None:
         got = _host.unpermute(rows, pair_rows, topk_weights)
         if got is not None:  # None: not a plain call, or one to refuse
@@ -706,7 +712,8 @@ def moe_mxfp4_linear(x: torch.Tensor, blocks: torch.Tensor, scales: torch.Tensor
     and scales [N, K/32] uint8, bias [N] bfloat16.  Per expert: blocks [E, N, K/2], scales
     [E, N, K/32], bias [E, N] and expert_offsets [E + 1] int32 (expert e has the rows
     [offsets[e], offsets[e + 1]); rows outside them keep what `out` held, and without `out` hold
-    anything).  Returns y [R, N]."""
+    anything).  Returns y [R, N].  The output
+    never requires a gradient: moe_mxfp4_linear_backward computes it."""
     if _host is not None and stream is None and out is None:
         got = _host.linear(False, 32, x, blocks, scales, None, bias, expert_offsets)
         if got is not None:  # None: not a plain call, or one to refuse
@@ -721,7 +728,8 @@ def moe_nvfp4_linear(x: torch.Tensor, blocks: torch.Tensor, scales: torch.Tensor
                      bias: Optional[torch.Tensor] = None, expert_offsets: Optional[torch.Tensor] = None,
                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """moe_mxfp4_linear over NVFP4 weights: scales [..., N, K/16] uint8 (E4M3) and scale2 [E]
-    float32 ([1] dense), which multiplies the product before the bias."""
+    float32 ([1] dense), which multiplies the product before the bias.  The output
+    never requires a gradient: moe_nvfp4_linear_backward computes it."""
     if _host is not None and stream is None and out is None:
         got = _host.linear(False, 16, x, blocks, scales, scale2, bias, expert_offsets)
         if got is not None:  # None: not a plain call, or one to refuse

@@ -405,7 +405,7 @@ __global__ __launch_bounds__(512, 2) void linear_one_kernel(LinearArgs a) {
 // operands of eight n, one for each k: operand j multiplies with k = kCodes m
 // + j as its row m.  Waves split N and add their sums in LDS in wave order.
 // Bound: the weights' bytes, at 1.9 TB/s (128 rows over 32 experts, 2880 x
-// 2880: 74 us, where tiles take 41), and for a small matrix the latency of a
+// 2880: 74 us, where tiles take 45), and for a small matrix the latency of a
 // pass (300 rows over 8 experts, N = 1000, K = 736: 8.1 us MXFP4, 9.1 NVFP4, of
 // which an empty launch is 2.2).  Not better: codes through LDS by the load
 // unit, a quarter of the load instructions (9.3 and 10.2 us); 16 waves a block
@@ -545,12 +545,14 @@ struct ScaleBytes {
 // 16-byte pieces XOR-swizzled so that the 128-bit reads of consecutive rows
 // hit distinct banks; scale bytes go straight to registers, 24 of a row at a
 // time.  Two blocks a CU: one converts and waits while the other multiplies.
-// Token blocks of 32 without rows are neither read nor multiplied.  Bound: the
-// bf16 MFMA rate under the card's power limit.  16384 rows, 2880 x 2880: dense
-// 235 us = 1160 TFLOP/s, as a large library product reaches; over 128 experts
-// 365 us = 745 TFLOP/s, with tiles filled to 89 % and the weights from HBM (the
-// clock fell to 1.5 GHz there, 1.7 to 1.9 dense).  Few rows: 512, 2880 x 2880:
-// 19 us; 4096 over 128 experts: 171 us, the weights at 3.4 TB/s.
+// Token blocks of 32 without rows are neither read nor multiplied.  Bound, by
+// sizes at 2880 x 2880: many dense rows the bf16 MFMA rate (16384: 240 us = 1130
+// TFLOP/s, as a large library product reaches); over experts also the weights,
+// needed once each (128 experts of 128 rows: 296 us), the tiles' empty rows and
+// XCDs with less to do (128 experts at random: 360 us = 750 TFLOP/s; 4096 rows
+// over them: 170 us, the weights at 3.4 TB/s); few dense rows the chain of
+// chunks of one block (256 and 512: 20 and 21 us).  NVFP4 266, 335, 421, 213, 26
+// and 27 us: twice the vector instructions to convert a code.
 //
 // The stages are arrays of their own and the loop is unrolled over the period
 // of both rings: the compiler waits for every load into an array that an LDS
@@ -798,9 +800,10 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinearArgs a) {
 // (v_perm; NVFP4 rounds the pair itself, exactly) into an operand for the even
 // and one for the odd k.  The chunk's scales lie transposed in LDS as bf16
 // (exact), written one chunk ahead from bytes loaded one chunk before that.
-// Bound: as the forward tiles.  16384 rows, 2880 x 2880: dense 254 us = 1070
-// TFLOP/s, over 128 experts 365 us = 745; odd N (2883; dy through registers, in
-// tiles of 64 rows) 461; 4096 rows over 128 experts 170 us.
+// Bound: as the forward tiles.  16384 rows, 2880 x 2880: dense 245 us = 1110
+// TFLOP/s, over 128 experts 352 us = 770; odd N (2883; dy through registers, in
+// tiles of 64 rows) 460; 4096 rows over 128 experts 174 us (NVFP4 264, 394, 512
+// and 194).
 constexpr int kBackK = 256;
 
 // The ring of a kernel for up to kMax blocks of 32 rows: as many stages as
