@@ -424,8 +424,7 @@ def moe_nvfp4_forward(x: torch.Tensor, router_logits: torch.Tensor,
 # ---- the layer's steps as operators of their own
 #
 # They record nothing for autograd: no output requires a gradient, also where an input does.  A caller
-# that trains joins a call and its _backward in a torch.autograd.Function.  An output given as `out`
-# (d_rows, ...) must not overlap an input.
+# that trains joins a call and its _backward in a torch.autograd.Function.
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
@@ -475,6 +474,16 @@ def _check_on(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: tor
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _apart(out: torch.Tensor, name: str, *inputs):
+    """Refuses an output that shares memory with an input (None: none): rows are read and written in no order."""
+    a, n = out.data_ptr(), out.numel() * out.element_size()
+    for t in inputs:
+        if t is not None and n and t.numel():
+            b = t.data_ptr()
+            if a < b + t.numel() * t.element_size() and b < a + n:
+                raise ValueError(f"{name} shares memory with an input")
+
+
 def _element_type(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -518,10 +527,12 @@ def moe_permute(x: torch.Tensor, sorted_pairs: torch.Tensor, top_k: int, out: Op
         out = x.new_empty((R, H))
     else:
         _check_on(out, "out", x.dtype, (R, H), dev)
+        _apart(out, "out", x, sorted_pairs)
     if pair_rows is None:
         pair_rows = sorted_pairs.new_empty((T * top_k,))
     else:
         _check_on(pair_rows, "pair_rows", torch.int32, (T * top_k,), dev)
+        _apart(pair_rows, "pair_rows", x, sorted_pairs, out)
     st = load().moe_permute(x.data_ptr(), code, sorted_pairs.data_ptr(), T, H, top_k, R, out.data_ptr(),
                             pair_rows.data_ptr(), _current_stream(x))
     _raise("moe_permute", st)
@@ -551,6 +562,7 @@ def moe_permute_backward(d_rows: torch.Tensor, pair_rows: torch.Tensor, top_k: i
         out = d_rows.new_empty((T, H))
     else:
         _check_on(out, "out", d_rows.dtype, (T, H), dev)
+        _apart(out, "out", d_rows, pair_rows)
     st = load().moe_permute_backward(d_rows.data_ptr(), code, pair_rows.data_ptr(), T, H, top_k, R, out.data_ptr(),
                                      _current_stream(d_rows))
     _raise("moe_permute_backward", st)
@@ -582,6 +594,7 @@ def moe_unpermute(rows: torch.Tensor, pair_rows: torch.Tensor, topk_weights: tor
         out = rows.new_empty((T, H))
     else:
         _check_on(out, "out", rows.dtype, (T, H), dev)
+        _apart(out, "out", rows, pair_rows, topk_weights)
     st = load().moe_unpermute(rows.data_ptr(), code, pair_rows.data_ptr(), topk_weights.data_ptr(), T, H, top_k, R,
                               out.data_ptr(), _current_stream(rows))
     _raise("moe_unpermute", st)
@@ -615,10 +628,12 @@ def moe_unpermute_backward(dy: torch.Tensor, rows: torch.Tensor, sorted_pairs: t
         d_rows = rows.new_empty((R, H))
     else:
         _check_on(d_rows, "d_rows", rows.dtype, (R, H), dev)
+        _apart(d_rows, "d_rows", dy, rows, sorted_pairs, pair_rows, topk_weights)
     if d_weights is None:
         d_weights = topk_weights.new_empty((T, top_k))
     else:
         _check_on(d_weights, "d_weights", torch.float32, (T, top_k), dev)
+        _apart(d_weights, "d_weights", dy, rows, sorted_pairs, pair_rows, topk_weights, d_rows)
     st = load().moe_unpermute_backward(dy.data_ptr(), rows.data_ptr(), code, sorted_pairs.data_ptr(),
                                        pair_rows.data_ptr(), topk_weights.data_ptr(), T, H, top_k, R,
                                        d_rows.data_ptr(), d_weights.data_ptr(), _current_stream(rows))
@@ -648,6 +663,7 @@ def moe_route_backward(topk_ids: torch.Tensor, topk_weights: torch.Tensor, d_wei
         out = topk_weights.new_empty((T, num_experts))
     else:
         _check_on(out, "out", torch.float32, (T, num_experts), dev)
+        _apart(out, "out", topk_ids, topk_weights, d_weights)
     st = load().moe_route_backward(topk_ids.data_ptr(), topk_weights.data_ptr(), d_weights.data_ptr(), T,
                                    num_experts, top_k, out.data_ptr(), _current_stream(out))
     _raise("moe_route_backward", st)
@@ -693,6 +709,7 @@ def _linear(fn: str, forward: bool, group: int, rows, blocks, scales, scale2, bi
         out = rows.new_empty((R, give))
     else:
         _check_on(out, "out", torch.bfloat16, (R, give), rows.device)
+        _apart(out, "out", rows, blocks, scales, scale2, bias, expert_offsets)
     args = [rows.data_ptr(), blocks.data_ptr(), scales.data_ptr()]
     if group == 16:
         args.append(scale2.data_ptr())

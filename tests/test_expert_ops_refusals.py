@@ -137,3 +137,12 @@ def test_linear_binding_refusals():
         binding.moe_mxfp4_linear_backward(x, blocks[None], scales[None])
     with pytest.raises(ValueError, match="dimensions"):
         binding.moe_nvfp4_linear(x[0], blocks, scales, None)
+
+
+def test_shared_memory_is_seen():
+    flat = torch.zeros(32)
+    binding._apart(flat[:16], "out", flat[16:], None, flat[:0])
+    binding._apart(flat[:0], "out", flat)
+    for a, b in ((flat, flat), (flat[:17], flat[16:]), (flat[16:], flat[:17]), (flat[4:8], flat)):
+        with pytest.raises(ValueError, match="out shares memory"):
+            binding._apart(a, "out", torch.zeros(3), b)

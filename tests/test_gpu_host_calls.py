@@ -155,3 +155,40 @@ def test_torch_makes_the_outputs_where_a_mode_looks_at_them(gpu):
         y = gpu.moe_mxfp4_linear(x, blocks, scales, None, offsets)
     assert any("empty" in n for n in Seen.names)
     assert torch.equal(y[1:7], want)
+
+
+def test_outputs_that_share_memory_with_an_input_are_refused(gpu):
+    """The kernels read and write in no order of their own: such a call would race with itself."""
+    d, k, E = _inputs(T=8, H=64, k=1, N=64, K=64)
+    x, pairs, w, off = d["x"], d["pairs"], d["w"], d["off"].to(torch.int32)
+    pr = gpu.moe_permute(x, pairs, k)[1]
+    both = torch.zeros(2 * x.numel() - 8, dtype=x.dtype, device="cuda")
+    first, second = both[:x.numel()].view_as(x), both[x.numel() - 8:].view_as(x)  # overlapping by a piece
+    lx, ly = d["lx"], d["ly"]
+    calls = [
+        lambda: gpu.moe_permute(x, pairs, k, out=x),
+        lambda: gpu.moe_permute(first, pairs, k, out=second),
+        lambda: gpu.moe_permute(second, pairs, k, out=first),
+        lambda: gpu.moe_permute(x, pairs, k, pair_rows=pairs),
+        lambda: gpu.moe_permute_backward(x, pr, k, out=x),
+        lambda: gpu.moe_unpermute(x, pr, w, out=x),
+        lambda: gpu.moe_unpermute_backward(d["rows"], x, pairs, pr, w, d_rows=x),
+        lambda: gpu.moe_unpermute_backward(x, d["rows"], pairs, pr, w, d_rows=x),
+        lambda: gpu.moe_unpermute_backward(x, d["rows"], pairs, pr, w, d_weights=w),
+        lambda: gpu.moe_route_backward(d["ids"], w, d["dw"], 1, out=w),
+        lambda: gpu.moe_route_backward(d["ids"], w, d["dw"], 1, out=d["dw"]),
+        lambda: gpu.moe_mxfp4_linear(lx, d["blocks"], d["s32"], None, off, out=lx),
+        lambda: gpu.moe_nvfp4_linear(lx, d["blocks"], d["s16"], d["scale2"], None, off, out=lx),
+        lambda: gpu.moe_mxfp4_linear_backward(ly, d["blocks"], d["s32"], off, out=ly),
+        lambda: gpu.moe_nvfp4_linear_backward(ly, d["blocks"], d["s16"], d["scale2"], off, out=ly),
+    ]
+    before = {n: t.clone() for n, t in d.items()}
+    for i, f in enumerate(calls):
+        with pytest.raises(ValueError, match="shares memory"):
+            f()
+            pytest.fail(f"call {i} was taken")
+    assert all(torch.equal(d[n], t) for n, t in before.items())
+    ends = both[:x.numel() - 8].view(-1, 8)  # side by side is no overlap
+    rows, _ = gpu.moe_permute(ends, torch.arange(len(ends), device="cuda", dtype=torch.int32), 1,
+                              out=both[x.numel() - 8:][:ends.numel()].view_as(ends))
+    assert torch.equal(rows, ends)
