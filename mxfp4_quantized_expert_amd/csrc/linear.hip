@@ -1127,7 +1127,7 @@ hipError_t linear(LinearArgs a, hipStream_t stream) {
   const int64_t n_tiles = (a.N + kTileN - 1) / kTileN;
   const mxlinear::Sizes sizes = sizes_of(a, kNv);
   if (a.K <= kOneMaxK) {
-    const int rows = mxlinear::stream_tile_rows(sizes);
+    const int rows = mxlinear::stream_tile_rows(sizes, mxfp4moe::device_cu_count());
     if (rows == 4) return launch_one<kNv, 1>(a, stream);
     if (rows == 8) return launch_one<kNv, 2>(a, stream);
   }

@@ -95,25 +95,32 @@ inline TilePlan plan_tiles(const Sizes& s, bool forward, int most_rows, int64_t 
 }
 
 // Rows of the tiles of the kernel that streams the weights past rows kept in
-// registers (4 or 8), or 0 for the other kernels.  It pays where there is much
-// to stream for few rows; from 12.7 MB of weights on, by what was measured (us,
-// MXFP4, weights from HBM, tiles of 4 and 8 rows and the best of the others):
-//   one row, N = 4096, 8192, 12288 and 32768, K = 2880 (6, 13, 19 and 50 MB):
-//     5.6, 6.3, 7.4 and 13.2 | - | 4.7, 6.4, 10.0 and 23.2
-//   8 rows of the first and the last: - | 9.9 and 17.8 | 5.4 and 23.5
+// registers (4 or 8), or 0 for the other kernels: up to a mean of 2 rows an
+// expert (dense: 4 rows) in tiles of 4, up to 6 (dense: 8) in tiles of 8 (us,
+// MXFP4, 2880 x 2880, 32 experts, means of 2, 3, 6 and 8: 28, 33, 46 and 56 in
+// tiles of 4 | 31, 32, 38 and 44 in tiles of 8 | 46, 47, 48 and 48 by the best of
+// the others; 5760 x 2880, 8: 105 | 81 | 77).  Not where the 16-row kernel
+// passes K in one round and there is little to stream, though two row groups
+// and more for every CU (us, MXFP4, weights from HBM, streamed | 16-row kernel):
+//   one row, K = 2880, N = 736, 1440, 2880, 4096, 8192, 12288 and 32768: 3.4, 4.5,
+//     5.1, 5.7, 6.3, 7.4 and 13.2 | 4.0, 4.5, 4.6, 4.7, 6.4, 10.0 and 23.2
+//   8 rows, K = 2880, N = 736, 2880, 5760 and 32768: 4.7, 8.5, 14.3 and 17.8 | 4.7,
+//     5.4, 7.7 and 23.5
+//   one row, K = 4096 and 8192, N = 736 and 2880: 4.1, 6.1, 5.3 and 7.0 | 5.7, 5.9,
+//     9.1 and 9.5
 //   16 rows over 16 experts and over 8, 736 x 736 (5 MB) and 1440 x 2880 (18 MB):
-//     6.4 and 9.3 | - | 4.9 and 11.2
-// and up to a mean of 2 rows an expert (dense: 4) in tiles of 4, up to 6 (dense:
-// 8) in tiles of 8 (2880 x 2880, 32 experts, means of 2, 3, 6 and 8: 28, 33, 46
-// and 56 | 31, 32, 38 and 44 | 46, 47, 48 and 48; 5760 x 2880, 8: 105 | 81 | 77).
-constexpr double kStreamBytes = 12.7e6;
+//     6.4 and 9.3 | 4.9 and 11.2
 constexpr int kMeanOf4 = 2, kMeanOf8 = 6, kDenseOf4 = 4, kDenseOf8 = 8;
+constexpr double kStreamBytes = 12.7e6;
+constexpr int kFewRoundK = 8 * 3 * 128;  // of the 16-row kernel: eight waves, three chunks each
 
-inline int stream_tile_rows(const Sizes& s) {
-  if (used_experts(s) * weight_bytes(s) < kStreamBytes) return 0;
-  if (s.rows <= (s.grouped ? kMeanOf4 * s.experts : kDenseOf4)) return 4;
-  if (s.rows <= (s.grouped ? kMeanOf8 * s.experts : kDenseOf8)) return 8;
-  return 0;
+inline int stream_tile_rows(const Sizes& s, int64_t cus) {
+  const int rows = s.rows <= (s.grouped ? kMeanOf4 * s.experts : kDenseOf4)   ? 4
+                   : s.rows <= (s.grouped ? kMeanOf8 * s.experts : kDenseOf8) ? 8
+                                                                              : 0;
+  const bool little = used_experts(s) * weight_bytes(s) < kStreamBytes;
+  const bool groups = used_experts(s) * ((s.n + 3) / 4) >= 2.0 * cus;
+  return little && groups && s.k <= kFewRoundK ? 0 : rows;
 }
 
 }  // namespace mxlinear

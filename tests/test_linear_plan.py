@@ -23,7 +23,7 @@ extern "C" int plan(int64_t rows, int64_t n, int64_t k, int64_t experts, int nv,
   return p.pays ? p.rows : 0;
 }
 extern "C" int stream(int64_t rows, int64_t n, int64_t k, int64_t experts, int nv) {
-  return stream_tile_rows(Sizes{rows, n, k, experts > 0 ? experts : 1, experts > 0, nv != 0});
+  return stream_tile_rows(Sizes{rows, n, k, experts > 0 ? experts : 1, experts > 0, nv != 0}, 256);
 }
 """
 
@@ -101,6 +101,13 @@ def test_choices_where_both_sides_were_measured(plan, rows, n, k, experts, forwa
     (16, 5760, 2880, 32, 4),     # 24, 27, 45
     (192, 2880, 2880, 32, 8),    # 46, 38, 48
     (320, 5760, 2880, 32, 0),    # 126, 94, 78
+    (1, 736, 2880, 0, 4),        # 3.4, 4.3, 4.0: fewer row groups than CUs
+    (1, 2880, 4096, 0, 4),       # 5.9, 8.0, 6.0: two rounds of the 16-row kernel
+    (1, 736, 12288, 0, 4),       # 6.0, 7.2, 11.8
+    (2, 1440, 8192, 0, 4),       # 9.2, 11.0, 9.6
+    (8, 736, 4096, 0, 8),        # 6.2, 6.2, 7.0
+    (16, 736, 736, 16, 0),       # 6.4, 7.5, 4.9
+    (24, 1000, 736, 8, 0),       # 6.4, 7.0, 4.8
 ])
 @pytest.mark.parametrize("nv", [0, 1])
 def test_streaming_where_both_sides_were_measured(plan, rows, n, k, experts, good, nv):
