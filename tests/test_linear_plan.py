@@ -69,7 +69,7 @@ def test_dense_tiles(plan):
     # us in tiles of 32, 64 and 128 rows
     (832, 5760, 2880, 128, True, (32, 64)),      # 277, 279, 292
     (1536, 5760, 2880, 128, True, (32, 64)),     # 288, 291, 303
-    (3072, 2880, 2880, 128, True, (64,)),        # 166, 159, 167
+    (768, 5760, 2880, 32, True, (64,)),          # 88, 82, 94
     (1280, 5760, 2880, 32, True, (64, 128)),     # 121, 89, 94
     (1792, 5760, 2880, 32, False, (64,)),        # 149, 104, 117
     (1792, 2880, 2880, 32, False, (64,)),        # 79, 56, 61
