@@ -458,6 +458,161 @@ int moe_nvfp4_linear_backward(const uint16_t* dy, const uint8_t* blocks, const u
                               const int32_t* expert_offsets, int64_t R, int64_t K, int64_t N, int64_t E, uint16_t* dx,
                               void* stream);
 
+/*
+ * moe_rms_norm, moe_rms_norm_fp8 - the root-mean-square norm ahead of the
+ * router and the experts, with the residual's addition, its rows out in the
+ * input's type or in 8 bits; moe_rms_norm_backward its gradients:
+ *
+ *   s = x + residual, rounded to the rows' type (s = x without a residual)
+ *   r[t] = (sum_i s[t, i]^2 / H + eps)^(-1/2)
+ *   y[t, i] = s[t, i] * r[t] * weight[i]
+ *   backward: dx[t, i] = r * (weight_i dy_i - s_i r^2 sum_j(s_j weight_j dy_j) / H) + d_summed_i
+ *             d_weight[i] = sum_t dy[t, i] s[t, i] r[t]
+ *
+ *   x, residual, summed, y, dy, d_summed, dx [T, H]: all of one element type
+ *            (dtype), aligned to it.  residual NULL: none, and summed is not
+ *            written (the gradient then takes x as summed).  d_summed, the
+ *            gradient that reaches s past the norm, NULL: none.  dx is the
+ *            gradient of x and of the residual alike.
+ *   weight   [H] of type weight_dtype: dtype, or MXFP4MOE_F32
+ *   codes    [T, H], scales [T, ceil(H / 128)]: y in 8 bits as moe_fp8_quantize
+ *            makes them, from y in fp32.  The gradient takes the rounding to
+ *            8 bits as if it were none.
+ *   rstd     [T] float32 out, r for the gradient
+ *   d_weight [H] float32 out, written whole
+ *   workspace: of moe_rms_norm_backward, device scratch of at least
+ *            *workspace_bytes bytes, 4-byte aligned; with workspace == NULL the
+ *            call only stores the size it needs.
+ *   T < 2^31, 1 <= H <= MXFP4MOE_MAX_NORM, eps >= 0 and finite.  T == 0: the
+ *   norm is a no-op, the gradient clears d_weight.
+ * fp32 throughout with one rounding at the end (squares and sums overflow as
+ * fp32 does); sums in an order fixed by the sizes.  Outputs alias no input.
+ */
+#define MXFP4MOE_MAX_NORM 32768
+int moe_rms_norm(const void* x, const void* residual, const void* weight, int dtype, int weight_dtype, float eps,
+                 int64_t T, int64_t H, void* summed, void* y, float* rstd, void* stream);
+int moe_rms_norm_fp8(const void* x, const void* residual, const void* weight, int dtype, int weight_dtype, float eps,
+                     int64_t T, int64_t H, void* summed, uint8_t* codes, float* scales, float* rstd, void* stream);
+int moe_rms_norm_backward(const void* dy, const void* d_summed, const void* summed, const void* weight, int dtype,
+                          int weight_dtype, const float* rstd, int64_t T, int64_t H, void* dx, float* d_weight,
+                          void* workspace, size_t* workspace_bytes, void* stream);
+
+/*
+ * moe_fp8_quantize - rows in 8 bits: E4M3 codes (OCP, finite only, largest
+ * 448) with a float32 scale for each 128 elements of a row (the last block of
+ * a row may be shorter):
+ *
+ *   largest = max(max |x|, 2^-100) over the block;  scale = largest / 448
+ *   code = e4m3_rne(x * (448 / largest)), in fp32
+ *
+ *   x [R, K] of element type dtype, aligned to it; codes [R, K] uint8;
+ *   scales [R, ceil(K / 128)] float32.  1 <= K <= MXFP4MOE_MAX_ROW,
+ *   R * ceil(K / 128) < 2^31.  R == 0 is a no-op.
+ * A NaN makes its block's scale and codes NaN; with an infinity the scale is
+ * infinite, its code NaN and the codes of the block's finite elements 0.
+ */
+int moe_fp8_quantize(const void* x, int dtype, int64_t R, int64_t K, uint8_t* codes, float* scales, void* stream);
+
+/*
+ * moe_fp8_linear - rows in 8 bits times 8-bit weights with a scale for each
+ * block of 128, dense or with each row's expert, and moe_fp8_linear_backward,
+ * the gradient to the rows (the weights, scales and bias are frozen and have
+ * none):
+ *
+ *   linear:          y[r, n]  = sum_k (x_scales[r, k/128] x[r, k]) (w_scales[e, n/128, k/128] w[e, n, k]) + bias[e, n]
+ *   linear_backward: dx[r, k] = sum_n dy[r, n] (w_scales[e, n/128, k/128] w[e, n, k])
+ *
+ * What moe_mxfp4_linear is for 4-bit weights; expert_offsets, rows outside of
+ * every expert and the bias as there.
+ *
+ *   x        [R, K] E4M3 codes, 16-byte aligned; x_scales [R, ceil(K / 128)]
+ *            float32: as moe_fp8_quantize and the _fp8 calls write them
+ *   w        [E, N, K] E4M3 codes, 16-byte aligned
+ *   w_scales [E, ceil(N / 128), ceil(K / 128)] float32
+ *   bias     [E, N] bf16, or NULL for none
+ *   y, dy    [R, N] bf16, dx [R, K] bf16; 16-byte aligned
+ *   K a multiple of 16, any N; N, K <= MXFP4MOE_MAX_LINEAR, N * K < 2^31;
+ *   1 <= E <= MXFP4MOE_MAX_EXPERTS; 0 <= R < 2^31.  R == 0 is a no-op.
+ * Products of codes (of a code and dy) are exact.  The matrix instructions add
+ * each 128 of the sum in fp32, but moe_fp8_linear's, the FP8 one, first adds
+ * eight neighbouring products as integers in steps of 2^-13 of the largest's
+ * power of two and cuts off what lies below.  The 128 are multiplied by their
+ * scale (the product of their two scales, in fp32) and added, in fp32, in an
+ * order fixed by the sizes; one rounding to bf16 at the end.  A code 0x7F or
+ * 0xFF is NaN.  Outputs alias no input.
+ */
+int moe_fp8_linear(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales,
+                   const uint16_t* bias, const int32_t* expert_offsets, int64_t R, int64_t K, int64_t N, int64_t E,
+                   uint16_t* y, void* stream);
+int moe_fp8_linear_backward(const uint16_t* dy, const uint8_t* w, const float* w_scales,
+                            const int32_t* expert_offsets, int64_t R, int64_t K, int64_t N, int64_t E, uint16_t* dx,
+                            void* stream);
+
+/*
+ * moe_swiglu, moe_swiglu_fp8 - the experts' activation between the two
+ * products, its rows out in the input's type or in 8 bits, and
+ * moe_swiglu_backward, its gradient:
+ *
+ *   g = min(gate, limit), u = min(max(up, -limit), limit)
+ *   a = g * sigmoid(alpha * g) * (u + offset)
+ *   d_gate = da (u + offset) sigmoid(alpha g) (1 + alpha g (1 - sigmoid(alpha g))) where gate <= limit, else 0
+ *   d_up   = da g sigmoid(alpha g) where |up| <= limit, else 0
+ *
+ * moe_mxfp4_forward's activation has alpha 1.702, limit 7, offset 1; the plain
+ * gated SiLU alpha 1, limit infinity, offset 0.
+ *
+ *   h, dh [R, 2 I]: gate i and up i at 2i and 2i + 1, or with `split` at i and
+ *         I + i; a, da [R, I]; all of element type dtype, aligned to it
+ *   codes [R, I], scales [R, ceil(I / 128)]: a in 8 bits as moe_fp8_quantize
+ *         makes them, from a in fp32; the gradient takes that rounding as if
+ *         it were none
+ *   limit > 0 (or infinity), alpha and offset finite; 1 <= I <=
+ *   MXFP4MOE_MAX_ROW / 2, R * ceil(I / 128) < 2^31.  R == 0 is a no-op.
+ * fp32, one rounding at the end.  Outputs alias no input.
+ */
+int moe_swiglu(const void* h, int dtype, int64_t R, int64_t I, float alpha, float limit, float offset, int split,
+               void* a, void* stream);
+int moe_swiglu_fp8(const void* h, int dtype, int64_t R, int64_t I, float alpha, float limit, float offset, int split,
+                   uint8_t* codes, float* scales, void* stream);
+int moe_swiglu_backward(const void* da, const void* h, int dtype, int64_t R, int64_t I, float alpha, float limit,
+                        float offset, int split, void* dh, void* stream);
+
+/*
+ * moe_balance_loss - the router's balance loss with the experts' counts, and
+ * moe_balance_loss_backward, its gradient to the logits:
+ *
+ *   p[t] = softmax(router_logits[t]) (all zeros where every logit is -infinity)
+ *   counts[e]  = picks of expert e by the tokens that count
+ *   density[e] = E * (counts[e] / sum_j counts[j]) / (number of those tokens)
+ *   loss       = sum over those tokens and all experts of p[t, e] density[e],
+ *                i.e. E * sum_e (share of the picks)_e * (mean probability)_e
+ *   d_logits[t, e] = d_loss * p[t, e] * (density[e] - sum_j p[t, j] density[j]) for those tokens, 0 for the others,
+ *                    + add_to[t, e]
+ *
+ * The counts have no gradient, so density is all that the gradient needs of
+ * the batch.
+ *
+ *   router_logits [T, E] float32;  topk_ids [T, top_k] int32, as
+ *              moe_mxfp4_route writes them (an id outside [0, E) counts for none)
+ *   token_mask [T] bytes: tokens with a 0 count for nothing (a padded batch);
+ *              NULL: every token counts.  Without a token, or a pick, to
+ *              count loss and density are 0.
+ *   loss       [1] float32, counts [E] int32, density [E] float32: out
+ *   d_loss     [1] float32, on the device
+ *   add_to     [T, E] float32 or NULL, e.g. moe_route_backward's d_logits; may
+ *              be d_logits itself.  d_logits [T, E] float32 out
+ *   workspace  as moe_rms_norm_backward's; of 0 bytes for few tokens, then
+ *              workspace may be any non-NULL pointer
+ *   E, top_k, T as moe_mxfp4_route.  T == 0: loss, counts and density are 0.
+ * fp32, in an order fixed by the sizes.  Other outputs alias no input.
+ */
+int moe_balance_loss(const float* router_logits, const int32_t* topk_ids, const uint8_t* token_mask, int64_t T,
+                     int64_t E, int64_t top_k, float* loss, int32_t* counts, float* density, void* workspace,
+                     size_t* workspace_bytes, void* stream);
+int moe_balance_loss_backward(const float* router_logits, const float* density, const float* d_loss,
+                              const uint8_t* token_mask, const float* add_to, int64_t T, int64_t E, float* d_logits,
+                              void* stream);
+
 /* Short English text for a status code (static storage). */
 const char* mxfp4moe_status_string(int status);
 
@@ -471,7 +626,9 @@ const char* mxfp4moe_status_string(int status);
  * 13 the MXFP8 activation quantizer of the ACT flags, 14 permute,
  * 15 unpermute (and the gradient of permute), 16 the gradient of unpermute,
  * 17 the gradient of the routing softmax, 18 the linear product, 19 its
- * gradient.
+ * gradient, 20 and 21 the norm and its gradient, 22 and 23 the activation and
+ * its gradient, 24 the quantizer to 8 bits, 25 and 26 the 8-bit product and its
+ * gradient, 27 and 28 the balance loss and its gradient.
  * mxfp4moe_profile_end(ms, capacity) synchronises on the recorded events,
  * stores up to `capacity` per-launch durations in milliseconds (host array),
  * releases the events and returns how many were stored (negative on error).

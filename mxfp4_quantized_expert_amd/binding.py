@@ -32,7 +32,9 @@ STATUS = {
 STAGES = {"route": 1, "group": 2, "gate_up": 3, "down": 4, "combine": 5, "dequant": 6,
           "gate_up_wide": 7, "gate_up_stream": 8, "down_wide": 9, "down_stream": 10,
           "gate_up_mid": 11, "down_mid": 12, "act_quant": 13, "permute": 14, "unpermute": 15,
-          "unpermute_backward": 16, "route_backward": 17, "linear": 18, "linear_backward": 19}
+          "unpermute_backward": 16, "route_backward": 17, "linear": 18, "linear_backward": 19,
+          "rms_norm": 20, "rms_norm_backward": 21, "swiglu": 22, "swiglu_backward": 23, "fp8_quantize": 24,
+          "fp8_linear": 25, "fp8_linear_backward": 26, "balance_loss": 27, "balance_loss_backward": 28}
 
 _lib: Optional[ctypes.CDLL] = None
 # The module of the short host path (csrc/host_calls.cpp), set with _lib; without it, or with one that
@@ -105,6 +107,30 @@ def load() -> ctypes.CDLL:
     lib.moe_mxfp4_linear_backward.restype = ctypes.c_int
     lib.moe_nvfp4_linear_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]
     lib.moe_nvfp4_linear_backward.restype = ctypes.c_int
+    size_p = ctypes.POINTER(ctypes.c_size_t)
+    f32, i32 = ctypes.c_float, ctypes.c_int
+    lib.moe_rms_norm.argtypes = [_vp, _vp, _vp, i32, i32, f32, _i64, _i64, _vp, _vp, _vp, _vp]
+    lib.moe_rms_norm.restype = ctypes.c_int
+    lib.moe_rms_norm_fp8.argtypes = [_vp, _vp, _vp, i32, i32, f32, _i64, _i64, _vp, _vp, _vp, _vp, _vp]
+    lib.moe_rms_norm_fp8.restype = ctypes.c_int
+    lib.moe_rms_norm_backward.argtypes = [_vp, _vp, _vp, _vp, i32, i32, _vp, _i64, _i64, _vp, _vp, _vp, size_p, _vp]
+    lib.moe_rms_norm_backward.restype = ctypes.c_int
+    lib.moe_fp8_quantize.argtypes = [_vp, i32, _i64, _i64, _vp, _vp, _vp]
+    lib.moe_fp8_quantize.restype = ctypes.c_int
+    lib.moe_fp8_linear.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]
+    lib.moe_fp8_linear.restype = ctypes.c_int
+    lib.moe_fp8_linear_backward.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp]
+    lib.moe_fp8_linear_backward.restype = ctypes.c_int
+    lib.moe_swiglu.argtypes = [_vp, i32, _i64, _i64, f32, f32, f32, i32, _vp, _vp]
+    lib.moe_swiglu.restype = ctypes.c_int
+    lib.moe_swiglu_fp8.argtypes = [_vp, i32, _i64, _i64, f32, f32, f32, i32, _vp, _vp, _vp]
+    lib.moe_swiglu_fp8.restype = ctypes.c_int
+    lib.moe_swiglu_backward.argtypes = [_vp, _vp, i32, _i64, _i64, f32, f32, f32, i32, _vp, _vp]
+    lib.moe_swiglu_backward.restype = ctypes.c_int
+    lib.moe_balance_loss.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, size_p, _vp]
+    lib.moe_balance_loss.restype = ctypes.c_int
+    lib.moe_balance_loss_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp]
+    lib.moe_balance_loss_backward.restype = ctypes.c_int
     lib.mxfp4moe_status_string.argtypes = [ctypes.c_int]
     lib.mxfp4moe_status_string.restype = ctypes.c_char_p
     lib.mxfp4moe_profile_begin.argtypes = [ctypes.c_int, ctypes.c_int]
@@ -784,6 +810,391 @@ def moe_nvfp4_linear_backward(dy: torch.Tensor, blocks: torch.Tensor, scales: to
         with _place(dy, stream):
             return moe_nvfp4_linear_backward(dy, blocks, scales, scale2, expert_offsets, out)
     return _linear("moe_nvfp4_linear_backward", False, 16, dy, blocks, scales, scale2, None, expert_offsets, out)
+
+
+# ---- what stands around the expert products: the norm, rows and weights in 8 bits, the activation, the
+# balance loss.  As the operators above they record nothing for autograd.
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _blocks(n: int) -> int:
+    """Blocks of 128 elements that share a scale."""
+    return (n + 127) // 128
+
+
+def _workspace(fn, like: torch.Tensor, *args) -> tuple:
+    """(workspace tensor, its size as an argument) of a call that answers with its size first."""
+    n = ctypes.c_size_t(0)
+    _raise(f"{fn.__name__}(workspace query)", fn(*args, None, ctypes.byref(n), None))
+    return like.new_empty((max(n.value, 1),), dtype=torch.uint8), n
+
+
+def _out(out, name: str, dtype: torch.dtype, shape, like: torch.Tensor, *inputs) -> torch.Tensor:
+    """The caller's output after its checks, or a new one."""
+    if out is None:
+        return like.new_empty(shape, dtype=dtype)
+    _check_on(out, name, dtype, shape, like.device)
+    _apart(out, name, *inputs)
+    return out
+
+
+def _norm_inputs(x, weight, residual):
+    """(element type, weight's, T, H) after the checks of the norm's inputs."""
+    code = _element_type(x, "x")
+    T, H = x.shape
+    _check(x, "x", x.dtype)
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError("weight must be a torch.Tensor")
+    _check_on(weight, "weight", torch.float32 if weight.dtype is torch.float32 else x.dtype, (H,), x.device)
+    if residual is not None:
+        _check_on(residual, "residual", x.dtype, (T, H), x.device)
+    return code, _DTYPES[weight.dtype], T, H
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                 out: Optional[torch.Tensor] = None, summed: Optional[torch.Tensor] = None,
+                 rstd: Optional[torch.Tensor] = None, stream=None):
+    """The norm ahead of the layer: s = x + residual (rounded to x's type; x without a residual),
+    y = s / sqrt(mean(s^2) + eps) * weight over the rows of x [T, H] (bfloat16, float16 or float32;
+    weight [H] of x's type or float32).  Returns (y [T, H], s [T, H], rstd [T] float32); without a
+    residual s is x itself.  s and rstd are what moe_rms_norm_backward takes; no output ever
+    requires a gradient."""
+    if _host is not None and stream is None and out is None and summed is None and rstd is None:
+        got = _host.rms_norm(x, weight, residual, eps, False)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
+    if _elsewhere(x, stream):
+        with _place(x, stream):
+            return moe_rms_norm(x, weight, residual, eps, out, summed, rstd)
+    code, wcode, T, H = _norm_inputs(x, weight, residual)
+    out = _out(out, "out", x.dtype, (T, H), x, x, weight, residual)
+    if residual is not None:
+        summed = _out(summed, "summed", x.dtype, (T, H), x, x, weight, residual, out)
+    elif summed is not None:
+        raise ValueError("summed is written only with a residual")
+    rstd = _out(rstd, "rstd", torch.float32, (T,), x, x, weight, residual, out, summed)
+    st = load().moe_rms_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), code, wcode, eps, T, H, _ptr(summed),
+                             out.data_ptr(), rstd.data_ptr(), _current_stream(x))
+    _raise("moe_rms_norm", st)
+    return out, x if residual is None else summed, rstd
+
+
+def moe_rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                     eps: float = 1e-5, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                     summed: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None, stream=None):
+    """moe_rms_norm with its rows in 8 bits: returns (codes [T, H] float8_e4m3fn, scales
+    [T, ceil(H / 128)] float32, s [T, H], rstd [T]), codes and scales as moe_fp8_quantize makes them
+    of the norm's float32 values.  The gradient is moe_rms_norm_backward's: the rounding to 8 bits
+    counts as none."""
+    plain = codes is None and scales is None and summed is None and rstd is None
+    if _host is not None and stream is None and plain:
+        got = _host.rms_norm(x, weight, residual, eps, True)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
+    if _elsewhere(x, stream):
+        with _place(x, stream):
+            return moe_rms_norm_fp8(x, weight, residual, eps, codes, scales, summed, rstd)
+    code, wcode, T, H = _norm_inputs(x, weight, residual)
+    codes = _out(codes, "codes", _E4M3, (T, H), x, x, weight, residual)
+    scales = _out(scales, "scales", torch.float32, (T, _blocks(H)), x, x, weight, residual, codes)
+    if residual is not None:
+        summed = _out(summed, "summed", x.dtype, (T, H), x, x, weight, residual, codes, scales)
+    elif summed is not None:
+        raise ValueError("summed is written only with a residual")
+    rstd = _out(rstd, "rstd", torch.float32, (T,), x, x, weight, residual, codes, scales, summed)
+    st = load().moe_rms_norm_fp8(x.data_ptr(), _ptr(residual), weight.data_ptr(), code, wcode, eps, T, H,
+                                 _ptr(summed), codes.data_ptr(), scales.data_ptr(), rstd.data_ptr(),
+                                 _current_stream(x))
+    _raise("moe_rms_norm_fp8", st)
+    return codes, scales, x if residual is None else summed, rstd
+
+
+def moe_rms_norm_backward(dy: torch.Tensor, summed: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                          d_summed: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                          d_weight: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of moe_rms_norm and moe_rms_norm_fp8 for dy [T, H]: (dx [T, H], d_weight [H] float32).
+    dx is the gradient of x and of the residual alike; d_summed [T, H] is what reaches s past the
+    norm (the residual stream's gradient) and is added to it."""
+    if _host is not None and stream is None and dx is None and d_weight is None:
+        got = _host.rms_norm_backward(dy, summed, weight, rstd, d_summed)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
+    if _elsewhere(dy, stream):
+        with _place(dy, stream):
+            return moe_rms_norm_backward(dy, summed, weight, rstd, d_summed, dx, d_weight)
+    code = _element_type(dy, "dy")
+    T, H = dy.shape
+    _check(dy, "dy", dy.dtype)
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError("weight must be a torch.Tensor")
+    _check_on(summed, "summed", dy.dtype, (T, H), dy.device)
+    _check_on(weight, "weight", torch.float32 if weight.dtype is torch.float32 else dy.dtype, (H,), dy.device)
+    _check_on(rstd, "rstd", torch.float32, (T,), dy.device)
+    if d_summed is not None:
+        _check_on(d_summed, "d_summed", dy.dtype, (T, H), dy.device)
+    dx = _out(dx, "dx", dy.dtype, (T, H), dy, dy, summed, weight, rstd, d_summed)
+    d_weight = _out(d_weight, "d_weight", torch.float32, (H,), dy, dy, summed, weight, rstd, d_summed, dx)
+    fn = load().moe_rms_norm_backward
+    wcode = _DTYPES[weight.dtype]
+    workspace, n = _workspace(fn, dy, None, None, None, None, code, wcode, None, T, H, None, None)
+    st = fn(dy.data_ptr(), _ptr(d_summed), summed.data_ptr(), weight.data_ptr(), code, wcode, rstd.data_ptr(), T, H,
+            dx.data_ptr(), d_weight.data_ptr(), workspace.data_ptr(), ctypes.byref(n), _current_stream(dy))
+    _raise("moe_rms_norm_backward", st)
+    return dx, d_weight
+
+
+def moe_fp8_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                     stream=None):
+    """Rows [R, K] (bfloat16, float16 or float32) in 8 bits: (codes [R, K] float8_e4m3fn, scales
+    [R, ceil(K / 128)] float32), scale = largest magnitude of 128 elements / 448 and code = element /
+    scale to nearest.  (moe_permute moves such rows too, as the two-byte type of half their width:
+    codes.view(torch.float16).)"""
+    if _host is not None and stream is None and codes is None and scales is None:
+        got = _host.fp8_quantize(x)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
+    if _elsewhere(x, stream):
+        with _place(x, stream):
+            return moe_fp8_quantize(x, codes, scales)
+    code = _element_type(x, "x")
+    R, K = x.shape
+    _check(x, "x", x.dtype)
+    codes = _out(codes, "codes", _E4M3, (R, K), x, x)
+    scales = _out(scales, "scales", torch.float32, (R, _blocks(K)), x, x, codes)
+    st = load().moe_fp8_quantize(x.data_ptr(), code, R, K, codes.data_ptr(), scales.data_ptr(), _current_stream(x))
+    _raise("moe_fp8_quantize", st)
+    return codes, scales
+
+
+def _fp8_weights(rows, name: str, row_type: torch.dtype, weight, weight_scales, bias, expert_offsets):
+    """(E, N, K) of an 8-bit linear operator, after the checks of every tensor but the rows' width."""
+    if not isinstance(rows, torch.Tensor) or not isinstance(weight, torch.Tensor):
+        raise TypeError(f"{name} and weight must be torch.Tensors")
+    lead = 2 if expert_offsets is None else 3
+    shape = weight.shape
+    if rows.dim() != 2:
+        raise ValueError(f"{name} has {rows.dim()} dimensions, expected 2")
+    if len(shape) != lead:
+        raise ValueError(f"weight has {len(shape)} dimensions, expected {lead} "
+                         f"{'without' if lead == 2 else 'with'} expert_offsets")
+    E = 1 if lead == 2 else shape[0]
+    N, K = shape[-2:]
+    dev = rows.device
+    _check(rows, name, row_type)
+    _check_on(weight, "weight", _E4M3, shape, dev)
+    _check_on(weight_scales, "weight_scales", torch.float32, (*shape[:-2], _blocks(N), _blocks(K)), dev)
+    if expert_offsets is not None:
+        _check_on(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev)
+    if bias is not None:
+        _check_on(bias, "bias", torch.bfloat16, shape[:-1], dev)
+    return E, N, K
+
+
+def moe_fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, weight: torch.Tensor, weight_scales: torch.Tensor,
+                   bias: Optional[torch.Tensor] = None, expert_offsets: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rows in 8 bits times 8-bit weights with a scale for each block of 128: y = x W^T (+ bias).
+    x [R, K] float8_e4m3fn with x_scales [R, ceil(K / 128)] float32, as moe_fp8_quantize and the _fp8
+    calls make them.  Dense: weight [N, K] float8_e4m3fn, weight_scales [ceil(N / 128), ceil(K / 128)]
+    float32, bias [N] bfloat16.  Per expert: weight [E, N, K], weight_scales [E, ., .], bias [E, N] and
+    expert_offsets [E + 1] int32 as in moe_mxfp4_linear (rows of no expert keep what `out` held, and
+    without `out` hold anything).  K is a multiple of 16.  Returns y [R, N] bfloat16, which never
+    requires a gradient: moe_fp8_linear_backward computes it."""
+    if _host is not None and stream is None and out is None:
+        got = _host.fp8_linear(x, x_scales, weight, weight_scales, bias, expert_offsets)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
+    if _elsewhere(x, stream):
+        with _place(x, stream):
+            return moe_fp8_linear(x, x_scales, weight, weight_scales, bias, expert_offsets, out)
+    E, N, K = _fp8_weights(x, "x", _E4M3, weight, weight_scales, bias, expert_offsets)
+    R, width = x.shape
+    if width != K:
+        raise ValueError(f"x has rows of {width}, expected {K}")
+    _check_on(x_scales, "x_scales", torch.float32, (R, _blocks(K)), x.device)
+    out = _out(out, "out", torch.bfloat16, (R, N), x, x, x_scales, weight, weight_scales, bias, expert_offsets)
+    st = load().moe_fp8_linear(x.data_ptr(), x_scales.data_ptr(), weight.data_ptr(), weight_scales.data_ptr(),
+                               _ptr(bias), _ptr(expert_offsets), R, K, N, E, out.data_ptr(), _current_stream(x))
+    _raise("moe_fp8_linear", st)
+    return out
+
+
+def moe_fp8_linear_backward(dy: torch.Tensor, weight: torch.Tensor, weight_scales: torch.Tensor,
+                            expert_offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                            stream=None) -> torch.Tensor:
+    """Gradient of moe_fp8_linear to its rows (as they were before they went to 8 bits): dx = dy W for
+    dy [R, N] bfloat16 (weights and offsets as there; the weights are frozen).  Returns dx [R, K]
+    bfloat16."""
+    if _host is not None and stream is None and out is None:
+        got = _host.fp8_linear_backward(dy, weight, weight_scales, expert_offsets)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
+    if _elsewhere(dy, stream):
+        with _place(dy, stream):
+            return moe_fp8_linear_backward(dy, weight, weight_scales, expert_offsets, out)
+    E, N, K = _fp8_weights(dy, "dy", torch.bfloat16, weight, weight_scales, None, expert_offsets)
+    R, width = dy.shape
+    if width != N:
+        raise ValueError(f"dy has rows of {width}, expected {N}")
+    out = _out(out, "out", torch.bfloat16, (R, K), dy, dy, weight, weight_scales, expert_offsets)
+    st = load().moe_fp8_linear_backward(dy.data_ptr(), weight.data_ptr(), weight_scales.data_ptr(),
+                                        _ptr(expert_offsets), R, K, N, E, out.data_ptr(), _current_stream(dy))
+    _raise("moe_fp8_linear_backward", st)
+    return out
+
+
+def _pairs_of(h):
+    """(element type, R, I) of rows of gates and ups."""
+    code = _element_type(h, "h")
+    R, width = h.shape
+    if width % 2:
+        raise ValueError(f"h has rows of {width}, not of gates and ups")
+    _check(h, "h", h.dtype)
+    return code, R, width // 2
+
+
+def moe_swiglu(h: torch.Tensor, split: bool = False, alpha: float = 1.702, limit: float = 7.0, offset: float = 1.0,
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The experts' activation: a = g sigmoid(alpha g) (u + offset) with g = min(gate, limit) and
+    u = clamp(up, -limit, limit) for h [R, 2 I] (bfloat16, float16 or float32), gate and up side by
+    side or, with split, in two halves of a row.  The defaults are the fused layer's; the plain gated
+    SiLU is alpha=1, limit=math.inf, offset=0.  Returns a [R, I], which never requires a gradient:
+    moe_swiglu_backward computes it."""
+    if _host is not None and stream is None and out is None:
+        got = _host.swiglu(h, split, alpha, limit, offset, False)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
+    if _elsewhere(h, stream):
+        with _place(h, stream):
+            return moe_swiglu(h, split, alpha, limit, offset, out)
+    code, R, I = _pairs_of(h)
+    out = _out(out, "out", h.dtype, (R, I), h, h)
+    st = load().moe_swiglu(h.data_ptr(), code, R, I, alpha, limit, offset, 1 if split else 0, out.data_ptr(),
+                           _current_stream(h))
+    _raise("moe_swiglu", st)
+    return out
+
+
+def moe_swiglu_fp8(h: torch.Tensor, split: bool = False, alpha: float = 1.702, limit: float = 7.0,
+                   offset: float = 1.0, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                   stream=None):
+    """moe_swiglu with its rows in 8 bits: returns (codes [R, I] float8_e4m3fn, scales [R, ceil(I / 128)]
+    float32) as moe_fp8_quantize makes them of the activation's float32 values.  The gradient is
+    moe_swiglu_backward's: the rounding to 8 bits counts as none."""
+    if _host is not None and stream is None and codes is None and scales is None:
+        got = _host.swiglu(h, split, alpha, limit, offset, True)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
+    if _elsewhere(h, stream):
+        with _place(h, stream):
+            return moe_swiglu_fp8(h, split, alpha, limit, offset, codes, scales)
+    code, R, I = _pairs_of(h)
+    codes = _out(codes, "codes", _E4M3, (R, I), h, h)
+    scales = _out(scales, "scales", torch.float32, (R, _blocks(I)), h, h, codes)
+    st = load().moe_swiglu_fp8(h.data_ptr(), code, R, I, alpha, limit, offset, 1 if split else 0, codes.data_ptr(),
+                               scales.data_ptr(), _current_stream(h))
+    _raise("moe_swiglu_fp8", st)
+    return codes, scales
+
+
+def moe_swiglu_backward(da: torch.Tensor, h: torch.Tensor, split: bool = False, alpha: float = 1.702,
+                        limit: float = 7.0, offset: float = 1.0, out: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """Gradient of moe_swiglu and moe_swiglu_fp8 for da [R, I] (h's type): dh [R, 2 I] in h's layout, 0
+    for gates past the limit and ups past the limits."""
+    if _host is not None and stream is None and out is None:
+        got = _host.swiglu_backward(da, h, split, alpha, limit, offset)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
+    if _elsewhere(h, stream):
+        with _place(h, stream):
+            return moe_swiglu_backward(da, h, split, alpha, limit, offset, out)
+    code, R, I = _pairs_of(h)
+    _check_on(da, "da", h.dtype, (R, I), h.device)
+    out = _out(out, "out", h.dtype, (R, 2 * I), h, h, da)
+    st = load().moe_swiglu_backward(da.data_ptr(), h.data_ptr(), code, R, I, alpha, limit, offset, 1 if split else 0,
+                                    out.data_ptr(), _current_stream(h))
+    _raise("moe_swiglu_backward", st)
+    return out
+
+
+def _logits_of(router_logits, token_mask):
+    """(T, E) after the checks of the logits and the mask."""
+    if not isinstance(router_logits, torch.Tensor):
+        raise TypeError("router_logits must be a torch.Tensor")
+    if router_logits.dim() != 2:
+        raise ValueError(f"router_logits has {router_logits.dim()} dimensions, expected 2")
+    T, E = router_logits.shape
+    _check(router_logits, "router_logits", torch.float32)
+    if token_mask is not None:
+        _check_on(token_mask, "token_mask", torch.bool, (T,), router_logits.device)
+    return T, E
+
+
+def moe_balance_loss(router_logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: Optional[torch.Tensor] = None,
+                     stream=None):
+    """The router's balance loss: E * sum over experts of (its share of the picks) * (its mean
+    probability), over the tokens whose token_mask [T] (bool) is True (None: every token).
+    router_logits [T, E] float32, topk_ids [T, top_k] int32.  Returns (loss [] float32, counts [E]
+    int32, density [E] float32): the picks of every expert, and what moe_balance_loss_backward takes.
+    No output ever requires a gradient."""
+    if _host is not None and stream is None:
+        got = _host.balance_loss(router_logits, topk_ids, token_mask)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
+    if _elsewhere(router_logits, stream):
+        with _place(router_logits, stream):
+            return moe_balance_loss(router_logits, topk_ids, token_mask)
+    T, E = _logits_of(router_logits, token_mask)
+    if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be a tensor of two dimensions")
+    top_k = topk_ids.shape[1]
+    _check_on(topk_ids, "topk_ids", torch.int32, (T, top_k), router_logits.device)
+    loss, density = router_logits.new_empty(()), router_logits.new_empty((E,))
+    counts = topk_ids.new_empty((E,))
+    fn = load().moe_balance_loss
+    workspace, n = _workspace(fn, router_logits, None, None, None, T, E, top_k, None, None, None)
+    st = fn(router_logits.data_ptr(), topk_ids.data_ptr(), _ptr(token_mask), T, E, top_k, loss.data_ptr(),
+            counts.data_ptr(), density.data_ptr(), workspace.data_ptr(), ctypes.byref(n),
+            _current_stream(router_logits))
+    _raise("moe_balance_loss", st)
+    return loss, counts, density
+
+
+def moe_balance_loss_backward(router_logits: torch.Tensor, density: torch.Tensor, d_loss: torch.Tensor,
+                              token_mask: Optional[torch.Tensor] = None, add_to: Optional[torch.Tensor] = None,
+                              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of moe_balance_loss to the logits, [T, E] float32, for d_loss (a float32 device tensor
+    of one element) and density [E] as moe_balance_loss made it; added to add_to [T, E] where that is
+    given (moe_route_backward's gradient of the same logits).  out may be add_to itself."""
+    if _host is not None and stream is None and out is None:
+        got = _host.balance_loss_backward(router_logits, density, d_loss, token_mask, add_to)
+        if got is not None:  # None: not a plain call, or one to refuse
+            return got
+    if _elsewhere(router_logits, stream):
+        with _place(router_logits, stream):
+            return moe_balance_loss_backward(router_logits, density, d_loss, token_mask, add_to, out)
+    T, E = _logits_of(router_logits, token_mask)
+    dev = router_logits.device
+    _check_on(density, "density", torch.float32, (E,), dev)
+    if not isinstance(d_loss, torch.Tensor) or d_loss.numel() != 1:
+        raise ValueError("d_loss must be a tensor of one element")
+    _check_on(d_loss, "d_loss", torch.float32, d_loss.shape, dev)
+    if add_to is not None:
+        _check_on(add_to, "add_to", torch.float32, (T, E), dev)
+    same = out is not None and add_to is not None and out.data_ptr() == add_to.data_ptr()
+    out = _out(out, "out", torch.float32, (T, E), router_logits, router_logits, density, d_loss, token_mask,
+               None if same else add_to)
+    st = load().moe_balance_loss_backward(router_logits.data_ptr(), density.data_ptr(), d_loss.data_ptr(),
+                                          _ptr(token_mask), _ptr(add_to), T, E, out.data_ptr(),
+                                          _current_stream(router_logits))
+    _raise("moe_balance_loss_backward", st)
+    return out
 
 
 def profile_begin(stage: str, max_calls: int) -> None:

@@ -147,6 +147,60 @@ int check_linear(const void* in, const void* blocks, const void* scales, const v
   return MXFP4MOE_OK;
 }
 
+// Sizes and types of the norm and its gradient.
+int check_norm(int dtype, int weight_dtype, int64_t T, int64_t H) {
+  if (dtype < kBf16 || dtype > kF32 || (weight_dtype != dtype && weight_dtype != kF32)) return MXFP4MOE_ERR_ARG;
+  if (T < 0 || T > (int64_t)0x7fffffff || H < 1 || H > MXFP4MOE_MAX_NORM) return MXFP4MOE_ERR_SHAPE;
+  return MXFP4MOE_OK;
+}
+
+int check_norm_forward(const void* x, const void* residual, const void* weight, int dtype, int weight_dtype, float eps,
+                       int64_t T, int64_t H, const void* summed, const float* rstd) {
+  int st = check_norm(dtype, weight_dtype, T, H);
+  if (st != MXFP4MOE_OK) return st;
+  if (!(eps >= 0.f) || eps > 3.4e38f) return MXFP4MOE_ERR_ARG;
+  if (T == 0) return MXFP4MOE_OK;
+  if (x == nullptr || weight == nullptr || rstd == nullptr || (residual != nullptr && summed == nullptr))
+    return MXFP4MOE_ERR_ARG;
+  const size_t el = element_bytes(dtype);
+  if (!aligned_to(x, el) || !aligned_to(residual, el) || !aligned_to(summed, el) ||
+      !aligned_to(weight, element_bytes(weight_dtype)) || !aligned_to(rstd, 4))
+    return MXFP4MOE_ERR_ALIGN;
+  return MXFP4MOE_OK;
+}
+
+// Rows that go in blocks of 128 elements.
+int check_blocks(int dtype, int64_t R, int64_t width, int64_t most) {
+  if (dtype < kBf16 || dtype > kF32) return MXFP4MOE_ERR_ARG;
+  if (R < 0 || width < 1 || width > most || R > (int64_t)0x7fffffff / ((width + 127) / 128)) return MXFP4MOE_ERR_SHAPE;
+  return MXFP4MOE_OK;
+}
+
+int check_swiglu(const void* h, int dtype, int64_t R, int64_t I, float alpha, float limit, float offset) {
+  int st = check_blocks(dtype, R, I, MXFP4MOE_MAX_ROW / 2);
+  if (st != MXFP4MOE_OK) return st;
+  constexpr float kMost = 3.4e38f;
+  if (!(limit > 0.f) || !(alpha >= -kMost && alpha <= kMost) || !(offset >= -kMost && offset <= kMost))
+    return MXFP4MOE_ERR_ARG;
+  if (R > 0 && h == nullptr) return MXFP4MOE_ERR_ARG;
+  return aligned_to(h, element_bytes(dtype)) ? MXFP4MOE_OK : MXFP4MOE_ERR_ALIGN;
+}
+
+// Sizes and pointers of the 8-bit linear operators; `in` and `out` are the rows read and written.
+int check_fp8_linear(const void* in, const void* w, const void* w_scales, const void* offsets, const void* out,
+                     int64_t R, int64_t K, int64_t N, int64_t E) {
+  if (R < 0 || R > (int64_t)0x7fffffff || N < 1 || K < 16 || (K & 15) != 0) return MXFP4MOE_ERR_SHAPE;
+  if (N > MXFP4MOE_MAX_LINEAR || K > MXFP4MOE_MAX_LINEAR || N > (int64_t)0x7fffffff / K) return MXFP4MOE_ERR_SHAPE;
+  if (E < 1 || E > MXFP4MOE_MAX_EXPERTS) return MXFP4MOE_ERR_SHAPE;
+  if (offsets == nullptr && E != 1) return MXFP4MOE_ERR_ARG;
+  if (R == 0) return MXFP4MOE_OK;
+  if (in == nullptr || w == nullptr || w_scales == nullptr || out == nullptr) return MXFP4MOE_ERR_ARG;
+  if (!aligned_to(in, 16) || !aligned_to(w, 16) || !aligned_to(out, 16) || !aligned_to(w_scales, 4) ||
+      !aligned_to(offsets, 4))
+    return MXFP4MOE_ERR_ALIGN;
+  return MXFP4MOE_OK;
+}
+
 int check_route_shape(int64_t T, int64_t E, int64_t top_k) {
   if (T < 0 || E < 1 || E > MXFP4MOE_MAX_EXPERTS) return MXFP4MOE_ERR_SHAPE;
   if (top_k < 1 || top_k > E || top_k > MXFP4MOE_MAX_TOPK) return MXFP4MOE_ERR_SHAPE;
@@ -617,6 +671,154 @@ int moe_nvfp4_linear_backward(const uint16_t* dy, const uint8_t* blocks, const u
   if (!aligned_to(scale2, 4)) return MXFP4MOE_ERR_ALIGN;
   hipError_t err =
       launch_linear_backward(dy, blocks, scales, scale2, expert_offsets, R, K, N, E, dx, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_rms_norm(const void* x, const void* residual, const void* weight, int dtype, int weight_dtype, float eps,
+                 int64_t T, int64_t H, void* summed, void* y, float* rstd, void* stream) {
+  int st = check_norm_forward(x, residual, weight, dtype, weight_dtype, eps, T, H, summed, rstd);
+  if (st != MXFP4MOE_OK || T == 0) return st;
+  if (y == nullptr) return MXFP4MOE_ERR_ARG;
+  if (!aligned_to(y, element_bytes(dtype))) return MXFP4MOE_ERR_ALIGN;
+  hipError_t err = launch_rms_norm(x, residual, weight, dtype, weight_dtype, eps, T, H, summed, y, nullptr, nullptr,
+                                   rstd, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_rms_norm_fp8(const void* x, const void* residual, const void* weight, int dtype, int weight_dtype, float eps,
+                     int64_t T, int64_t H, void* summed, uint8_t* codes, float* scales, float* rstd, void* stream) {
+  int st = check_norm_forward(x, residual, weight, dtype, weight_dtype, eps, T, H, summed, rstd);
+  if (st != MXFP4MOE_OK || T == 0) return st;
+  if (codes == nullptr || scales == nullptr) return MXFP4MOE_ERR_ARG;
+  if (!aligned_to(scales, 4)) return MXFP4MOE_ERR_ALIGN;
+  hipError_t err = launch_rms_norm(x, residual, weight, dtype, weight_dtype, eps, T, H, summed, nullptr, codes, scales,
+                                   rstd, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_rms_norm_backward(const void* dy, const void* d_summed, const void* summed, const void* weight, int dtype,
+                          int weight_dtype, const float* rstd, int64_t T, int64_t H, void* dx, float* d_weight,
+                          void* workspace, size_t* workspace_bytes, void* stream) {
+  int st = check_norm(dtype, weight_dtype, T, H);
+  if (st != MXFP4MOE_OK) return st;
+  if (workspace_bytes == nullptr) return MXFP4MOE_ERR_ARG;
+  const size_t need = rms_norm_backward_workspace(dtype, T, H);
+  if (workspace == nullptr) {
+    *workspace_bytes = need;
+    return MXFP4MOE_OK;
+  }
+  if (d_weight == nullptr ||
+      (T > 0 && (dy == nullptr || summed == nullptr || weight == nullptr || rstd == nullptr || dx == nullptr)))
+    return MXFP4MOE_ERR_ARG;
+  if (*workspace_bytes < need) return MXFP4MOE_ERR_WORKSPACE;
+  const size_t el = element_bytes(dtype);
+  if (!aligned_to(dy, el) || !aligned_to(d_summed, el) || !aligned_to(summed, el) || !aligned_to(dx, el) ||
+      !aligned_to(weight, element_bytes(weight_dtype)) || !aligned_to(rstd, 4) || !aligned_to(d_weight, 4) ||
+      !aligned_to(workspace, 4))
+    return MXFP4MOE_ERR_ALIGN;
+  hipError_t err = launch_rms_norm_backward(dy, d_summed, summed, weight, dtype, weight_dtype, rstd, T, H, dx, d_weight,
+                                            static_cast<float*>(workspace), (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_fp8_quantize(const void* x, int dtype, int64_t R, int64_t K, uint8_t* codes, float* scales, void* stream) {
+  int st = check_blocks(dtype, R, K, MXFP4MOE_MAX_ROW);
+  if (st != MXFP4MOE_OK || R == 0) return st;
+  if (x == nullptr || codes == nullptr || scales == nullptr) return MXFP4MOE_ERR_ARG;
+  if (!aligned_to(x, element_bytes(dtype)) || !aligned_to(scales, 4)) return MXFP4MOE_ERR_ALIGN;
+  hipError_t err = launch_fp8_quantize(x, dtype, R, K, codes, scales, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_fp8_linear(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales,
+                   const uint16_t* bias, const int32_t* expert_offsets, int64_t R, int64_t K, int64_t N, int64_t E,
+                   uint16_t* y, void* stream) {
+  int st = check_fp8_linear(x, w, w_scales, expert_offsets, y, R, K, N, E);
+  if (st != MXFP4MOE_OK || R == 0) return st;
+  if (x_scales == nullptr) return MXFP4MOE_ERR_ARG;
+  if (!aligned_to(x_scales, 4) || !aligned_to(bias, 2)) return MXFP4MOE_ERR_ALIGN;
+  hipError_t err =
+      launch_fp8_linear(x, x_scales, w, w_scales, bias, expert_offsets, R, K, N, E, y, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_fp8_linear_backward(const uint16_t* dy, const uint8_t* w, const float* w_scales, const int32_t* expert_offsets,
+                            int64_t R, int64_t K, int64_t N, int64_t E, uint16_t* dx, void* stream) {
+  int st = check_fp8_linear(dy, w, w_scales, expert_offsets, dx, R, K, N, E);
+  if (st != MXFP4MOE_OK || R == 0) return st;
+  hipError_t err = launch_fp8_linear_backward(dy, w, w_scales, expert_offsets, R, K, N, E, dx, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_swiglu(const void* h, int dtype, int64_t R, int64_t I, float alpha, float limit, float offset, int split,
+               void* a, void* stream) {
+  int st = check_swiglu(h, dtype, R, I, alpha, limit, offset);
+  if (st != MXFP4MOE_OK || R == 0) return st;
+  if (a == nullptr) return MXFP4MOE_ERR_ARG;
+  if (!aligned_to(a, element_bytes(dtype))) return MXFP4MOE_ERR_ALIGN;
+  hipError_t err =
+      launch_swiglu(h, dtype, R, I, alpha, limit, offset, split != 0, a, nullptr, nullptr, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_swiglu_fp8(const void* h, int dtype, int64_t R, int64_t I, float alpha, float limit, float offset, int split,
+                   uint8_t* codes, float* scales, void* stream) {
+  int st = check_swiglu(h, dtype, R, I, alpha, limit, offset);
+  if (st != MXFP4MOE_OK || R == 0) return st;
+  if (codes == nullptr || scales == nullptr) return MXFP4MOE_ERR_ARG;
+  if (!aligned_to(scales, 4)) return MXFP4MOE_ERR_ALIGN;
+  hipError_t err =
+      launch_swiglu(h, dtype, R, I, alpha, limit, offset, split != 0, nullptr, codes, scales, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_swiglu_backward(const void* da, const void* h, int dtype, int64_t R, int64_t I, float alpha, float limit,
+                        float offset, int split, void* dh, void* stream) {
+  int st = check_swiglu(h, dtype, R, I, alpha, limit, offset);
+  if (st != MXFP4MOE_OK || R == 0) return st;
+  if (da == nullptr || dh == nullptr) return MXFP4MOE_ERR_ARG;
+  const size_t el = element_bytes(dtype);
+  if (!aligned_to(da, el) || !aligned_to(dh, el)) return MXFP4MOE_ERR_ALIGN;
+  hipError_t err =
+      launch_swiglu_backward(da, h, dtype, R, I, alpha, limit, offset, split != 0, dh, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_balance_loss(const float* router_logits, const int32_t* topk_ids, const uint8_t* token_mask, int64_t T,
+                     int64_t E, int64_t top_k, float* loss, int32_t* counts, float* density, void* workspace,
+                     size_t* workspace_bytes, void* stream) {
+  int st = check_route_shape(T, E, top_k);
+  if (st != MXFP4MOE_OK) return st;
+  if (workspace_bytes == nullptr) return MXFP4MOE_ERR_ARG;
+  const size_t need = balance_loss_workspace(T, E);
+  if (workspace == nullptr) {
+    *workspace_bytes = need;
+    return MXFP4MOE_OK;
+  }
+  if (loss == nullptr || counts == nullptr || density == nullptr ||
+      (T > 0 && (router_logits == nullptr || topk_ids == nullptr)))
+    return MXFP4MOE_ERR_ARG;
+  if (*workspace_bytes < need) return MXFP4MOE_ERR_WORKSPACE;
+  if (!aligned_to(router_logits, 4) || !aligned_to(topk_ids, 4) || !aligned_to(loss, 4) || !aligned_to(counts, 4) ||
+      !aligned_to(density, 4) || (need > 0 && !aligned_to(workspace, 4)))
+    return MXFP4MOE_ERR_ALIGN;
+  hipError_t err = launch_balance_loss(router_logits, topk_ids, token_mask, T, E, top_k, loss, counts, density,
+                                       workspace, (hipStream_t)stream);
+  return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
+}
+
+int moe_balance_loss_backward(const float* router_logits, const float* density, const float* d_loss,
+                              const uint8_t* token_mask, const float* add_to, int64_t T, int64_t E, float* d_logits,
+                              void* stream) {
+  int st = check_route_shape(T, E, 1);
+  if (st != MXFP4MOE_OK || T == 0) return st;
+  if (router_logits == nullptr || density == nullptr || d_loss == nullptr || d_logits == nullptr)
+    return MXFP4MOE_ERR_ARG;
+  if (!aligned_to(router_logits, 4) || !aligned_to(density, 4) || !aligned_to(d_loss, 4) || !aligned_to(add_to, 4) ||
+      !aligned_to(d_logits, 4))
+    return MXFP4MOE_ERR_ALIGN;
+  hipError_t err = launch_balance_loss_backward(router_logits, density, d_loss, token_mask, add_to, T, E, d_logits,
+                                                (hipStream_t)stream);
   return err == hipSuccess ? MXFP4MOE_OK : MXFP4MOE_ERR_HIP;
 }
 

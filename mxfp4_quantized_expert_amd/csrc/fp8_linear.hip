@@ -1,0 +1,274 @@
+// Rows in 8 bits times 8-bit weights, dense or per expert, and the gradient to
+// the rows.
+//
+//   y[r, n]  = sum_k x[r, k] W_e[n, k] + b_e[n]
+//   dx[r, k] = sum_n dy[r, n] W_e[n, k]
+// for the rows r of expert e (expert_offsets; one expert without them).  x and
+// W are E4M3 codes; x has a float32 scale for each 128 k of a row, W one for
+// each 128 n x 128 k.  The weights are frozen, so the rows are all that has a
+// gradient; dy is bf16.
+//
+// Codes multiply exactly: two of them on the FP8 MFMA, a code (exact in bf16)
+// and dy on the bf16 one.  Each block of 128 of the summed axis is added up by
+// the MFMA, multiplied by its scales and added to the sum, in fp32; the bias
+// follows and the result is rounded once.  The MFMA sums are fp32, except that
+// the FP8 one adds eight neighbouring products as integers in steps of 2^-13
+// of the largest's power of two, and cuts off what lies below (measured by
+// pairs of products on MI355X; the older 16x16x32 form does the same).  That is
+// its price for twice the rate of the bf16 MFMA, on which the same codes would
+// be added in full; it is 2^-4 of the rounding of a bf16 result where products
+// are within a few powers of two of each other, as normal data are.
+#include "expert_device.h"
+#include "fp8_device.h"
+#include "internal.h"
+#include "mx_device.h"
+#include "row_tiles.h"
+
+namespace {
+
+using namespace mxtiles;
+using mx::bf16x8;
+using mx::f32x4;
+using mx::i32x8;
+using mx::u32x4;
+
+constexpr int kBlock = mx8::kBlock;
+
+struct Fp8Args {
+  const void* x;           // forward: x [R, K] codes; gradient: dy [R, N] bf16
+  const float* x_scales;   // forward: [R, ceil(K / 128)]
+  const uint8_t* w;        // [E, N, K] codes
+  const float* w_scales;   // [E, ceil(N / 128), ceil(K / 128)]
+  const uint16_t* bias;    // [E, N] or nullptr
+  const int32_t* offsets;  // [E + 1] or nullptr (E == 1, every row)
+  uint16_t* y;             // forward: y [R, N]; gradient: dx [R, K]
+  int R, K, N, E;
+  int max_tiles;           // row tiles, at most
+};
+
+// Sixteen rows of A times sixteen rows of B over 128 k of codes: a lane's 32
+// bytes are k 16 q .. + 15 and 64 + 16 q .. + 15 of row lane & 15 (q = lane >>
+// 4) on both sides; any agreed order of k gives the same sum.
+__device__ __forceinline__ f32x4 multiply(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1) {
+  const i32x8 a = {(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3], (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
+  const i32x8 b = {(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{}, 0, 0, 0, 0, 0, 0);
+}
+
+// Four consecutive outputs of a row, `n` of them in range (`whole`: always four, 8-byte aligned).
+__device__ __forceinline__ void store4(uint16_t* out, f32x4 v, const uint16_t* bias, int n, bool whole) {
+  if (bias != nullptr) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c < n) v[c] += mx::bf16_to_f32(bias[c]);
+  }
+  const uint2 packed = mxgemm::pack_bf16x4(v);
+  if (whole) {
+    *reinterpret_cast<uint2*>(out) = packed;
+    return;
+  }
+  const uint32_t d[2] = {packed.x, packed.y};
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (c < n) out[c] = (uint16_t)(d[c >> 1] >> (16 * (c & 1)));
+}
+
+// ---------------------------------------------------------------- few rows
+
+// y for row tiles of at most 16 rows: weights as the A operand, straight to
+// registers, x rows as B.  The waves of a block split K, kC blocks of 128 each
+// at a time (all loads of a wave in flight before the first product), for kG *
+// 16 weight rows; their sums meet in LDS, added in wave order.  Loads past K,
+// N or the tile's rows return zero from the buffer's bounds.
+constexpr int kFewRows = 16;
+
+template <int kC, int kG>
+__global__ __launch_bounds__(512) void fp8_linear_few_kernel(Fp8Args a) {
+  extern __shared__ f32x4 red[];
+  const int n_chunks = (a.N + 16 * kG - 1) / (16 * kG);
+  int ti, nc;
+  if (!map_block(a.max_tiles, n_chunks, ti, nc)) return;  // uniform per block
+  Tile t;
+  if (!find_tile(a, kFewRows, ti, t)) return;
+  const int K = a.K, N = a.N, n0 = nc * 16 * kG, kb = (K + kBlock - 1) / kBlock;
+  const int lane = mx::lane_id(), lr = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const auto rx = buffer(static_cast<const uint8_t*>(a.x) + (size_t)t.row0 * K, (uint32_t)t.rows * K);
+  const auto rw = buffer(a.w + ((size_t)t.e * N + n0) * K, (uint32_t)min(16 * kG, N - n0) * K);
+  const float* xs = a.x_scales + (size_t)(t.row0 + min(lr, t.rows - 1)) * kb;
+  const float* ws = a.w_scales + ((size_t)t.e * mx8::blocks_of(N) + n0 / kBlock) * kb;
+
+  f32x4 acc[kG] = {};
+  for (int c0 = wave * kC; c0 < kb; c0 += waves * kC) {
+    u32x4 x[kC][2], w[kG][kC][2];
+    float s[kC];
+#pragma unroll
+    for (int j = 0; j < kC; ++j) {
+      const int k = (c0 + j) * kBlock + 16 * q;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool in = k + 64 * h < K;
+#pragma unroll
+        for (int i = 0; i < kG; ++i)
+          w[i][j][h] = __builtin_amdgcn_raw_buffer_load_b128(rw, in ? (uint32_t)(lr + 16 * i) * K + k + 64 * h : kDead, 0, 0);
+        x[j][h] = __builtin_amdgcn_raw_buffer_load_b128(rx, in ? (uint32_t)lr * K + k + 64 * h : kDead, 0, 0);
+      }
+      const int c = min(c0 + j, kb - 1);
+      s[j] = xs[c] * ws[c];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < kC; ++j) {
+      if (c0 + j >= kb) break;  // uniform
+#pragma unroll
+      for (int i = 0; i < kG; ++i) {
+        const f32x4 p = multiply(w[i][j][0], w[i][j][1], x[j][0], x[j][1]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][c] = __builtin_fmaf(p[c], s[j], acc[i][c]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kG; ++i) red[(wave * kG + i) * 64 + lane] = acc[i];
+  __syncthreads();
+  for (int i = wave; i < kG; i += waves) {
+    f32x4 v = red[i * 64 + lane];
+    for (int u = 1; u < waves; ++u) v += red[(u * kG + i) * 64 + lane];
+    const int n = n0 + 16 * i + 4 * q;  // lane (row lr of the tile, q): features n .. n + 3
+    if (lr >= t.rows || n >= N) continue;
+    const uint16_t* bias = a.bias != nullptr ? a.bias + (size_t)t.e * N + n : nullptr;
+    store4(a.y + (size_t)(t.row0 + lr) * N + n, v, bias, min(4, N - n), (N & 3) == 0);
+  }
+}
+
+// Two codes (bytes 2 SEL and 2 SEL + 1 of `four`) as two bf16, exactly.
+template <int SEL>
+__device__ __forceinline__ uint32_t fp8x2_to_bf16x2(uint32_t four) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(four, 1.0f, SEL != 0));
+}
+
+// dx for row tiles of at most 16 rows.  The sum runs over weight rows, so the
+// MFMA's A operand is the transposed weights: lane (m, q) loads four codes, k =
+// 4 m .. 4 m + 3 of a block's 64, of eight weight rows n = 8 q .. 8 q + 7,
+// converts them to pairs of k and exchanges halves between the rows of a pair
+// (v_perm) into four operands of eight n, one for each k.  The waves of a block
+// take every waves-th block of 128 n and add their sums in LDS in wave order.
+constexpr int kBackFewK = 64;
+constexpr int kRedStride = 20;  // floats per lane in LDS: 16 and padding
+
+template <bool kAligned>
+__global__ __launch_bounds__(512) void fp8_linear_backward_few_kernel(Fp8Args a) {
+  extern __shared__ float redf[];
+  const int k_chunks = (a.K + kBackFewK - 1) / kBackFewK;
+  int ti, kc;
+  if (!map_block(a.max_tiles, k_chunks, ti, kc)) return;  // uniform per block
+  Tile t;
+  if (!find_tile(a, kFewRows, ti, t)) return;
+  const int K = a.K, N = a.N, k0 = kc * kBackFewK, kb = (K + kBlock - 1) / kBlock, nb = (N + kBlock - 1) / kBlock;
+  const int lane = mx::lane_id(), m = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const auto rw = buffer(a.w + (size_t)t.e * N * K, (uint32_t)N * K);
+  const uint16_t* dy0 = static_cast<const uint16_t*>(a.x) + (size_t)t.row0 * N;
+  const auto rd = buffer(dy0, (uint32_t)t.rows * N * 2);
+  const float* ws = a.w_scales + (size_t)t.e * nb * kb + k0 / kBlock;
+  const int row = min(m, t.rows - 1);  // columns past the tile's rows are dropped
+  const uint32_t col = k0 + 4 * m;
+
+  f32x4 acc[4] = {};
+  for (int b = wave; b < nb; b += waves) {
+    uint32_t w[4][8];
+    u32x4 d[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int n = kBlock * b + 32 * u + 8 * q;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[u][i] = __builtin_amdgcn_raw_buffer_load_b32(
+            rw, n + i < N && col < (uint32_t)K ? (uint32_t)(n + i) * K + col : kDead, 0, 0);
+      d[u] = load_dy8<kAligned>(rd, dy0 + (size_t)row * N, (uint32_t)row * N * 2, n, N,
+                                kBlock * b + 32 * u + 32 <= N);
+    }
+    const float s = ws[(size_t)b * kb];
+    __builtin_amdgcn_sched_barrier(0);
+    f32x4 part[4] = {};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint32_t r[8][2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        r[i][0] = fp8x2_to_bf16x2<0>(w[u][i]);
+        r[i][1] = fp8x2_to_bf16x2<1>(w[u][i]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        u32x4 op;
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+          op[p] = __builtin_amdgcn_perm(r[2 * p + 1][j >> 1], r[2 * p][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
+        part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx::as_bf16x8(op), mx::as_bf16x8(d[u]), part[j], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[j][c] = __builtin_fmaf(part[j][c], s, acc[j][c]);
+  }
+  // lane (row m of the tile, q) holds k = k0 + 16 q + 4 c + j in acc[j][c]
+  float* mine = redf + (wave * 64 + lane) * kRedStride;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<f32x4*>(mine + 4 * c) = f32x4{acc[0][c], acc[1][c], acc[2][c], acc[3][c]};
+  __syncthreads();
+  for (int i = threadIdx.x; i < 64 * 4; i += blockDim.x) {
+    const int l = i >> 2, c = i & 3;
+    f32x4 v = *reinterpret_cast<const f32x4*>(redf + l * kRedStride + 4 * c);
+    for (int u = 1; u < waves; ++u) v += *reinterpret_cast<const f32x4*>(redf + (u * 64 + l) * kRedStride + 4 * c);
+    const int k = k0 + 16 * (l >> 4) + 4 * c, r = l & 15;
+    if (r < t.rows && k < K) *reinterpret_cast<uint2*>(a.y + (size_t)(t.row0 + r) * K + k) = mxgemm::pack_bf16x4(v);
+  }
+}
+
+template <int kC>
+hipError_t launch_few(Fp8Args a, int waves, hipStream_t stream) {
+  // as many row groups to a block (x is read once for all) as leave two blocks for every CU
+  a.max_tiles = max_tiles(a, kFewRows);
+  const int64_t groups = ((int64_t)a.N + 15) / 16 * a.max_tiles, want = 2 * mxfp4moe::device_cu_count();
+  const int g = groups >= 4 * want ? 4 : groups >= 2 * want ? 2 : 1;
+  const dim3 grid = grid_of(a.max_tiles, ((int64_t)a.N + 16 * g - 1) / (16 * g));
+  const size_t lds = (size_t)waves * g * 64 * sizeof(f32x4);
+  if (g == 4) fp8_linear_few_kernel<kC, 4><<<grid, waves * 64, lds, stream>>>(a);
+  else if (g == 2) fp8_linear_few_kernel<kC, 2><<<grid, waves * 64, lds, stream>>>(a);
+  else fp8_linear_few_kernel<kC, 1><<<grid, waves * 64, lds, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+namespace mxfp4moe {
+
+hipError_t launch_fp8_linear(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales,
+                             const uint16_t* bias, const int32_t* offsets, int64_t R, int64_t K, int64_t N, int64_t E,
+                             uint16_t* y, hipStream_t stream) {
+  if (R == 0) return hipSuccess;
+  const Fp8Args a{x, x_scales, w, w_scales, bias, offsets, y, (int)R, (int)K, (int)N, (int)E, 0};
+  ProfileScope prof(kStageFp8Linear, stream);
+  const int chunks = (int)mx8::blocks_of(K), waves = chunks < 8 ? chunks : 8;
+  return (chunks + waves - 1) / waves <= 2 ? launch_few<2>(a, waves, stream) : launch_few<3>(a, waves, stream);
+}
+
+hipError_t launch_fp8_linear_backward(const uint16_t* dy, const uint8_t* w, const float* w_scales,
+                                      const int32_t* offsets, int64_t R, int64_t K, int64_t N, int64_t E, uint16_t* dx,
+                                      hipStream_t stream) {
+  if (R == 0) return hipSuccess;
+  Fp8Args a{dy, nullptr, w, w_scales, nullptr, offsets, dx, (int)R, (int)K, (int)N, (int)E, 0};
+  ProfileScope prof(kStageFp8LinearBackward, stream);
+  a.max_tiles = max_tiles(a, kFewRows);
+  const int blocks = (int)mx8::blocks_of(N), waves = blocks < 8 ? blocks : 8;
+  const dim3 grid = grid_of(a.max_tiles, (K + kBackFewK - 1) / kBackFewK);
+  const size_t lds = (size_t)waves * 64 * kRedStride * sizeof(float);
+  if (N % 2 == 0) fp8_linear_backward_few_kernel<true><<<grid, waves * 64, lds, stream>>>(a);
+  else fp8_linear_backward_few_kernel<false><<<grid, waves * 64, lds, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace mxfp4moe

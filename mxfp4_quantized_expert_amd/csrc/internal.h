@@ -28,7 +28,16 @@ enum Stage : int {
   kStageRouteBackward = 17,
   kStageLinear = 18,            // rows times 4-bit weights
   kStageLinearBackward = 19,    // ... and the gradient to the rows
-  kStageLast = kStageLinearBackward,
+  kStageRmsNorm = 20,           // the norm ahead of the layer
+  kStageRmsNormBackward = 21,
+  kStageSwiglu = 22,            // the experts' activation
+  kStageSwigluBackward = 23,
+  kStageFp8Quantize = 24,       // rows in 8 bits
+  kStageFp8Linear = 25,         // rows in 8 bits times 8-bit weights
+  kStageFp8LinearBackward = 26,
+  kStageBalance = 27,           // the router's balance loss
+  kStageBalanceBackward = 28,
+  kStageLast = kStageBalanceBackward,
 };
 
 // Records a HIP event pair around one launch when the benchmark hook asked for
@@ -173,6 +182,43 @@ hipError_t launch_linear(const uint16_t* x, const uint8_t* blocks, const uint8_t
 hipError_t launch_linear_backward(const uint16_t* dy, const uint8_t* blocks, const uint8_t* scales,
                                   const float* scale2, const int32_t* offsets, int64_t R, int64_t K, int64_t N,
                                   int64_t E, uint16_t* dx, hipStream_t stream);
+
+// The norm ahead of the layer (norm.hip).  codes != nullptr: rows out in 8
+// bits, else y.  weight_dtype: dtype or kF32.
+hipError_t launch_rms_norm(const void* x, const void* residual, const void* weight, int dtype, int weight_dtype,
+                           float eps, int64_t T, int64_t H, void* summed, void* y, uint8_t* codes, float* scales,
+                           float* rstd, hipStream_t stream);
+size_t rms_norm_backward_workspace(int dtype, int64_t T, int64_t H);
+hipError_t launch_rms_norm_backward(const void* dy, const void* d_summed, const void* summed, const void* weight,
+                                    int dtype, int weight_dtype, const float* rstd, int64_t T, int64_t H, void* dx,
+                                    float* d_weight, float* workspace, hipStream_t stream);
+
+// The experts' activation and rows in 8 bits (activation.hip).  codes !=
+// nullptr: rows out in 8 bits, else out.
+hipError_t launch_swiglu(const void* h, int dtype, int64_t R, int64_t I, float alpha, float limit, float offset,
+                         bool split, void* out, uint8_t* codes, float* scales, hipStream_t stream);
+hipError_t launch_swiglu_backward(const void* da, const void* h, int dtype, int64_t R, int64_t I, float alpha,
+                                  float limit, float offset, bool split, void* dh, hipStream_t stream);
+hipError_t launch_fp8_quantize(const void* x, int dtype, int64_t R, int64_t K, uint8_t* codes, float* scales,
+                               hipStream_t stream);
+
+// Rows in 8 bits times 8-bit weights and the gradient to the rows
+// (fp8_linear.hip).  offsets == nullptr: one expert, every row.
+hipError_t launch_fp8_linear(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales,
+                             const uint16_t* bias, const int32_t* offsets, int64_t R, int64_t K, int64_t N, int64_t E,
+                             uint16_t* y, hipStream_t stream);
+hipError_t launch_fp8_linear_backward(const uint16_t* dy, const uint8_t* w, const float* w_scales,
+                                      const int32_t* offsets, int64_t R, int64_t K, int64_t N, int64_t E, uint16_t* dx,
+                                      hipStream_t stream);
+
+// The router's balance loss (balance.hip).  mask, add: may be nullptr.
+size_t balance_loss_workspace(int64_t T, int64_t E);
+hipError_t launch_balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask, int64_t T, int64_t E,
+                               int64_t top_k, float* loss, int32_t* counts, float* density, void* workspace,
+                               hipStream_t stream);
+hipError_t launch_balance_loss_backward(const float* logits, const float* density, const float* d_loss,
+                                        const uint8_t* mask, const float* add, int64_t T, int64_t E, float* d_logits,
+                                        hipStream_t stream);
 
 hipError_t launch_dequant(const uint8_t* blocks, const uint8_t* scales, uint16_t* out, int64_t N, int64_t K,
                           hipStream_t stream);

@@ -1,0 +1,313 @@
+// The root-mean-square norm of token rows with the residual's addition, its
+// rows out in the input type or in 8 bits, and its gradients: what stands
+// ahead of the router and the experts.
+//
+//   s = x + residual, rounded to the rows' type;  r = (mean_i s_i^2 + eps)^(-1/2)
+//   y_i = s_i r w_i
+//   dx_i = r (w_i dy_i - s_i r^2 mean_j(s_j w_j dy_j)) + d_s_i  (dx and the
+//          residual's gradient alike), d_w_i = sum_t dy_ti s_ti r_t
+// fp32 throughout, one rounding at the end.  A row lies in the registers of
+// one wave (or of four or sixteen of one block), 8 elements a piece, so that
+// each tensor moves once; HBM is the bound, and for a few rows the latency of
+// a launch.
+#include "fp8_device.h"
+#include "internal.h"
+#include "mx_device.h"
+#include "row_device.h"
+
+namespace {
+
+using mx8::f32x8;
+using mx8::kPiece;
+using mxrow::Piece;
+
+struct NormArgs {
+  const void* x;
+  const void* residual;  // or nullptr
+  const void* weight;
+  void* summed;          // with a residual
+  void* y;               // or in 8 bits:
+  uint8_t* codes;
+  float* scales;
+  float* rstd;
+  float eps;
+  int64_t T;
+  int H;
+};
+
+// The sum over a row's waves, in every lane of them.  kWaves > 1: they are the
+// block.
+template <int kWaves>
+__device__ __forceinline__ float row_sum(float v, float* part) {
+  v = mx::wave_sum_f32(v);
+  if constexpr (kWaves > 1) {
+    __syncthreads();  // the last row's sums have been read
+    if (mx::lane_id() == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int u = 0; u < kWaves; ++u) v += part[u];
+  }
+  return v;
+}
+
+// kWaves waves a row, kP pieces of it a lane at most.
+template <typename E, typename W, bool kFp8, int kWaves, int kP>
+__global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : 256) void rms_norm_kernel(NormArgs a) {
+  using Pc = Piece<E, kPiece>;
+  constexpr int kRows = kWaves > 4 ? 1 : 4 / kWaves;  // of a block
+  __shared__ float part[16];
+  const int lane = mx::lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = wave % kWaves;
+  const int H = a.H, nv = (H + kPiece - 1) / kPiece;
+  const E* xs = static_cast<const E*>(a.x);
+  const E* rs = static_cast<const E*>(a.residual);
+  const W* w = static_cast<const W*>(a.weight);
+  for (int64_t t = (int64_t)blockIdx.x * kRows + wave / kWaves; t < a.T; t += (int64_t)gridDim.x * kRows) {
+    typename Pc::vec h[kP], res[kP];
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int v = (i * kWaves + sub) * 64 + lane;
+      h[i] = v < nv ? mx8::load_piece(xs + t * H, v, H) : typename Pc::vec{};
+      if (rs != nullptr) res[i] = v < nv ? mx8::load_piece(rs + t * H, v, H) : typename Pc::vec{};
+    }
+    typename Piece<W, kPiece>::vec wv[kP];
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int v = (i * kWaves + sub) * 64 + lane;
+      wv[i] = v < nv ? mx8::load_piece(w, v, H) : typename Piece<W, kPiece>::vec{};
+    }
+    float sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int v = (i * kWaves + sub) * 64 + lane;
+      if (rs != nullptr) {
+        h[i] = mx8::from_f32<E>(mx8::to_f32<E>(h[i]) + mx8::to_f32<E>(res[i]));
+        if (v < nv) mx8::store_piece(static_cast<E*>(a.summed) + t * H, v, H, h[i]);
+      }
+      const f32x8 f = mx8::to_f32<E>(h[i]);
+#pragma unroll
+      for (int c = 0; c < kPiece; ++c) sq = __builtin_fmaf(f[c], f[c], sq);
+    }
+    const float r = 1.0f / sqrtf(row_sum<kWaves>(sq, part) / (float)H + a.eps);
+    if (lane == 0 && sub == 0) a.rstd[t] = r;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int v = (i * kWaves + sub) * 64 + lane;
+      if ((v & ~15) >= nv) continue;  // whole rows of sixteen lanes
+      const f32x8 y = mx8::to_f32<E>(h[i]) * r * mx8::to_f32<W>(wv[i]);
+      if constexpr (kFp8) {
+        mx8::store_quantized(y, v, H, a.codes + t * H, a.scales + t * mx8::blocks_of(H));
+      } else if (v < nv) {
+        mx8::store_piece(static_cast<E*>(a.y) + t * H, v, H, mx8::from_f32<E>(y));
+      }
+    }
+  }
+}
+
+struct NormBackArgs {
+  const void* dy;
+  const void* d_summed;  // or nullptr
+  const void* summed;
+  const void* weight;
+  const float* rstd;
+  void* dx;
+  float* part;  // [blocks][H] sums of d_weight over the block's rows
+  int64_t T;
+  int H;
+};
+
+// A block takes every gridDim.x-th group of kRows rows and keeps its columns'
+// sums of d_weight in registers; they meet in LDS in wave order and leave as
+// one row of `part`.
+template <typename E, typename W, int kWaves, int kP>
+__global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : 256) void rms_norm_backward_kernel(NormBackArgs a) {
+  using Pc = Piece<E, kPiece>;
+  constexpr int kRows = kWaves > 4 ? 1 : 4 / kWaves;
+  __shared__ float part[16];
+  const int lane = mx::lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = wave % kWaves;
+  const int H = a.H, nv = (H + kPiece - 1) / kPiece;
+  const E* dys = static_cast<const E*>(a.dy);
+  const E* ds = static_cast<const E*>(a.d_summed);
+  const E* hs = static_cast<const E*>(a.summed);
+  const W* w = static_cast<const W*>(a.weight);
+  f32x8 dw[kP];
+#pragma unroll
+  for (int i = 0; i < kP; ++i) dw[i] = f32x8{};
+  for (int64_t t = (int64_t)blockIdx.x * kRows + wave / kWaves; t < a.T; t += (int64_t)gridDim.x * kRows) {
+    typename Pc::vec h[kP], g[kP], d[kP];
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int v = (i * kWaves + sub) * 64 + lane;
+      h[i] = v < nv ? mx8::load_piece(hs + t * H, v, H) : typename Pc::vec{};
+      g[i] = v < nv ? mx8::load_piece(dys + t * H, v, H) : typename Pc::vec{};
+      d[i] = ds != nullptr && v < nv ? mx8::load_piece(ds + t * H, v, H) : typename Pc::vec{};
+    }
+    const float r = a.rstd[t];
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int v = (i * kWaves + sub) * 64 + lane;
+      if (v >= nv) continue;
+      const f32x8 s = mx8::to_f32<E>(h[i]), y = mx8::to_f32<E>(g[i]), f = y * mx8::to_f32<W>(mx8::load_piece(w, v, H));
+#pragma unroll
+      for (int c = 0; c < kPiece; ++c) {
+        dot = __builtin_fmaf(f[c], s[c], dot);
+        dw[i][c] = __builtin_fmaf(y[c], s[c] * r, dw[i][c]);
+      }
+    }
+    // s r^2 mean(s w dy) as (s r) times what every element of the row shares
+    const float mean = row_sum<kWaves>(dot, part) / (float)H * r;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int v = (i * kWaves + sub) * 64 + lane;
+      if (v >= nv) continue;
+      const f32x8 s = mx8::to_f32<E>(h[i]), f = mx8::to_f32<E>(g[i]) * mx8::to_f32<W>(mx8::load_piece(w, v, H));
+      const f32x8 dx = r * (f - s * r * mean) + mx8::to_f32<E>(d[i]);
+      mx8::store_piece(static_cast<E*>(a.dx) + t * H, v, H, mx8::from_f32<E>(dx));
+    }
+  }
+  float* out = a.part + (size_t)blockIdx.x * H;
+  if constexpr (kRows > 1) {
+    extern __shared__ __attribute__((aligned(32))) float sums[];  // [nv * kPiece]
+    for (int u = 0; u < kRows; ++u) {
+      if (wave == u) {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+          const int v = i * 64 + lane;
+          if (v >= nv) continue;
+          f32x8* at = reinterpret_cast<f32x8*>(sums + kPiece * v);
+          if (u > 0) dw[i] += *at;
+          if (u + 1 < kRows) *at = dw[i];
+          else mx8::store_piece(out, v, H, dw[i]);
+        }
+      }
+      __syncthreads();
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const int v = (i * kWaves + sub) * 64 + lane;
+      if (v < nv) mx8::store_piece(out, v, H, dw[i]);
+    }
+  }
+}
+
+// d_weight[i] = sum of the blocks' rows of `part`: 64 columns a block, its
+// sixteen waves a sixteenth of the rows each, added in wave order.
+constexpr int kJoinWaves = 16;
+__global__ __launch_bounds__(64 * kJoinWaves) void rms_norm_join_kernel(const float* __restrict__ part, int rows,
+                                                                        int H, float* __restrict__ d_weight) {
+  __shared__ float sums[kJoinWaves][64];
+  const int lane = mx::lane_id(), wave = threadIdx.x >> 6, col = blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (col < H) {
+#pragma unroll 8
+    for (int r = wave; r < rows; r += kJoinWaves) s += part[(size_t)r * H + col];
+  }
+  sums[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && col < H) {
+    for (int u = 1; u < kJoinWaves; ++u) s += sums[u][lane];
+    d_weight[col] = s;
+  }
+}
+
+// A launch holds fewer than 2^32 threads; the kernels loop past that.
+constexpr int64_t kMaxBlocks = 1 << 20;
+
+// Pieces of a lane that the registers hold: 256 bytes of a row in each kernel's largest form.
+template <typename E>
+constexpr int kMostPieces = sizeof(E) == 4 ? 4 : 8;
+
+// Rows from which a wave each fills the chip; below, four share one.
+constexpr int64_t kManyRows = 1024;
+
+template <typename F>
+auto by_row(int64_t T, int64_t H, int most, F&& f) {
+  // -> f(waves of a row, pieces of a lane)
+  const int64_t nv = (H + kPiece - 1) / kPiece;
+  const int few = most / 4;
+  if (nv <= 64 * few) return f(1, few);
+  if (nv <= 64 * most) return T >= kManyRows ? f(1, most) : f(4, few);
+  if (nv <= 256 * most) return f(4, most);
+  return f(16, 4);
+}
+
+template <typename E, typename W, bool kFp8>
+hipError_t norm(const NormArgs& a, hipStream_t stream) {
+  constexpr int kMost = kMostPieces<E>, kFew = kMost / 4;
+  return by_row(a.T, a.H, kMost, [&](int waves, int pieces) {
+    const int64_t rows = waves > 4 ? 1 : 4 / waves, blocks = (a.T + rows - 1) / rows;
+    const unsigned grid = (unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks);
+    if (waves == 1 && pieces == kFew) rms_norm_kernel<E, W, kFp8, 1, kFew><<<grid, 256, 0, stream>>>(a);
+    else if (waves == 1) rms_norm_kernel<E, W, kFp8, 1, kMost><<<grid, 256, 0, stream>>>(a);
+    else if (waves == 4 && pieces == kFew) rms_norm_kernel<E, W, kFp8, 4, kFew><<<grid, 256, 0, stream>>>(a);
+    else if (waves == 4) rms_norm_kernel<E, W, kFp8, 4, kMost><<<grid, 256, 0, stream>>>(a);
+    else rms_norm_kernel<E, W, kFp8, 16, 4><<<grid, 1024, 0, stream>>>(a);
+    return hipGetLastError();
+  });
+}
+
+// Blocks of the gradient's kernel, and rows of `part`: two for every CU at most.
+int64_t back_blocks(int64_t T, int64_t H, int most) {
+  return by_row(T, H, most, [&](int waves, int) {
+    const int64_t rows = waves > 4 ? 1 : 4 / waves, blocks = (T + rows - 1) / rows;
+    const int64_t full = 2 * mxfp4moe::device_cu_count();
+    return blocks < full ? blocks : full;
+  });
+}
+
+template <typename E, typename W>
+hipError_t norm_backward(const NormBackArgs& a, float* d_weight, hipStream_t stream) {
+  constexpr int kMost = kMostPieces<E>, kFew = kMost / 4;
+  const unsigned grid = (unsigned)back_blocks(a.T, a.H, kMost);
+  const size_t lds = (size_t)((a.H + kPiece - 1) / kPiece) * kPiece * sizeof(float);
+  if (grid > 0) {
+    by_row(a.T, a.H, kMost, [&](int waves, int pieces) {
+      if (waves == 1 && pieces == kFew) rms_norm_backward_kernel<E, W, 1, kFew><<<grid, 256, lds, stream>>>(a);
+      else if (waves == 1) rms_norm_backward_kernel<E, W, 1, kMost><<<grid, 256, lds, stream>>>(a);
+      else if (waves == 4 && pieces == kFew) rms_norm_backward_kernel<E, W, 4, kFew><<<grid, 256, 0, stream>>>(a);
+      else if (waves == 4) rms_norm_backward_kernel<E, W, 4, kMost><<<grid, 256, 0, stream>>>(a);
+      else rms_norm_backward_kernel<E, W, 16, 4><<<grid, 1024, 0, stream>>>(a);
+      return 0;
+    });
+  }
+  rms_norm_join_kernel<<<(unsigned)((a.H + 63) / 64), 64 * kJoinWaves, 0, stream>>>(a.part, (int)grid, a.H, d_weight);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+namespace mxfp4moe {
+
+hipError_t launch_rms_norm(const void* x, const void* residual, const void* weight, int dtype, int weight_dtype,
+                           float eps, int64_t T, int64_t H, void* summed, void* y, uint8_t* codes, float* scales,
+                           float* rstd, hipStream_t stream) {
+  if (T == 0) return hipSuccess;
+  const NormArgs a{x, residual, weight, summed, y, codes, scales, rstd, eps, T, (int)H};
+  ProfileScope prof(kStageRmsNorm, stream);
+#define MX_NORM(E, W) (codes != nullptr ? norm<E, W, true>(a, stream) : norm<E, W, false>(a, stream))
+  if (dtype == kF32) return MX_NORM(float, float);
+  if (dtype == kF16) return weight_dtype == kF32 ? MX_NORM(_Float16, float) : MX_NORM(_Float16, _Float16);
+  return weight_dtype == kF32 ? MX_NORM(__bf16, float) : MX_NORM(__bf16, __bf16);
+#undef MX_NORM
+}
+
+size_t rms_norm_backward_workspace(int dtype, int64_t T, int64_t H) {
+  return (size_t)back_blocks(T, H, dtype == kF32 ? kMostPieces<float> : kMostPieces<__bf16>) * H * sizeof(float);
+}
+
+hipError_t launch_rms_norm_backward(const void* dy, const void* d_summed, const void* summed, const void* weight,
+                                    int dtype, int weight_dtype, const float* rstd, int64_t T, int64_t H, void* dx,
+                                    float* d_weight, float* workspace, hipStream_t stream) {
+  const NormBackArgs a{dy, d_summed, summed, weight, rstd, dx, workspace, T, (int)H};
+  ProfileScope prof(kStageRmsNormBackward, stream);
+  if (dtype == kF32) return norm_backward<float, float>(a, d_weight, stream);
+  if (dtype == kF16)
+    return weight_dtype == kF32 ? norm_backward<_Float16, float>(a, d_weight, stream)
+                                : norm_backward<_Float16, _Float16>(a, d_weight, stream);
+  return weight_dtype == kF32 ? norm_backward<__bf16, float>(a, d_weight, stream)
+                              : norm_backward<__bf16, __bf16>(a, d_weight, stream);
+}
+
+}  // namespace mxfp4moe
