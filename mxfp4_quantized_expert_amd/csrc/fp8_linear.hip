@@ -33,6 +33,8 @@ using mx::i32x8;
 using mx::u32x4;
 
 constexpr int kBlock = mx8::kBlock;
+// Floats that every lane reads alike, through the scalar cache.
+typedef const __attribute__((address_space(4))) float* ScalarFloats;
 
 struct Fp8Args {
   const void* x;           // forward: x [R, K] codes; gradient: dy [R, N] bf16
@@ -44,6 +46,7 @@ struct Fp8Args {
   uint16_t* y;             // forward: y [R, N]; gradient: dx [R, K]
   int R, K, N, E;
   int max_tiles;           // row tiles, at most
+  int tile_rows;           // rows of a tile (the 128-row kernels: 128, 64 or 32)
 };
 
 // Sixteen rows of A times sixteen rows of B over 128 k of codes: a lane's 32
@@ -53,6 +56,11 @@ __device__ __forceinline__ f32x4 multiply(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1
   const i32x8 a = {(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3], (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
   const i32x8 b = {(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{}, 0, 0, 0, 0, 0, 0);
+}
+
+__device__ __forceinline__ void take_up(f32x4& sum, const f32x4& part, float scale) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) sum[c] = __builtin_fmaf(part[c], scale, sum[c]);
 }
 
 // Four consecutive outputs of a row, `n` of them in range (`whole`: always four, 8-byte aligned).
@@ -122,9 +130,7 @@ __global__ __launch_bounds__(512) void fp8_linear_few_kernel(Fp8Args a) {
       if (c0 + j >= kb) break;  // uniform
 #pragma unroll
       for (int i = 0; i < kG; ++i) {
-        const f32x4 p = multiply(w[i][j][0], w[i][j][1], x[j][0], x[j][1]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[i][c] = __builtin_fmaf(p[c], s[j], acc[i][c]);
+        take_up(acc[i], multiply(w[i][j][0], w[i][j][1], x[j][0], x[j][1]), s[j]);
       }
     }
   }
@@ -209,9 +215,7 @@ __global__ __launch_bounds__(512) void fp8_linear_backward_few_kernel(Fp8Args a)
       }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[j][c] = __builtin_fmaf(part[j][c], s, acc[j][c]);
+    for (int j = 0; j < 4; ++j) take_up(acc[j], part[j], s);
   }
   // lane (row m of the tile, q) holds k = k0 + 16 q + 4 c + j in acc[j][c]
   float* mine = redf + (wave * 64 + lane) * kRedStride;
@@ -225,6 +229,170 @@ __global__ __launch_bounds__(512) void fp8_linear_backward_few_kernel(Fp8Args a)
     for (int u = 1; u < waves; ++u) v += *reinterpret_cast<const f32x4*>(redf + (u * 64 + l) * kRedStride + 4 * c);
     const int k = k0 + 16 * (l >> 4) + 4 * c, r = l & 15;
     if (r < t.rows && k < K) *reinterpret_cast<uint2*>(a.y + (size_t)(t.row0 + r) * K + k) = mxgemm::pack_bf16x4(v);
+  }
+}
+
+// --------------------------------------------------------------- many rows
+
+// y for row tiles of up to 128: 16x16x128 MFMA, a block of four waves makes 256
+// weight rows x 128 rows, each wave 64 x 128, in chunks of 128 k, the span of a
+// scale.  No wave shares its weights, so they go straight to registers, two
+// chunks ahead of their use; x travels into a ring of three LDS stages by the
+// load unit, with the chunk's 128 row scales.  Two blocks a CU.
+constexpr int kTileRows = 128, kTileN = 256, kStages = 4;
+constexpr int kScaleSlots = kTileRows / 4;  // a stage: the scales of the rows, then their 16-byte pieces, swizzled
+constexpr int kStageSlots = kScaleSlots + kTileRows * 8;
+
+template <int kLive>
+__device__ __forceinline__ void tile_chunks(f32x4 (&acc)[4][kTileRows / 16], u32x4* const (&xst)[kStages],
+                                            const __amdgpu_buffer_rsrc_t& rx,
+                                            const __amdgpu_buffer_rsrc_t (&rw)[4], const __amdgpu_buffer_rsrc_t& rs,
+                                            const ScalarFloats ws, int K, int kb, int wave, bool work) {
+  const int t = threadIdx.x, lane = t & 63, lr = lane & 15, q = lane >> 4;
+  // this thread's piece of a round of 32 rows of x
+  const int xr = t >> 3, xpart = (t & 7) ^ swizzle(xr & 15);
+  const uint32_t xoff = __umul24(xr, K) + 16 * xpart;
+  const uint32_t woff = __umul24(16 * (lr >> 2) + (lr & 3), K) + 16 * q;
+  const uint32_t soff = __umul24(64 * (wave & 1) + lane, 4 * kb);  // (waves 2 and 3 repeat what 0 and 1 load)
+  // a negative number for k past K is an offset past the buffer
+  const int xleft = K - 1 - 16 * xpart, wleft = K - 1 - 16 * q;
+  auto issue_x = [&](int c, u32x4* st) __attribute__((always_inline)) {
+    const uint32_t o = (xoff + c * kBlock) | ((uint32_t)(xleft - c * kBlock) & kDead);
+#pragma unroll
+    for (int k = 0; k < kLive; ++k) load_lds16(rx, st + kScaleSlots + wave * 64 + k * 256, o + (uint32_t)(32 * k) * K);
+    // (past the last chunk: the next row's, of no use)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(st + 16 * (wave & 1)), 4,
+                                             soff + 4 * c, 0, 0, 0);
+  };
+  u32x4 w[2][4][2];
+  auto issue_w = [&](int c, u32x4 (&r)[4][2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = c * kBlock + 64 * h;
+      const uint32_t o = (woff + k) | ((uint32_t)(wleft - k) & kDead);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i][h] = __builtin_amdgcn_raw_buffer_load_b128(rw[i], o, 0, 0);
+    }
+  };
+  constexpr int kXLoads = kLive + 1, kWLoads = 8;
+  issue_x(0, xst[0]);
+  issue_w(0, w[0]);
+  __builtin_amdgcn_sched_barrier(0);  // the waits count on this order
+  issue_x(1, xst[1]);
+  issue_w(1, w[1]);
+  float wscale = ws[0];
+  // piece q of row lr of a subtile; the other half's is 4 pieces on
+  const int b0 = lr * 8 + (q ^ swizzle(lr)), b1 = b0 ^ 4;
+
+  int c0 = 0;
+  auto chunk = [&](auto at) __attribute__((always_inline)) {
+    constexpr int p = decltype(at)::value;
+    const int c = c0 + p;
+    mxgemm::wait_loads_then_barrier<kXLoads + kWLoads>();
+    issue_x(c + 2, xst[(p + 2) % kStages]);
+    const float wnext = ws[min(c + 1, kb - 1)];
+    const u32x4* xs = xst[p] + kScaleSlots;
+    const float* sc = reinterpret_cast<const float*>(xst[p]);
+    if (work && c < kb) {
+      // a product's sums are taken up four products later, when they are there
+      u32x4 b[2][2];
+      f32x4 part[4];
+      float s = 0.f, raw = sc[lr];
+      b[0][0] = xs[b0];
+      b[0][1] = xs[b1];
+#pragma unroll
+      for (int cb = 0; cb < 2 * kLive; ++cb) {
+        const float before = s;
+        s = raw * wscale;
+        if (cb + 1 < 2 * kLive) {
+          b[(cb + 1) & 1][0] = xs[b0 + (cb + 1) * 128];
+          b[(cb + 1) & 1][1] = xs[b1 + (cb + 1) * 128];
+          raw = sc[16 * (cb + 1) + lr];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (cb > 0) take_up(acc[i][cb - 1], part[i], before);
+          part[i] = multiply(w[p & 1][i][0], w[p & 1][i][1], b[cb & 1][0], b[cb & 1][1]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) take_up(acc[i][2 * kLive - 1], part[i], s);
+    }
+    wscale = wnext;
+    __builtin_amdgcn_sched_barrier(0);
+    issue_w(c + 2, w[p & 1]);
+  };
+  // Whole periods of the stages and the register sets, without an exit: from a loop with exits inside, the compiler's
+  // waits would count the loads that are in flight at any of them.  Chunks past K load nothing and multiply nothing.
+  for (; c0 < kb; c0 += kStages)
+    each_of([&](auto at) __attribute__((always_inline)) { return chunk(at), true; },
+            std::make_integer_sequence<int, kStages>{});
+}
+
+__global__ __launch_bounds__(256, 2) void fp8_linear_tile_kernel(Fp8Args a) {
+  __shared__ __attribute__((aligned(16))) u32x4 x0[kStageSlots], x1[kStageSlots], x2[kStageSlots], x3[kStageSlots];
+  const int n_tiles = (a.N + kTileN - 1) / kTileN;
+  int ti, nt;
+  if (!map_tile(a, a.tile_rows, n_tiles, ti, nt)) return;  // uniform per block
+  Tile t;
+  if (!find_tile(a, a.tile_rows, ti, t)) return;
+  const int K = a.K, N = a.N, n0 = nt * kTileN, kb = (K + kBlock - 1) / kBlock;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, lr = lane & 15,
+            q = lane >> 4;
+  const int nw = n0 + wave * 64;
+  const bool work = nw < N;  // uniform: a wave past N only loads its share of x
+  const auto rx = buffer(static_cast<const uint8_t*>(a.x) + (size_t)t.row0 * K, (uint32_t)t.rows * K);
+  // weight row of operand row lr and subtile i: 16 (lr / 4) + 4 i + lr % 4 of the wave's 64, so that a lane's outputs
+  // are sixteen neighbours; a buffer for each i (a scalar offset could pass the bounds)
+  __amdgpu_buffer_rsrc_t rw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int rows = max(min(64, N - nw) - 4 * i, 0);
+    rw[i] = buffer(a.w + ((size_t)t.e * N + (rows > 0 ? nw + 4 * i : 0)) * K, (uint32_t)rows * K);
+  }
+  const auto rs = buffer(a.x_scales + (size_t)t.row0 * kb, (uint32_t)t.rows * kb * 4);
+  const ScalarFloats ws =
+      (ScalarFloats)(a.w_scales + ((size_t)t.e * mx8::blocks_of(N) + min(nw, N - 1) / kBlock) * kb);
+  u32x4* const xst[] = {x0, x1, x2, x3};
+  f32x4 acc[4][kTileRows / 16] = {};
+  const int live = (t.rows + 31) >> 5;
+  if (live == 4) tile_chunks<4>(acc, xst, rx, rw, rs, ws, K, kb, wave, work);
+  else if (live == 3) tile_chunks<3>(acc, xst, rx, rw, rs, ws, K, kb, wave, work);
+  else if (live == 2) tile_chunks<2>(acc, xst, rx, rw, rs, ws, K, kb, wave, work);
+  else tile_chunks<1>(acc, xst, rx, rw, rs, ws, K, kb, wave, work);
+  mxgemm::wait_loads_then_barrier<0>();  // no load still writes LDS
+  if (!work) return;
+
+  // lane (row lr of a subtile of rows, q): features 16 q + 4 i + j of the wave's 64 in acc[i][.][j]
+  const int n = nw + 16 * q;
+  if (n >= N) return;
+  const int have = min(16, N - n);
+  float bias[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    bias[i] = a.bias != nullptr ? mx::bf16_to_f32(a.bias[(size_t)t.e * N + min(n + i, N - 1)]) : 0.f;
+  const bool whole = (N & 7) == 0;
+#pragma unroll
+  for (int cb = 0; cb < kTileRows / 16; ++cb) {
+    if (cb >= 2 * live) break;
+    const int row = 16 * cb + lr;
+    if (row >= t.rows) continue;
+    uint16_t* y = a.y + (size_t)(t.row0 + row) * N + n;
+    uint32_t d[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      d[i] = mx::pack_bf16x2_rne(acc[i >> 1][cb][2 * (i & 1)] + bias[2 * i],
+                                 acc[i >> 1][cb][2 * (i & 1) + 1] + bias[2 * i + 1]);
+    if (whole) {
+      *reinterpret_cast<u32x4*>(y) = u32x4{d[0], d[1], d[2], d[3]};
+      if (have > 8) *reinterpret_cast<u32x4*>(y + 8) = u32x4{d[4], d[5], d[6], d[7]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < have) y[i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
+    }
   }
 }
 
@@ -250,8 +418,14 @@ hipError_t launch_fp8_linear(const uint8_t* x, const float* x_scales, const uint
                              const uint16_t* bias, const int32_t* offsets, int64_t R, int64_t K, int64_t N, int64_t E,
                              uint16_t* y, hipStream_t stream) {
   if (R == 0) return hipSuccess;
-  const Fp8Args a{x, x_scales, w, w_scales, bias, offsets, y, (int)R, (int)K, (int)N, (int)E, 0};
+  Fp8Args a{x, x_scales, w, w_scales, bias, offsets, y, (int)R, (int)K, (int)N, (int)E, 0, 0};
   ProfileScope prof(kStageFp8Linear, stream);
+  if (R > 16 * E) {
+    a.tile_rows = 128;
+    a.max_tiles = max_tiles(a, a.tile_rows);
+    fp8_linear_tile_kernel<<<grid_of(a.max_tiles, (N + kTileN - 1) / kTileN), 256, 0, stream>>>(a);
+    return hipGetLastError();
+  }
   const int chunks = (int)mx8::blocks_of(K), waves = chunks < 8 ? chunks : 8;
   return (chunks + waves - 1) / waves <= 2 ? launch_few<2>(a, waves, stream) : launch_few<3>(a, waves, stream);
 }
@@ -260,7 +434,7 @@ hipError_t launch_fp8_linear_backward(const uint16_t* dy, const uint8_t* w, cons
                                       const int32_t* offsets, int64_t R, int64_t K, int64_t N, int64_t E, uint16_t* dx,
                                       hipStream_t stream) {
   if (R == 0) return hipSuccess;
-  Fp8Args a{dy, nullptr, w, w_scales, nullptr, offsets, dx, (int)R, (int)K, (int)N, (int)E, 0};
+  Fp8Args a{dy, nullptr, w, w_scales, nullptr, offsets, dx, (int)R, (int)K, (int)N, (int)E, 0, 0};
   ProfileScope prof(kStageFp8LinearBackward, stream);
   a.max_tiles = max_tiles(a, kFewRows);
   const int blocks = (int)mx8::blocks_of(N), waves = blocks < 8 ? blocks : 8;
