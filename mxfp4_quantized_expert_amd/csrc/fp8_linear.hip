@@ -396,6 +396,193 @@ __global__ __launch_bounds__(256, 2) void fp8_linear_tile_kernel(Fp8Args a) {
   }
 }
 
+// dx for row tiles of up to 64: 32x32x16 bf16 MFMA, a block of four waves makes
+// 256 k x 64 rows, each wave 64 x 64, in chunks of 64 weight rows n; two of
+// them are the span of a scale, added up in sums of their own.  The weights'
+// bytes and dy travel into rings of LDS stages by the load unit.  The A operand
+// needs eight n of one k, so the codes are read transposed: of a group of
+// sixteen lanes each reads eight bytes of one of eight rows
+// (ds_read_b64_tr_b8), and lane c gets byte c of the eight rows.  Two blocks a
+// CU.
+constexpr int kBackK = 256, kBackRows = 64, kBackStages = 3;
+constexpr int kWSlots = 1024, kDSlots = kBackRows * 8;  // 16-byte slots of a stage: 64 n x 256 codes, 64 rows x 64 n
+
+typedef __attribute__((__vector_size__(2 * sizeof(int)))) int i32x2;
+using mx::f32x16;
+
+__device__ __forceinline__ u32x4 fp8x8_to_bf16x8(i32x2 v) {
+  return u32x4{fp8x2_to_bf16x2<0>(v[0]), fp8x2_to_bf16x2<1>(v[0]), fp8x2_to_bf16x2<0>(v[1]), fp8x2_to_bf16x2<1>(v[1])};
+}
+
+template <int kLive, bool kAligned>
+__device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][2], u32x4* const (&dst)[kBackStages],
+                                                u32x4* const (&wst)[kBackStages], const __amdgpu_buffer_rsrc_t& rd,
+                                                const uint16_t* dy, const __amdgpu_buffer_rsrc_t& rw,
+                                                const ScalarFloats ws, int rows, int K, int N, int kb, int k0,
+                                                int wave, bool work) {
+  const int t = threadIdx.x, lane = t & 63, half = lane >> 5, lrow = lane & 31, mg = (lane >> 4) & 1, c16 = lane & 15;
+  const int chunks = (N + 63) >> 6, nb = (chunks + 1) >> 1;
+  // this thread's pieces of a stage: of dy row pr (of 32), of weight row t / 16 (of 16)
+  const int pr = t >> 3, part_d = (t & 7) ^ swizzle(pr);
+  const uint32_t doff = (uint32_t)pr * N * 2 + 16 * part_d;
+  const uint32_t woff = (uint32_t)(t >> 4) * K + k0 + 16 * ((t & 15) ^ (((t >> 4) & 7) << 1));
+  constexpr int kLoads = kAligned ? 4 + kLive : 4;
+  u32x4 dreg[kLive];
+  auto load_dy = [&](int c) __attribute__((always_inline)) {
+    const int n = 64 * c + 8 * part_d;
+#pragma unroll
+    for (int k = 0; k < kLive; ++k)
+      dreg[k] = load_dy8<false>(rd, dy + (size_t)min(pr + 32 * k, rows - 1) * N, 0, n, N, 64 * c + 64 <= N);
+  };
+  auto store_dy = [&](u32x4* st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < kLive; ++k) st[t + k * 256] = dreg[k];
+  };
+  auto issue = [&](int c, u32x4* d, u32x4* w) __attribute__((always_inline)) {  // past N: zeros, or for dy the next row
+#pragma unroll
+    for (int k = 0; k < 4; ++k) load_lds16(rw, w + wave * 64 + k * 256, woff + (uint32_t)(64 * c + 16 * k) * K);
+    if constexpr (kAligned) {
+#pragma unroll
+      for (int k = 0; k < kLive; ++k)
+        load_lds16(rd, d + wave * 64 + k * 256, doff + (uint32_t)(k * 32) * N * 2 + c * 128);
+    }
+  };
+  if (!kAligned) {
+    load_dy(0);
+    store_dy(dst[0]);
+    load_dy(1);
+  }
+#pragma unroll
+  for (int c = 0; c < kBackStages - 1; ++c) {
+    __builtin_amdgcn_sched_barrier(0);  // the waits count on this order
+    issue(c, dst[c], wst[c]);
+  }
+  int boff[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) boff[s] = lrow * 8 + ((2 * s + half) ^ swizzle(lrow));
+  // codes: this lane's address for row i = c16 / 2 of the eight of a step, byte 8 (c16 & 1) of the wave's piece 2 r + mg
+  const int ai = c16 >> 1;
+  int aoff[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) aoff[r] = (8 * half + ai) * 256 + (((wave * 4 + 2 * r + mg) ^ (ai << 1)) * 16) + 8 * (c16 & 1);
+
+  f32x16 part[2][2];
+  float wscale = ws[0];
+  int c0 = 0;
+  auto chunk = [&](auto at) __attribute__((always_inline)) {
+    constexpr int p = decltype(at)::value, kOdd = p & 1;
+    const int c = c0 + p;
+    mxgemm::wait_loads_then_barrier<(kBackStages - 2) * kLoads>();
+    if (!kAligned) {  // (every wave is past the stage that this one overwrites)
+      store_dy(dst[(p + 1) % kBackStages]);
+      load_dy(c + 2);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    issue(c + kBackStages - 1, dst[(p + kBackStages - 1) % kBackStages], wst[(p + kBackStages - 1) % kBackStages]);
+    if (kAligned && c == chunks - 1 && (N & 63) != 0) {  // uniform: dy past N becomes zeros as the weights there are
+      uint16_t* stage = reinterpret_cast<uint16_t*>(dst[p % kBackStages]);
+      for (int i = t; i < kLive * 32 * 64; i += 256) {
+        const int r = i >> 6, col = i & 63;
+        if (64 * c + col >= N) stage[r * 64 + 8 * ((col >> 3) ^ swizzle(r & 31)) + (col & 7)] = 0;
+      }
+      mxgemm::lds_reads_then_barrier();
+    }
+    if (work && c < chunks) {
+      const u32x4* base = dst[p % kBackStages];
+      const uint8_t* codes = reinterpret_cast<const uint8_t*>(wst[p % kBackStages]);
+      u32x4 b[4][kLive];
+      i32x2 w[4][2];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          w[s][r] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+              (__attribute__((address_space(3))) i32x2*)(codes + aoff[r] + s * 16 * 256));
+#pragma unroll
+        for (int cb = 0; cb < kLive; ++cb) b[s][cb] = base[boff[s] + cb * 256];
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const bf16x8 op = mx::as_bf16x8(fp8x8_to_bf16x8(w[s][r]));
+#pragma unroll
+          for (int cb = 0; cb < kLive; ++cb)
+            part[r][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op, mx::as_bf16x8(b[s][cb]),
+                                                                  s == 0 && !kOdd ? f32x16{} : part[r][cb], 0, 0, 0);
+        }
+    }
+    if constexpr (kOdd) {
+      if (work && c - 1 < chunks) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int cb = 0; cb < kLive; ++cb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[r][cb][i] = __builtin_fmaf(part[r][cb][i], wscale, acc[r][cb][i]);
+      }
+      wscale = ws[(size_t)min((c + 1) >> 1, nb - 1) * kb];
+    }
+  };
+  // whole periods without an exit, as above
+  for (; c0 < chunks; c0 += 2 * kBackStages)
+    each_of([&](auto at) __attribute__((always_inline)) { return chunk(at), true; },
+            std::make_integer_sequence<int, 2 * kBackStages>{});
+}
+
+constexpr int kOutStride = 72;  // bf16 per row of a wave's outputs in LDS: 64 and padding
+
+template <bool kAligned>
+__global__ __launch_bounds__(256, 2) void fp8_linear_backward_tile_kernel(Fp8Args a) {
+  __shared__ __attribute__((aligned(16))) u32x4 w0[kWSlots], w1[kWSlots], w2[kWSlots];
+  __shared__ __attribute__((aligned(16))) u32x4 d0[kDSlots], d1[kDSlots], d2[kDSlots];
+  const int k_tiles = (a.K + kBackK - 1) / kBackK;
+  int ti, kt;
+  if (!map_tile(a, a.tile_rows, k_tiles, ti, kt)) return;  // uniform per block
+  Tile t;
+  if (!find_tile(a, a.tile_rows, ti, t)) return;
+  const int K = a.K, N = a.N, k0 = kt * kBackK, kb = (K + kBlock - 1) / kBlock;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int kw = k0 + wave * 64;
+  const bool work = kw < K;  // uniform: a wave past K only loads its share
+  const uint16_t* dy = static_cast<const uint16_t*>(a.x) + (size_t)t.row0 * N;
+  const auto rd = buffer(dy, (uint32_t)t.rows * N * 2);
+  const auto rw = buffer(a.w + (size_t)t.e * N * K, (uint32_t)N * K);
+  const ScalarFloats ws = (ScalarFloats)(a.w_scales + (size_t)t.e * mx8::blocks_of(N) * kb + min(kw, K - 1) / kBlock);
+  u32x4* const dst[] = {d0, d1, d2};
+  u32x4* const wst[] = {w0, w1, w2};
+  f32x16 acc[2][2] = {};
+  const int live = (t.rows + 31) >> 5;
+  if (live == 2) backward_chunks<2, kAligned>(acc, dst, wst, rd, dy, rw, ws, t.rows, K, N, kb, k0, wave, work);
+  else backward_chunks<1, kAligned>(acc, dst, wst, rd, dy, rw, ws, t.rows, K, N, kb, k0, wave, work);
+
+  // lane (row lane & 31 of the block, half): k = 32 r + 8 i + 4 half + j of the wave's 64 in acc[r][.][4 i + j]
+  mxgemm::wait_loads_then_barrier<0>();  // no load still writes LDS, no wave still reads it
+  if (!work) return;                     // no barrier follows
+  const int half = lane >> 5, lrow = lane & 31;
+  static_assert(32 * kOutStride * sizeof(uint16_t) <= sizeof(w0), "a wave's rows fit in a stage");
+  uint16_t* out = reinterpret_cast<uint16_t*>(wave == 0 ? w0 : wave == 1 ? w1 : wave == 2 ? w2 : d0);
+#pragma unroll
+  for (int cb = 0; cb < 2; ++cb) {
+    if (cb >= live) break;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint2*>(out + lrow * kOutStride + 32 * r + 8 * i + 4 * half) = mxgemm::pack_bf16x4(
+            f32x4{acc[r][cb][4 * i], acc[r][cb][4 * i + 1], acc[r][cb][4 * i + 2], acc[r][cb][4 * i + 3]});
+    asm volatile("" ::: "memory");  // a wave's own LDS traffic is in order
+    const int rows = min(32, t.rows - cb * 32);
+    uint16_t* dx = a.y + (size_t)(t.row0 + cb * 32) * K + kw;
+    for (int p = lane; p < rows * 8; p += 64) {
+      const int r = p >> 3, col = (p & 7) * 8;
+      if (kw + col < K)
+        *reinterpret_cast<u32x4*>(dx + (size_t)r * K + col) = *reinterpret_cast<const u32x4*>(out + r * kOutStride + col);
+    }
+    asm volatile("" ::: "memory");
+  }
+}
+
 template <int kC>
 hipError_t launch_few(Fp8Args a, int waves, hipStream_t stream) {
   // as many row groups to a block (x is read once for all) as leave two blocks for every CU
@@ -436,6 +623,14 @@ hipError_t launch_fp8_linear_backward(const uint16_t* dy, const uint8_t* w, cons
   if (R == 0) return hipSuccess;
   Fp8Args a{dy, nullptr, w, w_scales, nullptr, offsets, dx, (int)R, (int)K, (int)N, (int)E, 0, 0};
   ProfileScope prof(kStageFp8LinearBackward, stream);
+  if (R > 16 * E) {
+    a.tile_rows = kBackRows;
+    a.max_tiles = max_tiles(a, a.tile_rows);
+    const dim3 grid = grid_of(a.max_tiles, (K + kBackK - 1) / kBackK);
+    if (N % 2 == 0) fp8_linear_backward_tile_kernel<true><<<grid, 256, 0, stream>>>(a);
+    else fp8_linear_backward_tile_kernel<false><<<grid, 256, 0, stream>>>(a);
+    return hipGetLastError();
+  }
   a.max_tiles = max_tiles(a, kFewRows);
   const int blocks = (int)mx8::blocks_of(N), waves = blocks < 8 ? blocks : 8;
   const dim3 grid = grid_of(a.max_tiles, (K + kBackFewK - 1) / kBackFewK);
