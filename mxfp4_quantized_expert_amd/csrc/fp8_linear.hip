@@ -20,6 +20,7 @@
 // are within a few powers of two of each other, as normal data are.
 #include "expert_device.h"
 #include "fp8_device.h"
+#include "fp8_plan.h"
 #include "internal.h"
 #include "mx_device.h"
 #include "row_tiles.h"
@@ -46,7 +47,7 @@ struct Fp8Args {
   uint16_t* y;             // forward: y [R, N]; gradient: dx [R, K]
   int R, K, N, E;
   int max_tiles;           // row tiles, at most
-  int tile_rows;           // rows of a tile (the 128-row kernels: 128, 64 or 32)
+  int tile_rows;           // rows of a tile of the kernels with tiles in LDS
 };
 
 // Sixteen rows of A times sixteen rows of B over 128 k of codes: a lane's 32
@@ -83,69 +84,92 @@ __device__ __forceinline__ void store4(uint16_t* out, f32x4 v, const uint16_t* b
 
 // ---------------------------------------------------------------- few rows
 
-// y for row tiles of at most 16 rows: weights as the A operand, straight to
-// registers, x rows as B.  The waves of a block split K, kC blocks of 128 each
-// at a time (all loads of a wave in flight before the first product), for kG *
-// 16 weight rows; their sums meet in LDS, added in wave order.  Loads past K,
-// N or the tile's rows return zero from the buffer's bounds.
-constexpr int kFewRows = 16;
+// y for row tiles of at most 16 kR rows: weights as the A operand, rows as B,
+// both straight to registers.  The waves of a block split K, kC blocks of 128
+// each at a time (all loads of a wave in flight before the first product), for
+// kG * 16 weight rows, so a block has no barrier before its sums meet in LDS,
+// added in wave order: one round of latency, 4.1 us for one row of 2880 x 2880,
+// 9.3 for 128.  Weight row 4 kG (m / 4) + 4 i + m % 4 is operand row m
+// of subtile i, so that a lane's outputs are neighbours.  Loads past K, N or
+// the tile's rows return zero from the buffer's bounds.
+constexpr int kMeet = 8;  // subtiles that meet in LDS at a time
 
-template <int kC, int kG>
+template <int kC, int kG, int kR>
 __global__ __launch_bounds__(512) void fp8_linear_few_kernel(Fp8Args a) {
-  extern __shared__ f32x4 red[];
+  extern __shared__ f32x4 red[];  // [waves][min(kG kR, kMeet)][64]
   const int n_chunks = (a.N + 16 * kG - 1) / (16 * kG);
   int ti, nc;
   if (!map_block(a.max_tiles, n_chunks, ti, nc)) return;  // uniform per block
   Tile t;
-  if (!find_tile(a, kFewRows, ti, t)) return;
+  if (!find_tile(a, 16 * kR, ti, t)) return;
   const int K = a.K, N = a.N, n0 = nc * 16 * kG, kb = (K + kBlock - 1) / kBlock;
   const int lane = mx::lane_id(), lr = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const auto rx = buffer(static_cast<const uint8_t*>(a.x) + (size_t)t.row0 * K, (uint32_t)t.rows * K);
   const auto rw = buffer(a.w + ((size_t)t.e * N + n0) * K, (uint32_t)min(16 * kG, N - n0) * K);
-  const float* xs = a.x_scales + (size_t)(t.row0 + min(lr, t.rows - 1)) * kb;
-  const float* ws = a.w_scales + ((size_t)t.e * mx8::blocks_of(N) + n0 / kBlock) * kb;
+  const auto rs = buffer(a.x_scales + (size_t)t.row0 * kb, (uint32_t)t.rows * kb * 4);
+  const ScalarFloats ws = (ScalarFloats)(a.w_scales + ((size_t)t.e * mx8::blocks_of(N) + n0 / kBlock) * kb);
+  const uint32_t woff = __umul24(4 * kG * (lr >> 2) + (lr & 3), K) + 16 * q;
 
-  f32x4 acc[kG] = {};
+  f32x4 acc[kG][kR] = {};
   for (int c0 = wave * kC; c0 < kb; c0 += waves * kC) {
-    u32x4 x[kC][2], w[kG][kC][2];
-    float s[kC];
+    u32x4 x[kC][kR][2], w[kC][kG][2];
+    float s[kC][kR], u[kC];
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
-      const int k = (c0 + j) * kBlock + 16 * q;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const bool in = k + 64 * h < K;
+        const int k = (c0 + j) * kBlock + 64 * h;
+        const bool in = k + 16 * q < K;
 #pragma unroll
         for (int i = 0; i < kG; ++i)
-          w[i][j][h] = __builtin_amdgcn_raw_buffer_load_b128(rw, in ? (uint32_t)(lr + 16 * i) * K + k + 64 * h : kDead, 0, 0);
-        x[j][h] = __builtin_amdgcn_raw_buffer_load_b128(rx, in ? (uint32_t)lr * K + k + 64 * h : kDead, 0, 0);
+          w[j][i][h] = __builtin_amdgcn_raw_buffer_load_b128(rw, in ? woff + __umul24(4 * i, K) + k : kDead, 0, 0);
+#pragma unroll
+        for (int r = 0; r < kR; ++r)
+          x[j][r][h] =
+              __builtin_amdgcn_raw_buffer_load_b128(rx, in ? __umul24(16 * r + lr, K) + 16 * q + k : kDead, 0, 0);
       }
       const int c = min(c0 + j, kb - 1);
-      s[j] = xs[c] * ws[c];
+      u[j] = ws[c];
+#pragma unroll
+      for (int r = 0; r < kR; ++r)
+        s[j][r] = __builtin_bit_cast(
+            float, __builtin_amdgcn_raw_buffer_load_b32(rs, __umul24(16 * r + lr, 4 * kb) + 4 * c, 0, 0));
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
       if (c0 + j >= kb) break;  // uniform
 #pragma unroll
-      for (int i = 0; i < kG; ++i) {
-        take_up(acc[i], multiply(w[i][j][0], w[i][j][1], x[j][0], x[j][1]), s[j]);
+      for (int r = 0; r < kR; ++r) {
+        const float scale = s[j][r] * u[j];
+#pragma unroll
+        for (int i = 0; i < kG; ++i)
+          take_up(acc[i][r], multiply(w[j][i][0], w[j][i][1], x[j][r][0], x[j][r][1]), scale);
       }
     }
   }
+  // lane (row lr of subtile r, q): features n0 + 4 kG q + 4 i .. + 3 in acc[i][r]
+  constexpr int kAll = kG * kR, kAtOnce = kAll < kMeet ? kAll : kMeet;
 #pragma unroll
-  for (int i = 0; i < kG; ++i) red[(wave * kG + i) * 64 + lane] = acc[i];
-  __syncthreads();
-  for (int i = wave; i < kG; i += waves) {
-    f32x4 v = red[i * 64 + lane];
-    for (int u = 1; u < waves; ++u) v += red[(u * kG + i) * 64 + lane];
-    const int n = n0 + 16 * i + 4 * q;  // lane (row lr of the tile, q): features n .. n + 3
-    if (lr >= t.rows || n >= N) continue;
-    const uint16_t* bias = a.bias != nullptr ? a.bias + (size_t)t.e * N + n : nullptr;
-    store4(a.y + (size_t)(t.row0 + lr) * N + n, v, bias, min(4, N - n), (N & 3) == 0);
+  for (int first = 0; first < kAll; first += kAtOnce) {
+    if (first > 0) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      red[(wave * kAtOnce + i) * 64 + lane] = acc[(first + i) % kG][(first + i) / kG];
+    __syncthreads();
+    for (int i = wave; i < kAtOnce; i += waves) {
+      f32x4 v = red[i * 64 + lane];
+      for (int u = 1; u < waves; ++u) v += red[(u * kAtOnce + i) * 64 + lane];
+      const int n = n0 + 4 * kG * q + 4 * ((first + i) % kG), row = 16 * ((first + i) / kG) + lr;
+      if (row >= t.rows || n >= N) continue;
+      const uint16_t* bias = a.bias != nullptr ? a.bias + (size_t)t.e * N + n : nullptr;
+      store4(a.y + (size_t)(t.row0 + row) * N + n, v, bias, min(4, N - n), (N & 3) == 0);
+    }
   }
 }
+
+constexpr int kFewRows = 16;
 
 // Two codes (bytes 2 SEL and 2 SEL + 1 of `four`) as two bf16, exactly.
 template <int SEL>
@@ -234,137 +258,58 @@ __global__ __launch_bounds__(512) void fp8_linear_backward_few_kernel(Fp8Args a)
 
 // --------------------------------------------------------------- many rows
 
-// y for row tiles of up to 128: 16x16x128 MFMA, a block of four waves makes 256
-// weight rows x 128 rows, each wave 64 x 128, in chunks of 128 k, the span of a
-// scale.  No wave shares its weights, so they go straight to registers, two
-// chunks ahead of their use; x travels into a ring of three LDS stages by the
-// load unit, with the chunk's 128 row scales.  Two blocks a CU.
-constexpr int kTileRows = 128, kTileN = 256, kStages = 4;
-constexpr int kScaleSlots = kTileRows / 4;  // a stage: the scales of the rows, then their 16-byte pieces, swizzled
-constexpr int kStageSlots = kScaleSlots + kTileRows * 8;
+// y for larger row tiles: 16x16x128 MFMA, a block of kWaves waves makes 64
+// kWaves weight rows x kRows rows, each wave 64 x kRows, in chunks of 128 k, the
+// span of a scale.  x travels into a ring of LDS stages by the load unit, with
+// the chunk's scales.  No wave shares its weights: they come to registers in
+// whole lines of 128 bytes, kAhead chunks before they are wanted, and from there
+// through an LDS place of the wave's own into operands.  (Loaded as operands,
+// sixteen rows of 16 bytes at a time, they arrive at 8.9 TB/s from the caches,
+// whole lines at 25.)  Eight waves a CU.
+//   us at N = K = 2880: 512 dense rows 15.3, 2048 29.0, 4096 47.7, 16384 155 (1750
+// TFLOP/s); 128 experts: 256 rows 205 and 1024 rows 242 (1.06 GB of weights at
+// 4.4 TB/s), 16384 rows 335, with N = 5760 658 (826 TFLOP/s, 2.1 GB of weights
+// and 0.6 GB of rows at 4.2 TB/s: HBM and the matrix cores take turns).
+template <int kRows, int kWaves>
+struct Tiles {
+  static constexpr int kN = 64 * kWaves;
+  static constexpr int kAhead = kRows > 64 ? 1 : 2, kStages = kRows > 64 || kWaves < 4 ? 2 : 4;
+  // a stage: the scales of the rows and of the waves' weights, the rows' 16-byte pieces
+  static constexpr int kScales = kRows / 4 + 16, kSlots = kScales + kRows * 8, kOwn = 64 * 8;
+  static_assert(kStages % kAhead == 0, "register sets repeat with the stages");
+  static_assert((kStages * kSlots + kWaves * kOwn) * 16 <= 20 * 1024 * kWaves, "eight waves a CU");
+};
 
-template <int kLive>
-__device__ __forceinline__ void tile_chunks(f32x4 (&acc)[4][kTileRows / 16], u32x4* const (&xst)[kStages],
-                                            const __amdgpu_buffer_rsrc_t& rx,
-                                            const __amdgpu_buffer_rsrc_t (&rw)[4], const __amdgpu_buffer_rsrc_t& rs,
-                                            const ScalarFloats ws, int K, int kb, int wave, bool work) {
-  const int t = threadIdx.x, lane = t & 63, lr = lane & 15, q = lane >> 4;
-  // this thread's piece of a round of 32 rows of x
-  const int xr = t >> 3, xpart = (t & 7) ^ swizzle(xr & 15);
-  const uint32_t xoff = __umul24(xr, K) + 16 * xpart;
-  const uint32_t woff = __umul24(16 * (lr >> 2) + (lr & 3), K) + 16 * q;
-  const uint32_t soff = __umul24(64 * (wave & 1) + lane, 4 * kb);  // (waves 2 and 3 repeat what 0 and 1 load)
-  // a negative number for k past K is an offset past the buffer
-  const int xleft = K - 1 - 16 * xpart, wleft = K - 1 - 16 * q;
-  auto issue_x = [&](int c, u32x4* st) __attribute__((always_inline)) {
-    const uint32_t o = (xoff + c * kBlock) | ((uint32_t)(xleft - c * kBlock) & kDead);
-#pragma unroll
-    for (int k = 0; k < kLive; ++k) load_lds16(rx, st + kScaleSlots + wave * 64 + k * 256, o + (uint32_t)(32 * k) * K);
-    // (past the last chunk: the next row's, of no use)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(st + 16 * (wave & 1)), 4,
-                                             soff + 4 * c, 0, 0, 0);
-  };
-  u32x4 w[2][4][2];
-  auto issue_w = [&](int c, u32x4 (&r)[4][2]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = c * kBlock + 64 * h;
-      const uint32_t o = (woff + k) | ((uint32_t)(wleft - k) & kDead);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r[i][h] = __builtin_amdgcn_raw_buffer_load_b128(rw[i], o, 0, 0);
-    }
-  };
-  constexpr int kXLoads = kLive + 1, kWLoads = 8;
-  issue_x(0, xst[0]);
-  issue_w(0, w[0]);
-  __builtin_amdgcn_sched_barrier(0);  // the waits count on this order
-  issue_x(1, xst[1]);
-  issue_w(1, w[1]);
-  float wscale = ws[0];
-  // piece q of row lr of a subtile; the other half's is 4 pieces on
-  const int b0 = lr * 8 + (q ^ swizzle(lr)), b1 = b0 ^ 4;
-
-  int c0 = 0;
-  auto chunk = [&](auto at) __attribute__((always_inline)) {
-    constexpr int p = decltype(at)::value;
-    const int c = c0 + p;
-    mxgemm::wait_loads_then_barrier<kXLoads + kWLoads>();
-    issue_x(c + 2, xst[(p + 2) % kStages]);
-    const float wnext = ws[min(c + 1, kb - 1)];
-    const u32x4* xs = xst[p] + kScaleSlots;
-    const float* sc = reinterpret_cast<const float*>(xst[p]);
-    if (work && c < kb) {
-      // a product's sums are taken up four products later, when they are there
-      u32x4 b[2][2];
-      f32x4 part[4];
-      float s = 0.f, raw = sc[lr];
-      b[0][0] = xs[b0];
-      b[0][1] = xs[b1];
-#pragma unroll
-      for (int cb = 0; cb < 2 * kLive; ++cb) {
-        const float before = s;
-        s = raw * wscale;
-        if (cb + 1 < 2 * kLive) {
-          b[(cb + 1) & 1][0] = xs[b0 + (cb + 1) * 128];
-          b[(cb + 1) & 1][1] = xs[b1 + (cb + 1) * 128];
-          raw = sc[16 * (cb + 1) + lr];
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (cb > 0) take_up(acc[i][cb - 1], part[i], before);
-          part[i] = multiply(w[p & 1][i][0], w[p & 1][i][1], b[cb & 1][0], b[cb & 1][1]);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) take_up(acc[i][2 * kLive - 1], part[i], s);
-    }
-    wscale = wnext;
-    __builtin_amdgcn_sched_barrier(0);
-    issue_w(c + 2, w[p & 1]);
-  };
-  // Whole periods of the stages and the register sets, without an exit: from a loop with exits inside, the compiler's
-  // waits would count the loads that are in flight at any of them.  Chunks past K load nothing and multiply nothing.
-  for (; c0 < kb; c0 += kStages)
-    each_of([&](auto at) __attribute__((always_inline)) { return chunk(at), true; },
-            std::make_integer_sequence<int, kStages>{});
+// Piece p of row r of a subtile of sixteen lies at slot p ^ swizzle16(r): no two lanes that the LDS serves together
+// (0-3, 12-15, 20-27; 4-11, 16-19, 28-31; and so on) read the same banks.
+__device__ __forceinline__ int swizzle16(int row) {
+  const int h = row >> 1;
+  return (h & 1) | ((h >> 1) & 2) | ((h ^ (h << 1)) & 4);
 }
 
-__global__ __launch_bounds__(256, 2) void fp8_linear_tile_kernel(Fp8Args a) {
-  __shared__ __attribute__((aligned(16))) u32x4 x0[kStageSlots], x1[kStageSlots], x2[kStageSlots], x3[kStageSlots];
-  const int n_tiles = (a.N + kTileN - 1) / kTileN;
-  int ti, nt;
-  if (!map_tile(a, a.tile_rows, n_tiles, ti, nt)) return;  // uniform per block
-  Tile t;
-  if (!find_tile(a, a.tile_rows, ti, t)) return;
-  const int K = a.K, N = a.N, n0 = nt * kTileN, kb = (K + kBlock - 1) / kBlock;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, lr = lane & 15,
-            q = lane >> 4;
-  const int nw = n0 + wave * 64;
-  const bool work = nw < N;  // uniform: a wave past N only loads its share of x
-  const auto rx = buffer(static_cast<const uint8_t*>(a.x) + (size_t)t.row0 * K, (uint32_t)t.rows * K);
-  // weight row of operand row lr and subtile i: 16 (lr / 4) + 4 i + lr % 4 of the wave's 64, so that a lane's outputs
-  // are sixteen neighbours; a buffer for each i (a scalar offset could pass the bounds)
-  __amdgpu_buffer_rsrc_t rw[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int rows = max(min(64, N - nw) - 4 * i, 0);
-    rw[i] = buffer(a.w + ((size_t)t.e * N + (rows > 0 ? nw + 4 * i : 0)) * K, (uint32_t)rows * K);
-  }
-  const auto rs = buffer(a.x_scales + (size_t)t.row0 * kb, (uint32_t)t.rows * kb * 4);
-  const ScalarFloats ws =
-      (ScalarFloats)(a.w_scales + ((size_t)t.e * mx8::blocks_of(N) + min(nw, N - 1) / kBlock) * kb);
-  u32x4* const xst[] = {x0, x1, x2, x3};
-  f32x4 acc[4][kTileRows / 16] = {};
-  const int live = (t.rows + 31) >> 5;
-  if (live == 4) tile_chunks<4>(acc, xst, rx, rw, rs, ws, K, kb, wave, work);
-  else if (live == 3) tile_chunks<3>(acc, xst, rx, rw, rs, ws, K, kb, wave, work);
-  else if (live == 2) tile_chunks<2>(acc, xst, rx, rw, rs, ws, K, kb, wave, work);
-  else tile_chunks<1>(acc, xst, rx, rw, rs, ws, K, kb, wave, work);
-  mxgemm::wait_loads_then_barrier<0>();  // no load still writes LDS
-  if (!work) return;
+// chunk(0), chunk(1), ... (as compile-time numbers) of every period from c0 on, and of what is left.  Whole periods
+// have no exit: from a loop with exits inside, the compiler's waits would count the loads that are in flight at any of
+// them.
+template <int kPeriod, typename F>
+__device__ __forceinline__ void all_chunks(int chunks, int& c0, F&& chunk) {
+  for (; c0 + kPeriod <= chunks; c0 += kPeriod)
+    each_of([&](auto at) __attribute__((always_inline)) { return chunk(at), true; },
+            std::make_integer_sequence<int, kPeriod>{});
+  each_of([&](auto at) __attribute__((always_inline)) {
+    if (c0 + decltype(at)::value >= chunks) return false;  // uniform
+    chunk(at);
+    return true;
+  }, std::make_integer_sequence<int, kPeriod - 1>{});
+}
 
+struct TileBuffers {
+  __amdgpu_buffer_rsrc_t x, w, s;  // w: the wave's weight rows; s: the scales that it loads, of the rows or the weights
+};
+
+// The rows of a wave's 64 weight rows nw .. leave.
+template <int kLive>
+__device__ __forceinline__ void leave(const Fp8Args& a, const Tile& t, int nw, const f32x4 (&acc)[4][2 * kLive]) {
+  const int lane = threadIdx.x & 63, lr = lane & 15, q = lane >> 4, N = a.N;
   // lane (row lr of a subtile of rows, q): features 16 q + 4 i + j of the wave's 64 in acc[i][.][j]
   const int n = nw + 16 * q;
   if (n >= N) return;
@@ -375,8 +320,7 @@ __global__ __launch_bounds__(256, 2) void fp8_linear_tile_kernel(Fp8Args a) {
     bias[i] = a.bias != nullptr ? mx::bf16_to_f32(a.bias[(size_t)t.e * N + min(n + i, N - 1)]) : 0.f;
   const bool whole = (N & 7) == 0;
 #pragma unroll
-  for (int cb = 0; cb < kTileRows / 16; ++cb) {
-    if (cb >= 2 * live) break;
+  for (int cb = 0; cb < 2 * kLive; ++cb) {
     const int row = 16 * cb + lr;
     if (row >= t.rows) continue;
     uint16_t* y = a.y + (size_t)(t.row0 + row) * N + n;
@@ -394,6 +338,224 @@ __global__ __launch_bounds__(256, 2) void fp8_linear_tile_kernel(Fp8Args a) {
         if (i < have) y[i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
     }
   }
+}
+
+// A wave's share of a tile with kLive blocks of 32 rows; kWork: with weight rows, else it only loads its share of x.
+// (Each instance to its end: where they met again, the compiler moved and spilled their sums.)
+template <int kRows, int kWaves, int kLive, bool kWork>
+__device__ __forceinline__ void run_tile(const Fp8Args& args, const Tile& tile, int nw,
+                                         u32x4* const (&st)[Tiles<kRows, kWaves>::kStages], u32x4* own, const TileBuffers& r,
+                                         int kb, int wave) {
+  const int K = args.K;
+  f32x4 acc[4][2 * kLive] = {};
+  using T = Tiles<kRows, kWaves>;
+  constexpr int kStages = T::kStages, kAhead = T::kAhead, kRound = 8 * kWaves;
+  const int t = threadIdx.x, lane = t & 63, lr = lane & 15, q = lane >> 4;
+  // this thread's piece of a round of kRound rows of x
+  const int xrow = t >> 3, xpiece = (t & 7) ^ swizzle16(xrow & 15);
+  const uint32_t xoff = __umul24(xrow, K) + 16 * xpiece;
+  const int xleft = K - 1 - 16 * xpiece;  // a negative number for k past K is an offset past the buffer
+  // the first waves load the rows' scales, the last the weights' for the four waves; the others repeat
+  constexpr int kScaleWaves = kRows / 64;
+  const int scale_part = wave == kWaves - 1 ? kScaleWaves : wave % kScaleWaves;
+  const uint32_t soff = wave < kWaves - 1 ? __umul24(64 * scale_part + lane, 4 * kb)
+                        : lane < kWaves   ? (64 * lane / kBlock) * 4 * kb
+                                          : kDead;
+  static_assert(kScaleWaves < kWaves, "waves for the scales");
+  constexpr int kXRounds = 32 * kLive / kRound, kXLoads = kXRounds + 1, kWLoads = kWork ? 8 : 0;
+  // where chunk c starts, as a number that the compiler does not know: it would keep offsets of its own for each of a
+  // loop's chunks, in registers that are not there
+  auto start_of = [](int c) __attribute__((always_inline)) {
+    int k = c * kBlock;
+    asm("" : "+s"(k));
+    return k;
+  };
+  auto issue_x = [&](int k, int load, u32x4* to) __attribute__((always_inline)) {
+    if (load < kXRounds) {
+      const uint32_t o = (xoff + k) | ((uint32_t)(xleft - k) & kDead);
+      load_lds16(r.x, to + T::kScales + wave * 64 + load * 64 * kWaves, o + (uint32_t)(kRound * load) * K);
+    } else {
+      const uint32_t o = (soff + ((uint32_t)k >> 5)) | ((uint32_t)(kb - 1 - k / kBlock) & kDead);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r.s, (__attribute__((address_space(3))) void*)(to + 16 * scale_part), 4,
+                                               o, 0, 0, 0);
+    }
+  };
+  // load j of a chunk's weights: eight rows, 8 j + lane / 8, whole lines
+  const int wrow = lane >> 3;
+  const uint32_t woff = __umul24(wrow, K) + 16 * (lane & 7);
+  const int wleft = K - 1 - 16 * (lane & 7);
+  u32x4 w[kAhead][8];
+  auto issue_w = [&](int k, int j, u32x4& to) __attribute__((always_inline)) {
+    const uint32_t o = (woff + k) | ((uint32_t)(wleft - k) & kDead);
+    to = __builtin_amdgcn_raw_buffer_load_b128(r.w, o + (uint32_t)(8 * j) * K, 0, 0);
+  };
+  // weight row n = 16 (m / 4) + 4 i + m % 4 of the wave's 64 is operand row m of subtile i, so that a lane's outputs are
+  // sixteen neighbours; in LDS rows of 8 pieces, swizzled by m
+  const int put = wrow * 8 + ((lane & 7) ^ ((wrow >> 1) & 1));
+  auto put_w = [&](int j, const u32x4& from) __attribute__((always_inline)) {
+    own[64 * j + (put ^ (swizzle16(4 * (j >> 1))))] = from;
+  };
+  const int take = (16 * (lr >> 2) + (lr & 3)) * 8 + (q ^ swizzle16(lr));
+  // piece q of a row of a subtile; the other half's is 4 pieces on
+  const int xat = T::kScales + lr * 8 + (q ^ swizzle16(lr));
+
+#pragma unroll
+  for (int c = 0; c < kStages - 1; ++c) {
+#pragma unroll
+    for (int j = 0; j < kXLoads; ++j) issue_x(c * kBlock, j, st[c]);
+    __builtin_amdgcn_sched_barrier(0);  // the waits count on this order
+  }
+  if constexpr (kWork) {
+    u32x4 first[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) issue_w(0, j, first[j]);
+#pragma unroll
+    for (int c = 0; c < kAhead; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) issue_w((c + 1) * kBlock, j, w[(c + 1) % kAhead][j]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) put_w(j, first[j]);
+  }
+
+  // a product's sums are taken up kLag products later, when they are there, a chunk's last ones in the next chunk
+  constexpr int kSteps = 8 * kLive, kLag = kRows > 64 ? 2 : 4;
+  f32x4 part[kLag] = {};
+  float s[2] = {};
+  auto take_up_step = [&](auto at) __attribute__((always_inline)) {
+    constexpr int n = decltype(at)::value;
+    take_up(acc[n % 4][n / 4], part[n % kLag], s[(n / 4) & 1]);
+  };
+  int c0 = 0;
+  auto chunk = [&](auto at_chunk) __attribute__((always_inline)) {
+    constexpr int p = decltype(at_chunk)::value;
+    const int next_x = start_of(c0 + p + kStages - 1), next_w = start_of(c0 + p + 1 + kAhead);
+    // x of this chunk is there; loads of the later chunks' x and weights may be on their way
+    mxgemm::wait_loads_then_barrier<kWLoads + (kStages - 2) * (kXLoads + kWLoads)>();
+    u32x4* const to = st[(p + kStages - 1) % kStages];
+    if constexpr (!kWork) {
+#pragma unroll
+      for (int j = 0; j < kXLoads; ++j) issue_x(next_x, j, to);
+    } else {
+      const u32x4* from = st[p];
+      const float* sc = reinterpret_cast<const float*>(from);
+      u32x4 a[4][2], b[2][2];
+      float raw[2];
+      int x0 = xat, x1 = xat ^ 4, row = lr;
+      if constexpr (kRows <= 64) asm("" : "+v"(x0), "+v"(x1), "+v"(row));  // (as above: no addresses for each stage)
+      auto read = [&](int cb) __attribute__((always_inline)) {
+        b[cb & 1][0] = from[x0 + cb * 128];
+        b[cb & 1][1] = from[x1 + cb * 128];
+        raw[cb & 1] = sc[16 * cb + row];
+      };
+      read(0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i][0] = own[take + 32 * i];
+        a[i][1] = own[(take ^ 4) + 32 * i];
+      }
+      const float wscale = sc[kRows + wave];
+      __builtin_amdgcn_sched_barrier(0);
+      // once the operands are read, the next chunk's weights take their place in LDS
+      each_of([&](auto at) __attribute__((always_inline)) {
+        constexpr int n = decltype(at)::value, i = n % 4, cb = n / 4;
+        if constexpr (n % 4 == kLag % 4 && n >= kLag) s[((n - kLag) / 4) & 1] = raw[((n - kLag) / 4) & 1] * wscale;
+        if constexpr (i == 0 && cb + 1 < 2 * kLive) read(cb + 1);
+        take_up_step(std::integral_constant<int, n >= kLag ? n - kLag : kSteps - kLag + n>{});
+        part[n % kLag] = multiply(a[i][0], a[i][1], b[cb & 1][0], b[cb & 1][1]);
+        // (all of x before the weights: the wait above counts on it)
+        constexpr int kFirstW = kLive > 1 ? kXLoads : 0;
+        if constexpr (kLive == 1 && n == 0) {
+#pragma unroll
+          for (int j = 0; j < kXLoads; ++j) issue_x(next_x, j, to);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (kLive > 1 && n < kXLoads) issue_x(next_x, n, to);
+        if constexpr (n >= kFirstW && n < kFirstW + 8) {
+          put_w(n - kFirstW, w[(p + 1) % kAhead][n - kFirstW]);
+          issue_w(next_w, n - kFirstW, w[(p + 1) % kAhead][n - kFirstW]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        return true;
+      }, std::make_integer_sequence<int, kSteps>{});
+      if constexpr (kLag == 4) s[(2 * kLive - 1) & 1] = raw[(2 * kLive - 1) & 1] * wscale;
+    }
+  };
+  if constexpr (kRows > 64) {
+    // (two at least, and a copy for one more: with a loop that may not run the registers do not suffice; a chunk past K
+    // adds zeros)
+    do {
+      each_of([&](auto at) __attribute__((always_inline)) { return chunk(at), true; },
+              std::make_integer_sequence<int, kStages>{});
+      c0 += kStages;
+    } while (c0 + kStages <= kb);
+    if (c0 < kb) chunk(std::integral_constant<int, 0>{});
+  } else {
+    all_chunks<kStages>(kb, c0, chunk);
+  }
+  if constexpr (kWork)
+    each_of([&](auto at) __attribute__((always_inline)) {
+      take_up_step(std::integral_constant<int, kSteps - kLag + decltype(at)::value>{});
+      return true;
+    }, std::make_integer_sequence<int, kLag>{});
+  mxgemm::wait_loads_then_barrier<0>();  // no load still writes LDS
+  if constexpr (kWork) leave<kLive>(args, tile, nw, acc);
+}
+
+template <int kRows, int kWaves>
+__global__ __launch_bounds__(64 * kWaves, 2) void fp8_linear_tile_kernel(Fp8Args a) {
+  using T = Tiles<kRows, kWaves>;
+  __shared__ __attribute__((aligned(16))) u32x4 own[kWaves * T::kOwn];
+  __shared__ __attribute__((aligned(16))) u32x4 st0[T::kSlots], st1[T::kSlots];
+  const int n_tiles = (a.N + T::kN - 1) / T::kN;
+  int ti, nt;
+  if (!map_tile(a, a.tile_rows, n_tiles, ti, nt)) return;  // uniform per block
+  Tile t;
+  if (!find_tile(a, a.tile_rows, ti, t)) return;
+  const int K = a.K, N = a.N, n0 = nt * T::kN, kb = (K + kBlock - 1) / kBlock, nb = (N + kBlock - 1) / kBlock;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = n0 + wave * 64;
+  const bool work = nw < N;  // uniform
+  const TileBuffers r{
+      buffer(static_cast<const uint8_t*>(a.x) + (size_t)t.row0 * K, (uint32_t)t.rows * K),
+      buffer(a.w + ((size_t)t.e * N + (work ? nw : 0)) * K, (uint32_t)min(64, N - (work ? nw : 0)) * K),
+      wave == kWaves - 1
+          ? buffer(a.w_scales + ((size_t)t.e * nb + n0 / kBlock) * kb, (uint32_t)(nb - n0 / kBlock) * kb * 4)
+          : buffer(a.x_scales + (size_t)t.row0 * kb, (uint32_t)t.rows * kb * 4)};
+  const int live = (t.rows + 31) >> 5;
+  auto run = [&](u32x4* const (&st)[T::kStages]) __attribute__((always_inline)) {
+    u32x4* const mine = own + wave * T::kOwn;
+#define MX_CHUNKS(LIVE)                                                             \
+  do {                                                                              \
+    if (work) run_tile<kRows, kWaves, LIVE, true>(a, t, nw, st, mine, r, kb, wave); \
+    else run_tile<kRows, kWaves, LIVE, false>(a, t, nw, st, mine, r, kb, wave);     \
+  } while (0)
+    if constexpr (kRows > 64) {
+      if (live > 3) MX_CHUNKS(4);
+      else if (live > 2) MX_CHUNKS(3);
+    }
+    if (live == 2) MX_CHUNKS(2);
+    else if (live < 2) MX_CHUNKS(1);
+#undef MX_CHUNKS
+  };
+  if constexpr (T::kStages == 2) {
+    u32x4* const st[] = {st0, st1};
+    run(st);
+  } else {
+    static_assert(T::kStages == 4, "stages are arrays of their own");
+    __shared__ __attribute__((aligned(16))) u32x4 st2[T::kSlots], st3[T::kSlots];
+    u32x4* const st[] = {st0, st1, st2, st3};
+    run(st);
+  }
+}
+
+template <int kRows, int kWaves>
+hipError_t launch_tiles(Fp8Args a, int rows, hipStream_t stream) {
+  using T = Tiles<kRows, kWaves>;
+  a.tile_rows = rows;
+  a.max_tiles = max_tiles(a, rows);
+  fp8_linear_tile_kernel<kRows, kWaves>
+      <<<grid_of(a.max_tiles, (a.N + T::kN - 1) / T::kN), 64 * kWaves, 0, stream>>>(a);
+  return hipGetLastError();
 }
 
 // dx for row tiles of up to 64: 32x32x16 bf16 MFMA, a block of four waves makes
@@ -583,17 +745,16 @@ __global__ __launch_bounds__(256, 2) void fp8_linear_backward_tile_kernel(Fp8Arg
   }
 }
 
-template <int kC>
-hipError_t launch_few(Fp8Args a, int waves, hipStream_t stream) {
-  // as many row groups to a block (x is read once for all) as leave two blocks for every CU
-  a.max_tiles = max_tiles(a, kFewRows);
-  const int64_t groups = ((int64_t)a.N + 15) / 16 * a.max_tiles, want = 2 * mxfp4moe::device_cu_count();
-  const int g = groups >= 4 * want ? 4 : groups >= 2 * want ? 2 : 1;
-  const dim3 grid = grid_of(a.max_tiles, ((int64_t)a.N + 16 * g - 1) / (16 * g));
-  const size_t lds = (size_t)waves * g * 64 * sizeof(f32x4);
-  if (g == 4) fp8_linear_few_kernel<kC, 4><<<grid, waves * 64, lds, stream>>>(a);
-  else if (g == 2) fp8_linear_few_kernel<kC, 2><<<grid, waves * 64, lds, stream>>>(a);
-  else fp8_linear_few_kernel<kC, 1><<<grid, waves * 64, lds, stream>>>(a);
+template <int kR, int kG>
+hipError_t launch_few(Fp8Args a, hipStream_t stream) {
+  a.max_tiles = max_tiles(a, 16 * kR);
+  const int chunks = (a.K + kBlock - 1) / kBlock, waves = chunks < 8 ? chunks : 8, c = (chunks + waves - 1) / waves;
+  constexpr int c_most = kG + kR > 5 ? 2 : 3;  // what the registers hold
+  const dim3 grid = grid_of(a.max_tiles, ((int64_t)a.N + 16 * kG - 1) / (16 * kG));
+  const size_t lds = (size_t)waves * (kG * kR < kMeet ? kG * kR : kMeet) * 64 * sizeof(f32x4);
+  if (c == 1) fp8_linear_few_kernel<1, kG, kR><<<grid, waves * 64, lds, stream>>>(a);
+  else if (c == 2) fp8_linear_few_kernel<2, kG, kR><<<grid, waves * 64, lds, stream>>>(a);
+  else fp8_linear_few_kernel<c_most, kG, kR><<<grid, waves * 64, lds, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -607,14 +768,13 @@ hipError_t launch_fp8_linear(const uint8_t* x, const float* x_scales, const uint
   if (R == 0) return hipSuccess;
   Fp8Args a{x, x_scales, w, w_scales, bias, offsets, y, (int)R, (int)K, (int)N, (int)E, 0, 0};
   ProfileScope prof(kStageFp8Linear, stream);
-  if (R > 16 * E) {
-    a.tile_rows = 128;
-    a.max_tiles = max_tiles(a, a.tile_rows);
-    fp8_linear_tile_kernel<<<grid_of(a.max_tiles, (N + kTileN - 1) / kTileN), 256, 0, stream>>>(a);
-    return hipGetLastError();
+  const mxfp8::Plan p = mxfp8::plan_forward(R, N, E, device_cu_count());
+  if (p.few) {
+    if (p.rows == 16) return launch_few<1, 1>(a, stream);
+    return p.cols == 32 ? launch_few<2, 2>(a, stream) : launch_few<2, 4>(a, stream);
   }
-  const int chunks = (int)mx8::blocks_of(K), waves = chunks < 8 ? chunks : 8;
-  return (chunks + waves - 1) / waves <= 2 ? launch_few<2>(a, waves, stream) : launch_few<3>(a, waves, stream);
+  if (p.rows == 128) return launch_tiles<128, 4>(a, 128, stream);
+  return p.cols == 256 ? launch_tiles<64, 4>(a, 64, stream) : launch_tiles<64, 2>(a, p.rows, stream);
 }
 
 hipError_t launch_fp8_linear_backward(const uint16_t* dy, const uint8_t* w, const float* w_scales,

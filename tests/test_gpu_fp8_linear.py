@@ -138,6 +138,48 @@ def test_per_expert(gpu, counts, N, K):
     check_both(gpu, Weights(len(counts), N, K, seed=N), sum(counts), offsets_of(counts), label=f"{len(counts)} experts")
 
 
+# Sizes that reach each of the tiles of 32, 64 and 128 rows (csrc/fp8_plan.h), with one block of 128
+# and several, whole and cut ones, and counts of weight rows that leave waves with little or nothing.
+DENSE_TILES = [(R, N, K) for R, N in ((60, 2222), (120, 2500), (250, 2600), (500, 2564), (1000, 2690), (2100, 2600))
+               for K in (16, 128, 144, 256, 400, 768)]
+
+
+@pytest.mark.parametrize("R,N,K", DENSE_TILES)
+def test_dense_tiles(gpu, R, N, K):
+    check_both(gpu, Weights(1, N, K, seed=R + N, dense=True), R, bias=K % 128 != 0, label="dense")
+
+
+@pytest.mark.parametrize("mean", [1, 20, 70])
+@pytest.mark.parametrize("K", [112, 272, 512])
+def test_tiles_of_many_experts(gpu, mean, K):
+    """Uneven counts, an expert without rows and one with rows for several tiles among them."""
+    E = 64
+    counts = np.random.default_rng(mean + K).multinomial(mean * E, np.random.default_rng(mean).dirichlet(np.full(E, 2.0)))
+    counts[3], counts[17] = 0, counts[17] + counts[3]
+    check_both(gpu, Weights(E, 1100, K, seed=K), int(counts.sum()), offsets_of(counts), label=f"mean {mean}")
+
+
+@pytest.mark.parametrize("R,N,K", [(3, 96, 128), (60, 2222, 128), (250, 2600, 128), (500, 2564, 272), (1000, 2690, 128),
+                                   (2100, 2600, 128), (2100, 2600, 144)])
+def test_scales_that_are_not_finite_stay_in_their_places(gpu, R, N, K):
+    """An infinite or NaN scale of a row reaches that row, of a block of weights its outputs; nothing
+    else, blocks of zeros behind K included."""
+    w = Weights(1, N, K, seed=5, dense=True)
+    x, xs = torch.full((R, K), 0x38, dtype=torch.uint8, device="cuda").view(E4M3), torch.ones((R, L.blocks(K)), device="cuda")
+    w.codes.view(torch.uint8).fill_(0x38)
+    xs[R // 2, 0], xs[R - 1, -1] = float("nan"), float("inf")
+    y = gpu.moe_fp8_linear(x, xs, w.codes, w.scales)
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[R // 2], bad[R - 1] = True, True
+    assert torch.equal(~torch.isfinite(y), bad)
+    xs.fill_(1.0)
+    w.scales[-1, 0] = float("nan")
+    y = gpu.moe_fp8_linear(x, xs, w.codes, w.scales)
+    bad.fill_(False)
+    bad[:, (N - 1) // 128 * 128:] = True
+    assert torch.equal(torch.isnan(y), bad)
+
+
 def test_rows_of_no_expert_are_left(gpu):
     """A rank's share: rows before the first and from the last offset on keep what they held."""
     for counts, R, first in (([5, 0, 20], 60, 11), ([0, 0, 0], 9, 4), ([150, 90], 300, 33)):
