@@ -169,8 +169,6 @@ __global__ __launch_bounds__(512) void fp8_linear_few_kernel(Fp8Args a) {
   }
 }
 
-constexpr int kFewRows = 16;
-
 // Two codes (bytes 2 SEL and 2 SEL + 1 of `four`) as two bf16, exactly.
 template <int SEL>
 __device__ __forceinline__ uint32_t fp8x2_to_bf16x2(uint32_t four) {
@@ -182,8 +180,12 @@ __device__ __forceinline__ uint32_t fp8x2_to_bf16x2(uint32_t four) {
 // 4 m .. 4 m + 3 of a block's 64, of eight weight rows n = 8 q .. 8 q + 7,
 // converts them to pairs of k and exchanges halves between the rows of a pair
 // (v_perm) into four operands of eight n, one for each k.  The waves of a block
-// take every waves-th block of 128 n and add their sums in LDS in wave order.
+// take every waves-th block of 128 n and add their sums in LDS in wave order: one
+// row of 2880 x 2880 8.1 us, 64 rows 9.2.  (32 or 64 rows a block, to convert the
+// weights for more rows at a time, were no faster at any size: 64 rows 12.4 and
+// 19.8 us, 256 rows 22.2 and 19.8.)
 constexpr int kBackFewK = 64;
+constexpr int kBackFewRows = 16;
 constexpr int kRedStride = 20;  // floats per lane in LDS: 16 and padding
 
 template <bool kAligned>
@@ -193,7 +195,7 @@ __global__ __launch_bounds__(512) void fp8_linear_backward_few_kernel(Fp8Args a)
   int ti, kc;
   if (!map_block(a.max_tiles, k_chunks, ti, kc)) return;  // uniform per block
   Tile t;
-  if (!find_tile(a, kFewRows, ti, t)) return;
+  if (!find_tile(a, kBackFewRows, ti, t)) return;
   const int K = a.K, N = a.N, k0 = kc * kBackFewK, kb = (K + kBlock - 1) / kBlock, nb = (N + kBlock - 1) / kBlock;
   const int lane = mx::lane_id(), m = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
@@ -201,9 +203,9 @@ __global__ __launch_bounds__(512) void fp8_linear_backward_few_kernel(Fp8Args a)
   const uint16_t* dy0 = static_cast<const uint16_t*>(a.x) + (size_t)t.row0 * N;
   const auto rd = buffer(dy0, (uint32_t)t.rows * N * 2);
   const float* ws = a.w_scales + (size_t)t.e * nb * kb + k0 / kBlock;
-  const int row = min(m, t.rows - 1);  // columns past the tile's rows are dropped
   const uint32_t col = k0 + 4 * m;
 
+  const int row = min(m, t.rows - 1);  // columns past the tile's rows are dropped
   f32x4 acc[4] = {};
   for (int b = wave; b < nb; b += waves) {
     uint32_t w[4][8];
@@ -564,10 +566,17 @@ hipError_t launch_tiles(Fp8Args a, int rows, hipStream_t stream) {
 // bytes and dy travel into rings of LDS stages by the load unit.  The A operand
 // needs eight n of one k, so the codes are read transposed: of a group of
 // sixteen lanes each reads eight bytes of one of eight rows
-// (ds_read_b64_tr_b8), and lane c gets byte c of the eight rows.  Two blocks a
-// CU.
+// (ds_read_b64_tr_b8), and lane c gets byte c of the eight rows.  A half chunk's
+// operands are read while the products of the other are made, and a product's A
+// operand is converted while the one before runs.  Two blocks a CU.
+//   us at N = K = 2880: 512 dense rows 24.5, 2048 43, 16384 273 (990 TFLOP/s, the
+// matrix cores busy for 52% of the cycles at 1.84 GHz); 128 experts: 256 rows 194
+// and 1024 rows 230 (1.06 GB of weights at 4.6 TB/s), 16384 rows 423.  Rows of dy
+// that no 16 bytes divide travel through registers, element by element: 2048
+// rows at N = 2876 93 us.
 constexpr int kBackK = 256, kBackRows = 64, kBackStages = 3;
-constexpr int kWSlots = 1024, kDSlots = kBackRows * 8;  // 16-byte slots of a stage: 64 n x 256 codes, 64 rows x 64 n
+constexpr int kCodeSlots = 1024, kDSlots = kBackRows * 8;  // 16-byte slots of a stage: 64 n x 256 codes, 64 rows x 64 n
+constexpr int kWSlots = kCodeSlots + 4 * 16;              // ... and the codes' scale for each wave, 64 times
 
 typedef __attribute__((__vector_size__(2 * sizeof(int)))) int i32x2;
 using mx::f32x16;
@@ -576,157 +585,15 @@ __device__ __forceinline__ u32x4 fp8x8_to_bf16x8(i32x2 v) {
   return u32x4{fp8x2_to_bf16x2<0>(v[0]), fp8x2_to_bf16x2<1>(v[0]), fp8x2_to_bf16x2<0>(v[1]), fp8x2_to_bf16x2<1>(v[1])};
 }
 
-template <int kLive, bool kAligned>
-__device__ __forceinline__ void backward_chunks(f32x16 (&acc)[2][2], u32x4* const (&dst)[kBackStages],
-                                                u32x4* const (&wst)[kBackStages], const __amdgpu_buffer_rsrc_t& rd,
-                                                const uint16_t* dy, const __amdgpu_buffer_rsrc_t& rw,
-                                                const ScalarFloats ws, int rows, int K, int N, int kb, int k0,
-                                                int wave, bool work) {
-  const int t = threadIdx.x, lane = t & 63, half = lane >> 5, lrow = lane & 31, mg = (lane >> 4) & 1, c16 = lane & 15;
-  const int chunks = (N + 63) >> 6, nb = (chunks + 1) >> 1;
-  // this thread's pieces of a stage: of dy row pr (of 32), of weight row t / 16 (of 16)
-  const int pr = t >> 3, part_d = (t & 7) ^ swizzle(pr);
-  const uint32_t doff = (uint32_t)pr * N * 2 + 16 * part_d;
-  const uint32_t woff = (uint32_t)(t >> 4) * K + k0 + 16 * ((t & 15) ^ (((t >> 4) & 7) << 1));
-  constexpr int kLoads = kAligned ? 4 + kLive : 4;
-  u32x4 dreg[kLive];
-  auto load_dy = [&](int c) __attribute__((always_inline)) {
-    const int n = 64 * c + 8 * part_d;
-#pragma unroll
-    for (int k = 0; k < kLive; ++k)
-      dreg[k] = load_dy8<false>(rd, dy + (size_t)min(pr + 32 * k, rows - 1) * N, 0, n, N, 64 * c + 64 <= N);
-  };
-  auto store_dy = [&](u32x4* st) __attribute__((always_inline)) {
-#pragma unroll
-    for (int k = 0; k < kLive; ++k) st[t + k * 256] = dreg[k];
-  };
-  auto issue = [&](int c, u32x4* d, u32x4* w) __attribute__((always_inline)) {  // past N: zeros, or for dy the next row
-#pragma unroll
-    for (int k = 0; k < 4; ++k) load_lds16(rw, w + wave * 64 + k * 256, woff + (uint32_t)(64 * c + 16 * k) * K);
-    if constexpr (kAligned) {
-#pragma unroll
-      for (int k = 0; k < kLive; ++k)
-        load_lds16(rd, d + wave * 64 + k * 256, doff + (uint32_t)(k * 32) * N * 2 + c * 128);
-    }
-  };
-  if (!kAligned) {
-    load_dy(0);
-    store_dy(dst[0]);
-    load_dy(1);
-  }
-#pragma unroll
-  for (int c = 0; c < kBackStages - 1; ++c) {
-    __builtin_amdgcn_sched_barrier(0);  // the waits count on this order
-    issue(c, dst[c], wst[c]);
-  }
-  int boff[4];
-#pragma unroll
-  for (int s = 0; s < 4; ++s) boff[s] = lrow * 8 + ((2 * s + half) ^ swizzle(lrow));
-  // codes: this lane's address for row i = c16 / 2 of the eight of a step, byte 8 (c16 & 1) of the wave's piece 2 r + mg
-  const int ai = c16 >> 1;
-  int aoff[2];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) aoff[r] = (8 * half + ai) * 256 + (((wave * 4 + 2 * r + mg) ^ (ai << 1)) * 16) + 8 * (c16 & 1);
-
-  f32x16 part[2][2];
-  float wscale = ws[0];
-  int c0 = 0;
-  auto chunk = [&](auto at) __attribute__((always_inline)) {
-    constexpr int p = decltype(at)::value, kOdd = p & 1;
-    const int c = c0 + p;
-    mxgemm::wait_loads_then_barrier<(kBackStages - 2) * kLoads>();
-    if (!kAligned) {  // (every wave is past the stage that this one overwrites)
-      store_dy(dst[(p + 1) % kBackStages]);
-      load_dy(c + 2);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    issue(c + kBackStages - 1, dst[(p + kBackStages - 1) % kBackStages], wst[(p + kBackStages - 1) % kBackStages]);
-    if (kAligned && c == chunks - 1 && (N & 63) != 0) {  // uniform: dy past N becomes zeros as the weights there are
-      uint16_t* stage = reinterpret_cast<uint16_t*>(dst[p % kBackStages]);
-      for (int i = t; i < kLive * 32 * 64; i += 256) {
-        const int r = i >> 6, col = i & 63;
-        if (64 * c + col >= N) stage[r * 64 + 8 * ((col >> 3) ^ swizzle(r & 31)) + (col & 7)] = 0;
-      }
-      mxgemm::lds_reads_then_barrier();
-    }
-    if (work && c < chunks) {
-      const u32x4* base = dst[p % kBackStages];
-      const uint8_t* codes = reinterpret_cast<const uint8_t*>(wst[p % kBackStages]);
-      u32x4 b[4][kLive];
-      i32x2 w[4][2];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          w[s][r] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-              (__attribute__((address_space(3))) i32x2*)(codes + aoff[r] + s * 16 * 256));
-#pragma unroll
-        for (int cb = 0; cb < kLive; ++cb) b[s][cb] = base[boff[s] + cb * 256];
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const bf16x8 op = mx::as_bf16x8(fp8x8_to_bf16x8(w[s][r]));
-#pragma unroll
-          for (int cb = 0; cb < kLive; ++cb)
-            part[r][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op, mx::as_bf16x8(b[s][cb]),
-                                                                  s == 0 && !kOdd ? f32x16{} : part[r][cb], 0, 0, 0);
-        }
-    }
-    if constexpr (kOdd) {
-      if (work && c - 1 < chunks) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int cb = 0; cb < kLive; ++cb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[r][cb][i] = __builtin_fmaf(part[r][cb][i], wscale, acc[r][cb][i]);
-      }
-      wscale = ws[(size_t)min((c + 1) >> 1, nb - 1) * kb];
-    }
-  };
-  // whole periods without an exit, as above
-  for (; c0 < chunks; c0 += 2 * kBackStages)
-    each_of([&](auto at) __attribute__((always_inline)) { return chunk(at), true; },
-            std::make_integer_sequence<int, 2 * kBackStages>{});
-}
-
 constexpr int kOutStride = 72;  // bf16 per row of a wave's outputs in LDS: 64 and padding
 
-template <bool kAligned>
-__global__ __launch_bounds__(256, 2) void fp8_linear_backward_tile_kernel(Fp8Args a) {
-  __shared__ __attribute__((aligned(16))) u32x4 w0[kWSlots], w1[kWSlots], w2[kWSlots];
-  __shared__ __attribute__((aligned(16))) u32x4 d0[kDSlots], d1[kDSlots], d2[kDSlots];
-  const int k_tiles = (a.K + kBackK - 1) / kBackK;
-  int ti, kt;
-  if (!map_tile(a, a.tile_rows, k_tiles, ti, kt)) return;  // uniform per block
-  Tile t;
-  if (!find_tile(a, a.tile_rows, ti, t)) return;
-  const int K = a.K, N = a.N, k0 = kt * kBackK, kb = (K + kBlock - 1) / kBlock;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int kw = k0 + wave * 64;
-  const bool work = kw < K;  // uniform: a wave past K only loads its share
-  const uint16_t* dy = static_cast<const uint16_t*>(a.x) + (size_t)t.row0 * N;
-  const auto rd = buffer(dy, (uint32_t)t.rows * N * 2);
-  const auto rw = buffer(a.w + (size_t)t.e * N * K, (uint32_t)N * K);
-  const ScalarFloats ws = (ScalarFloats)(a.w_scales + (size_t)t.e * mx8::blocks_of(N) * kb + min(kw, K - 1) / kBlock);
-  u32x4* const dst[] = {d0, d1, d2};
-  u32x4* const wst[] = {w0, w1, w2};
-  f32x16 acc[2][2] = {};
-  const int live = (t.rows + 31) >> 5;
-  if (live == 2) backward_chunks<2, kAligned>(acc, dst, wst, rd, dy, rw, ws, t.rows, K, N, kb, k0, wave, work);
-  else backward_chunks<1, kAligned>(acc, dst, wst, rd, dy, rw, ws, t.rows, K, N, kb, k0, wave, work);
-
+// The rows of a wave's 64 k leave through `out`, LDS that nothing else uses any more.
+template <int kLive>
+__device__ __forceinline__ void leave_back(const Fp8Args& a, const Tile& t, int kw, uint16_t* out, const f32x16 (&acc)[2][kLive]) {
   // lane (row lane & 31 of the block, half): k = 32 r + 8 i + 4 half + j of the wave's 64 in acc[r][.][4 i + j]
-  mxgemm::wait_loads_then_barrier<0>();  // no load still writes LDS, no wave still reads it
-  if (!work) return;                     // no barrier follows
-  const int half = lane >> 5, lrow = lane & 31;
-  static_assert(32 * kOutStride * sizeof(uint16_t) <= sizeof(w0), "a wave's rows fit in a stage");
-  uint16_t* out = reinterpret_cast<uint16_t*>(wave == 0 ? w0 : wave == 1 ? w1 : wave == 2 ? w2 : d0);
+  const int lane = threadIdx.x & 63, half = lane >> 5, lrow = lane & 31, K = a.K;
 #pragma unroll
-  for (int cb = 0; cb < 2; ++cb) {
-    if (cb >= live) break;
+  for (int cb = 0; cb < kLive; ++cb) {
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -745,6 +612,183 @@ __global__ __launch_bounds__(256, 2) void fp8_linear_backward_tile_kernel(Fp8Arg
   }
 }
 
+// A wave's share of a tile with kLive blocks of 32 rows, as above.
+template <int kLive, bool kAligned, bool kWork>
+__device__ __forceinline__ void run_back(const Fp8Args& args, const Tile& tile, u32x4* const (&dst)[kBackStages],
+                                         u32x4* const (&wst)[kBackStages], const __amdgpu_buffer_rsrc_t& rd,
+                                         const __amdgpu_buffer_rsrc_t& rw, int k0, int wave) {
+  const int K = args.K, N = args.N, kb = (K + kBlock - 1) / kBlock, kw = k0 + 64 * wave;
+  f32x16 acc[2][kLive] = {};
+  const int t = threadIdx.x, lane = t & 63, half = lane >> 5, lrow = lane & 31, mg = (lane >> 4) & 1, c16 = lane & 15;
+  const int chunks = (N + 63) >> 6, nb = (chunks + 1) >> 1;
+  const auto rs = buffer(args.w_scales + (size_t)tile.e * nb * kb, (uint32_t)nb * kb * 4);
+  const uint32_t soff = 4 * (min(kw, K - 1) / kBlock);
+  // this thread's pieces of a stage: of dy row pr (of 32), of weight row t / 16 (of 16)
+  const int pr = t >> 3, part_d = (t & 7) ^ swizzle(pr);
+  const uint32_t doff = (uint32_t)pr * N * 2 + 16 * part_d;
+  const int dleft = N - 1 - 8 * part_d;  // a negative number for n past N is an offset past the buffer
+  const uint32_t woff = (uint32_t)(t >> 4) * K + k0 + 16 * ((t & 15) ^ (((t >> 4) & 7) << 1));
+  constexpr int kLoads = kAligned ? 5 + kLive : 5;
+  u32x4 dreg[kLive];
+  auto load_dy = [&](int c) __attribute__((always_inline)) {
+    const int n = 64 * c + 8 * part_d;
+#pragma unroll
+    for (int k = 0; k < kLive; ++k) {
+      uint32_t e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        e[i] = __builtin_amdgcn_raw_buffer_load_b16(rd, n + i < N ? ((uint32_t)(pr + 32 * k) * N + n + i) * 2 : kDead, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dreg[k][i] = e[2 * i] | (e[2 * i + 1] << 16);
+    }
+  };
+  auto store_dy = [&](u32x4* st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < kLive; ++k) st[t + k * 256] = dreg[k];
+  };
+  auto issue = [&](int c, u32x4* d, u32x4* w) __attribute__((always_inline)) {  // past N: zeros
+#pragma unroll
+    for (int k = 0; k < 4; ++k) load_lds16(rw, w + wave * 64 + k * 256, woff + (uint32_t)(64 * c + 16 * k) * K);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(w + kCodeSlots + wave * 16), 4,
+                                             soff + 4 * __umul24(c >> 1, kb), 0, 0, 0);
+    if constexpr (kAligned) {
+      const uint32_t o = (doff + 128 * c) | ((uint32_t)(dleft - 64 * c) & kDead);
+#pragma unroll
+      for (int k = 0; k < kLive; ++k) load_lds16(rd, d + wave * 64 + k * 256, o + (uint32_t)(k * 32) * N * 2);
+    }
+  };
+  if (!kAligned) {
+    load_dy(0);
+    store_dy(dst[0]);
+  }
+#pragma unroll
+  for (int c = 0; c < kBackStages; ++c) {
+    __builtin_amdgcn_sched_barrier(0);  // the waits count on this order
+    issue(c, dst[c], wst[c]);
+  }
+  int boff[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) boff[s] = lrow * 8 + ((2 * s + half) ^ swizzle(lrow));
+  // codes: this lane's address for row i = c16 / 2 of the eight of a step, byte 8 (c16 & 1) of the wave's piece 2 r + mg
+  const int ai = c16 >> 1;
+  int aoff[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) aoff[r] = (8 * half + ai) * 256 + (((wave * 4 + 2 * r + mg) ^ (ai << 1)) * 16) + 8 * (c16 & 1);
+
+  // operands of a half chunk, read while the other half's products are made
+  u32x4 b[2][2][kLive];
+  i32x2 w[2][2][2];
+  auto read = [&](auto at_half, int stage) __attribute__((always_inline)) {
+    constexpr int h = decltype(at_half)::value;
+    const u32x4* base = dst[stage];
+    const uint8_t* codes = reinterpret_cast<const uint8_t*>(wst[stage]);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        w[h][s][r] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            (__attribute__((address_space(3))) i32x2*)(codes + aoff[r] + (2 * h + s) * 16 * 256));
+#pragma unroll
+      for (int cb = 0; cb < kLive; ++cb) b[h][s][cb] = base[boff[2 * h + s] + cb * 256];
+    }
+  };
+  f32x16 part[2][kLive] = {};
+  float wscale = 0.f;
+  auto take_up_block = [&](int r, int cb) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[r][cb][i] = __builtin_fmaf(part[r][cb][i], wscale, acc[r][cb][i]);
+  };
+  // The products of a half chunk; the next A operand is converted while one runs.  first: they open a block of 128 n, and
+  // the sums of the last block are taken up.
+  u32x4 op;
+  auto multiply_half = [&](auto at_half, bool first) __attribute__((always_inline)) {
+    constexpr int h = decltype(at_half)::value;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int s = j >> 1, r = j & 1;
+      const bf16x8 now = mx::as_bf16x8(op);
+#pragma unroll
+      for (int cb = 0; cb < kLive; ++cb) {
+        if (first && s == 0) take_up_block(r, cb);
+        part[r][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now, mx::as_bf16x8(b[h][s][cb]),
+                                                              first && s == 0 ? f32x16{} : part[r][cb], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (cb == 0) op = fp8x8_to_bf16x8(j < 3 ? w[h][(j + 1) >> 1][(j + 1) & 1] : w[1 - h][0][0]);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr std::integral_constant<int, 0> kFirst{};
+  constexpr std::integral_constant<int, 1> kSecond{};
+  mxgemm::wait_loads_then_barrier<(kBackStages - 1) * kLoads>();
+  if constexpr (kWork) {
+    read(kFirst, 0);
+    op = fp8x8_to_bf16x8(w[0][0][0]);
+  }
+  int c0 = 0;
+  auto chunk = [&](auto at) __attribute__((always_inline)) {
+    constexpr int p = decltype(at)::value, stage = p % kBackStages, next = (p + 1) % kBackStages;
+    const int c = c0 + p;
+    if constexpr (kWork) {
+      read(kSecond, stage);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply_half(kFirst, p % 2 == 0);
+      if constexpr (p % 2 == 0) wscale = *reinterpret_cast<const float*>(wst[stage] + kCodeSlots + wave * 16);
+    }
+    if (!kAligned) {
+      load_dy(c + 1);
+      store_dy(dst[next]);
+    }
+    // the next chunk is there, and no wave still reads this one
+    mxgemm::wait_loads_then_barrier<(kBackStages - 2) * kLoads>();
+    if constexpr (kWork) {
+      read(kFirst, next);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    int ahead = __builtin_amdgcn_readfirstlane(c + kBackStages);
+    asm("" : "+s"(ahead));  // (as above: no offsets for each of a period's chunks)
+    issue(ahead, dst[stage], wst[stage]);
+    if constexpr (kWork) multiply_half(kSecond, false);
+  };
+  all_chunks<2 * kBackStages>(chunks, c0, chunk);
+  mxgemm::wait_loads_then_barrier<0>();  // no load still writes LDS, no wave still reads it
+  if constexpr (kWork) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int cb = 0; cb < kLive; ++cb) take_up_block(r, cb);
+    static_assert(32 * kOutStride * sizeof(uint16_t) <= kWSlots * 16, "a wave's rows fit in a stage");
+    static_assert(32 * kOutStride * sizeof(uint16_t) <= kDSlots * 16, "... of dy as well");
+    u32x4* const out = wave == 0 ? wst[0] : wave == 1 ? wst[1] : wave == 2 ? wst[2] : dst[0];
+    leave_back<kLive>(args, tile, kw, reinterpret_cast<uint16_t*>(out), acc);
+  }
+}
+
+template <bool kAligned>
+__global__ __launch_bounds__(256, 2) void fp8_linear_backward_tile_kernel(Fp8Args a) {
+  __shared__ __attribute__((aligned(16))) u32x4 w0[kWSlots], w1[kWSlots], w2[kWSlots];
+  __shared__ __attribute__((aligned(16))) u32x4 d0[kDSlots], d1[kDSlots], d2[kDSlots];
+  const int k_tiles = (a.K + kBackK - 1) / kBackK;
+  int ti, kt;
+  if (!map_tile(a, kBackRows, k_tiles, ti, kt)) return;  // uniform per block
+  Tile t;
+  if (!find_tile(a, kBackRows, ti, t)) return;
+  const int K = a.K, N = a.N, k0 = kt * kBackK;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool work = k0 + wave * 64 < K;  // uniform: a wave past K only loads its share
+  const auto rd = buffer(static_cast<const uint16_t*>(a.x) + (size_t)t.row0 * N, (uint32_t)t.rows * N * 2);
+  const auto rw = buffer(a.w + (size_t)t.e * N * K, (uint32_t)N * K);
+  u32x4* const dst[] = {d0, d1, d2};
+  u32x4* const wst[] = {w0, w1, w2};
+  if (t.rows > 32) {
+    if (work) run_back<2, kAligned, true>(a, t, dst, wst, rd, rw, k0, wave);
+    else run_back<2, kAligned, false>(a, t, dst, wst, rd, rw, k0, wave);
+  } else {
+    if (work) run_back<1, kAligned, true>(a, t, dst, wst, rd, rw, k0, wave);
+    else run_back<1, kAligned, false>(a, t, dst, wst, rd, rw, k0, wave);
+  }
+}
+
 template <int kR, int kG>
 hipError_t launch_few(Fp8Args a, hipStream_t stream) {
   a.max_tiles = max_tiles(a, 16 * kR);
@@ -755,6 +799,24 @@ hipError_t launch_few(Fp8Args a, hipStream_t stream) {
   if (c == 1) fp8_linear_few_kernel<1, kG, kR><<<grid, waves * 64, lds, stream>>>(a);
   else if (c == 2) fp8_linear_few_kernel<2, kG, kR><<<grid, waves * 64, lds, stream>>>(a);
   else fp8_linear_few_kernel<c_most, kG, kR><<<grid, waves * 64, lds, stream>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_back_tiles(Fp8Args a, hipStream_t stream) {
+  a.max_tiles = max_tiles(a, kBackRows);
+  const dim3 grid = grid_of(a.max_tiles, (a.K + kBackK - 1) / kBackK);
+  if (a.N % 8 == 0) fp8_linear_backward_tile_kernel<true><<<grid, 256, 0, stream>>>(a);
+  else fp8_linear_backward_tile_kernel<false><<<grid, 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_back_few(Fp8Args a, hipStream_t stream) {
+  a.max_tiles = max_tiles(a, kBackFewRows);
+  const int blocks = (int)mx8::blocks_of(a.N), waves = blocks < 8 ? blocks : 8;
+  const dim3 grid = grid_of(a.max_tiles, (a.K + kBackFewK - 1) / kBackFewK);
+  const size_t lds = (size_t)waves * 64 * kRedStride * sizeof(float);
+  if (a.N % 2 == 0) fp8_linear_backward_few_kernel<true><<<grid, waves * 64, lds, stream>>>(a);
+  else fp8_linear_backward_few_kernel<false><<<grid, waves * 64, lds, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -783,21 +845,7 @@ hipError_t launch_fp8_linear_backward(const uint16_t* dy, const uint8_t* w, cons
   if (R == 0) return hipSuccess;
   Fp8Args a{dy, nullptr, w, w_scales, nullptr, offsets, dx, (int)R, (int)K, (int)N, (int)E, 0, 0};
   ProfileScope prof(kStageFp8LinearBackward, stream);
-  if (R > 16 * E) {
-    a.tile_rows = kBackRows;
-    a.max_tiles = max_tiles(a, a.tile_rows);
-    const dim3 grid = grid_of(a.max_tiles, (K + kBackK - 1) / kBackK);
-    if (N % 2 == 0) fp8_linear_backward_tile_kernel<true><<<grid, 256, 0, stream>>>(a);
-    else fp8_linear_backward_tile_kernel<false><<<grid, 256, 0, stream>>>(a);
-    return hipGetLastError();
-  }
-  a.max_tiles = max_tiles(a, kFewRows);
-  const int blocks = (int)mx8::blocks_of(N), waves = blocks < 8 ? blocks : 8;
-  const dim3 grid = grid_of(a.max_tiles, (K + kBackFewK - 1) / kBackFewK);
-  const size_t lds = (size_t)waves * 64 * kRedStride * sizeof(float);
-  if (N % 2 == 0) fp8_linear_backward_few_kernel<true><<<grid, waves * 64, lds, stream>>>(a);
-  else fp8_linear_backward_few_kernel<false><<<grid, waves * 64, lds, stream>>>(a);
-  return hipGetLastError();
+  return mxfp8::backward_has_few(R, K, E, device_cu_count()) ? launch_back_few(a, stream) : launch_back_tiles(a, stream);
 }
 
 }  // namespace mxfp4moe

@@ -49,4 +49,15 @@ inline Plan plan_forward(int64_t rows, int64_t n, int64_t experts, int64_t cus) 
   return experts > 1 && rows < 64 * used ? Plan{false, 64, 256} : Plan{false, 128, 256};
 }
 
+// dx: the 16-row kernel up to two blocks of it a CU, for a dense matrix, which
+// stays in the caches for all its row tiles, four (us, 16 rows x 64 k and 64 x 256;
+// dense, N = K = 2880: 64 rows 9.2 and 23.9, 256 rows [720 blocks] 20.4 and 24.2,
+// 512 rows [1440] 33.9 and 24.4; 32 experts: 4 rows [180] 9.5 and 16.3, 16 rows
+// [720] 27.1 and 23.4; 8 experts, N = 1000, K = 736: 512 rows [384] 8.0 and 12.0,
+// 2048 rows [1536] 21.9 and 12.3; 128 experts, N = K = 736: 16 rows [192] 6.1 and
+// 7.3, 64 rows [768] 13.5 and 9.0).
+inline bool backward_has_few(int64_t rows, int64_t k, int64_t experts, int64_t cus) {
+  return blocks_of(rows, k, experts, 16, 64) <= (experts > 1 ? 2 : 4) * cus;
+}
+
 }  // namespace mxfp8

@@ -14,6 +14,9 @@ extern "C" int forward(int64_t rows, int64_t n, int64_t experts) {
   const mxfp8::Plan p = mxfp8::plan_forward(rows, n, experts, 256);
   return (p.few ? 1 : -1) * (1000 * p.rows + p.cols);
 }
+extern "C" int backward_few(int64_t rows, int64_t k, int64_t experts) {
+  return mxfp8::backward_has_few(rows, k, experts, 256);
+}
 """
 
 
@@ -25,7 +28,7 @@ def plan(tmp_path_factory):
                     "-I" + os.path.join(ROOT, "mxfp4_quantized_expert_amd", "csrc"), str(d / "shim.cpp"), "-o",
                     str(d / "shim.so")], check=True)
     lib = ctypes.CDLL(str(d / "shim.so"))
-    lib.forward.argtypes = [ctypes.c_int64] * 3
+    lib.forward.argtypes = lib.backward_few.argtypes = [ctypes.c_int64] * 3
 
     def forward(rows, n, experts):
         v = lib.forward(rows, n, experts)
@@ -65,3 +68,12 @@ def test_every_size_has_a_kernel(plan):
             for experts in (1, 2, 8, 32, 128, 4096):
                 seen.add(plan.choice(rows, n, experts))
     assert seen == built
+
+
+@pytest.mark.parametrize("rows,k,experts,few", [
+    (1, 2880, 1, True), (256, 2880, 1, True), (512, 2880, 1, False), (16384, 2880, 1, False), (300, 736, 8, True),
+    (512, 736, 8, True), (2048, 736, 8, False), (4, 2880, 32, True), (16, 2880, 32, False), (16, 736, 128, True),
+    (64, 736, 128, False), (16384, 2880, 128, False),
+])
+def test_backward(plan, rows, k, experts, few):
+    assert bool(plan.backward_few(rows, k, experts)) is few

@@ -149,6 +149,17 @@ def test_dense_tiles(gpu, R, N, K):
     check_both(gpu, Weights(1, N, K, seed=R + N, dense=True), R, bias=K % 128 != 0, label="dense")
 
 
+# ... and each path of the gradient's: N that 8 divides and not, shorter than a chunk of 64, with whole
+# periods of six of them and not, last row tiles of one block of 32 rows and two, K that leaves waves idle.
+@pytest.mark.parametrize("R,N,K", [(1040, 8, 1040), (1057, 64, 1040), (1040, 131, 1040), (2000, 72, 544), (1500, 384, 720),
+                                   (1100, 1096, 1008), (1090, 1150, 1008), (1040, 8200, 1040)])
+def test_dense_gradient_tiles(gpu, R, N, K):
+    w = Weights(1, N, K, seed=N, dense=True)
+    dy = normal(R, R, N, dtype=torch.bfloat16)
+    want, mag, _ = X.linear_backward(f64(dy), w.f64, None)
+    assert_sums(gpu.moe_fp8_linear_backward(dy, w.codes, w.scales), want, mag, N, "dx")
+
+
 @pytest.mark.parametrize("mean", [1, 20, 70])
 @pytest.mark.parametrize("K", [112, 272, 512])
 def test_tiles_of_many_experts(gpu, mean, K):
@@ -156,7 +167,8 @@ def test_tiles_of_many_experts(gpu, mean, K):
     E = 64
     counts = np.random.default_rng(mean + K).multinomial(mean * E, np.random.default_rng(mean).dirichlet(np.full(E, 2.0)))
     counts[3], counts[17] = 0, counts[17] + counts[3]
-    check_both(gpu, Weights(E, 1100, K, seed=K), int(counts.sum()), offsets_of(counts), label=f"mean {mean}")
+    for N in (1100, 1128):
+        check_both(gpu, Weights(E, N, K, seed=K), int(counts.sum()), offsets_of(counts), label=f"mean {mean}")
 
 
 @pytest.mark.parametrize("R,N,K", [(3, 96, 128), (60, 2222, 128), (250, 2600, 128), (500, 2564, 272), (1000, 2690, 128),
