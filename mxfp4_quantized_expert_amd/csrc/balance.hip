@@ -5,10 +5,12 @@
 //   c_e = picks of expert e by them;  density_e = E c_e / (sum_j c_j) / V
 //   loss = sum_t m_t sum_e p_te density_e  (= E sum_e (share of picks)_e (mean probability)_e)
 //   d_logits_te = d_loss m_t p_te (density_e - sum_j p_tj density_j)
-// The counts have no gradient.  Sixteen lanes hold a token's logits (64 beyond
-// 128 experts) and keep their experts' sums of probabilities over the tokens
+// The counts have no gradient.  Eight lanes hold a token's logits (sixteen beyond
+// 32 experts, 64 beyond 128) and keep their experts' sums of probabilities over the tokens
 // that they meet; sums are fp32 in an order fixed by the sizes, counts are
-// whole numbers in LDS.  HBM is the bound, and for a few tokens a launch.
+// whole numbers in LDS.  HBM is the bound, and for a few tokens a launch: 256
+// tokens of 32 experts 4.4 us and 2.8 (the gradient), 32768 of 128 6.4 + 5.4 and
+// 8.5 (50 MB of logits and gradients, 5.9 TB/s).
 #include "../../include/mxfp4moe.h"
 #include "internal.h"
 #include "mx_device.h"
@@ -17,9 +19,14 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
+constexpr int kAlone = 4;  // rounds of tokens that one block takes alone
 
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 typedef f32x4v f32x4loose __attribute__((aligned(4)));
+typedef int32_t i32x4v __attribute__((ext_vector_type(4)));
+typedef i32x4v i32x4loose __attribute__((aligned(4)));
+
+constexpr int kDppHalfMirror = 0x141;  // lane i of eight gets lane 7 - i's
 
 // A token's logits over kLanes lanes, kPer of them each: chunk j of a lane is
 // experts 4 (kLanes j + lane) .. + 3.
@@ -48,12 +55,15 @@ struct Token {
     if constexpr (kLanes == 64) return mx::wave_sum_f32(x);
     x += __int_as_float(mx::dpp_i32<mx::kDppQuadXor1>(__float_as_int(x)));
     x += __int_as_float(mx::dpp_i32<mx::kDppQuadXor2>(__float_as_int(x)));
+    if constexpr (kLanes == 8) return x + __int_as_float(mx::dpp_i32<kDppHalfMirror>(__float_as_int(x)));
     x += __int_as_float(mx::dpp_i32<mx::kDppRowRor4>(__float_as_int(x)));
     return x + __int_as_float(mx::dpp_i32<mx::kDppRowRor8>(__float_as_int(x)));
   }
   static __device__ __forceinline__ float largest(float x) {
     x = __builtin_elementwise_maximum(x, __int_as_float(mx::dpp_i32<mx::kDppQuadXor1>(__float_as_int(x))));
     x = __builtin_elementwise_maximum(x, __int_as_float(mx::dpp_i32<mx::kDppQuadXor2>(__float_as_int(x))));
+    if constexpr (kLanes == 8)
+      return __builtin_elementwise_maximum(x, __int_as_float(mx::dpp_i32<kDppHalfMirror>(__float_as_int(x))));
     x = __builtin_elementwise_maximum(x, __int_as_float(mx::dpp_i32<mx::kDppRowRor4>(__float_as_int(x))));
     x = __builtin_elementwise_maximum(x, __int_as_float(mx::dpp_i32<mx::kDppRowRor8>(__float_as_int(x))));
     if constexpr (kLanes == 64) {
@@ -95,36 +105,48 @@ struct BalanceArgs {
   float* loss;
   int32_t* counts;
   float* density;
-  // sums of the blocks, where there are several: [blocks][E] probabilities, [blocks][E] counts, [blocks] tokens
-  float* part_p;
-  int32_t* part_c;
-  int32_t* part_live;
+  float* part;  // sums of the blocks, where there are several: rows of part_floats(E)
 };
 
-// Sum over the block's threads in a fixed order, in every thread.
-template <typename V>
-__device__ V block_sum(V v, V* lds) {
-  __syncthreads();
-  lds[threadIdx.x] = v;
-  __syncthreads();
-  for (int n = kThreads / 2; n > 0; n >>= 1) {
-    if ((int)threadIdx.x < n) lds[threadIdx.x] += lds[threadIdx.x + n];
-    __syncthreads();
-  }
-  return lds[0];
+// E sums of probabilities, E counts and the tokens that count.
+__host__ __device__ constexpr int padded(int E) { return (E + 3) & ~3; }
+__host__ __device__ constexpr int part_floats(int E) { return 2 * padded(E) + 4; }
+
+__device__ __forceinline__ int32_t wave_total(int32_t v) {
+  return __builtin_amdgcn_readlane(mx::wave_inclusive_sum(v), 63);
 }
 
-// Thread e < E has its expert's sum of probabilities and count.
-__device__ void finish(const BalanceArgs& a, float p, int32_t count, int32_t live, float* lds) {
-  const int e = threadIdx.x;
-  const int32_t picks = block_sum<int32_t>(e < a.E ? count : 0, reinterpret_cast<int32_t*>(lds));
-  const float density = (float)a.E * ((float)count / (float)max(picks, 1)) / (float)max(live, 1);
+// Thread e < E has its expert's sum of probabilities and count, each thread the tokens that it counted.  sums: LDS.
+__device__ void finish(const BalanceArgs& a, float p, int32_t count, int32_t live, float* sums) {
+  const int e = threadIdx.x, wave = threadIdx.x >> 6;
+  int32_t* const picks_of = reinterpret_cast<int32_t*>(sums);  // [3][kWaves]: picks, tokens, loss
+  const int32_t w_picks = wave_total(count), w_live = wave_total(live);
+  __syncthreads();  // (sums is free)
+  if (mx::lane_id() == 0) {
+    picks_of[wave] = w_picks;
+    picks_of[kWaves + wave] = w_live;
+  }
+  __syncthreads();
+  int32_t picks = 0, tokens = 0;
+#pragma unroll
+  for (int u = 0; u < kWaves; ++u) {
+    picks += picks_of[u];
+    tokens += picks_of[kWaves + u];
+  }
+  const float density = (float)a.E * ((float)count / (float)max(picks, 1)) / (float)max(tokens, 1);
   if (e < a.E) {
     a.counts[e] = count;
     a.density[e] = density;
   }
-  const float loss = block_sum<float>(e < a.E ? p * density : 0.f, lds);
-  if (e == 0) *a.loss = loss;
+  const float w_loss = mx::wave_sum_f32(p * density);
+  if (mx::lane_id() == 0) sums[2 * kWaves + wave] = w_loss;
+  __syncthreads();
+  if (e == 0) {
+    float loss = 0.f;
+#pragma unroll
+    for (int u = 0; u < kWaves; ++u) loss += sums[2 * kWaves + u];
+    *a.loss = loss;
+  }
 }
 
 template <int kLanes, int kPer>
@@ -132,38 +154,46 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a) {
   using Tk = Token<kLanes, kPer>;
   constexpr int kRound = kThreads / kLanes;  // tokens of a block at a time
   __shared__ int32_t counts[MXFP4MOE_MAX_EXPERTS];
-  __shared__ int32_t live;
-  __shared__ float sums[kThreads > kWaves * kLanes * kPer ? kThreads : kWaves * kLanes * kPer];
-  const int E = a.E;
-  for (int e = threadIdx.x; e < E; e += kThreads) counts[e] = 0;
-  if (threadIdx.x == 0) live = 0;
-  __syncthreads();
-  float p[kPer] = {};
-  for (int64_t t0 = (int64_t)blockIdx.x * kRound; t0 < a.T; t0 += (int64_t)gridDim.x * kRound) {
-    const int n = (int)min((int64_t)kRound, a.T - t0);
-    const int at = threadIdx.x / kLanes;
-    const bool counts_here = at < n && (a.mask == nullptr || a.mask[t0 + at] != 0);
-    float v[kPer];
-    if (counts_here) {
-      Tk::load(a.logits + (t0 + at) * E, E, -__builtin_inff(), v);
+  __shared__ float sums[kWaves * kLanes * kPer];
+  const int E = a.E, at = threadIdx.x / kLanes;
+  const int64_t step = (int64_t)gridDim.x * kRound;
+  bool next_counts;
+  float next[kPer];
+  auto load = [&](int64_t t0) __attribute__((always_inline)) {
+    next_counts = t0 + at < a.T && (a.mask == nullptr || a.mask[t0 + at] != 0);
+    if (next_counts) {
+      Tk::load(a.logits + (t0 + at) * E, E, -__builtin_inff(), next);
     } else {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = -__builtin_inff();
+      for (int i = 0; i < kPer; ++i) next[i] = -__builtin_inff();
     }
-    Tk::softmax(v);
+  };
+  load((int64_t)blockIdx.x * kRound);
+  for (int e = threadIdx.x; e < E; e += kThreads) counts[e] = 0;
+  __syncthreads();
+  float p[kPer] = {};
+  int32_t live = 0;
+  for (int64_t t0 = (int64_t)blockIdx.x * kRound; t0 < a.T; t0 += step) {
+    const int n = (int)min((int64_t)kRound, a.T - t0);
+    float v[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) p[i] += v[i];
-    if (counts_here && (threadIdx.x & (kLanes - 1)) == 0) atomicAdd(&live, 1);
+    for (int i = 0; i < kPer; ++i) v[i] = next[i];
+    live += next_counts && (threadIdx.x & (kLanes - 1)) == 0;
+    if (t0 + step < a.T) load(t0 + step);  // (uniform: past the last token there is nothing to load)
     for (int i = threadIdx.x; i < n * a.top_k; i += kThreads) {
       const int32_t e = a.ids[t0 * a.top_k + i];
       if (e >= 0 && e < E && (a.mask == nullptr || a.mask[t0 + i / a.top_k] != 0)) atomicAdd(&counts[e], 1);
     }
+    Tk::softmax(v);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) p[i] += v[i];
   }
   // the tokens of a wave, then the waves
   const int lane = mx::lane_id(), wave = threadIdx.x >> 6;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    if constexpr (kLanes == 16) {
+    if constexpr (kLanes == 8) p[i] += __shfl_xor(p[i], 8);
+    if constexpr (kLanes <= 16) {
       p[i] += __shfl_xor(p[i], 16);
       p[i] += __shfl_xor(p[i], 32);
     }
@@ -181,41 +211,72 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a) {
     finish(a, sum, count, live, sums);
     return;
   }
-  if (e < E) {
-    a.part_p[(size_t)blockIdx.x * E + e] = sum;
-    a.part_c[(size_t)blockIdx.x * E + e] = count;
+  float* const row = a.part + (size_t)blockIdx.x * part_floats(E);
+  int32_t* const irow = reinterpret_cast<int32_t*>(row);
+  if (e < padded(E)) {
+    row[e] = sum;
+    irow[padded(E) + e] = count;
   }
-  if (e == 0) a.part_live[blockIdx.x] = live;
+  const int32_t w_live = wave_total(live);
+  __syncthreads();
+  if (lane == 0) counts[wave] = w_live;
+  __syncthreads();
+  if (e < 4) {
+    int32_t all = 0;
+#pragma unroll
+    for (int u = 0; u < kWaves; ++u) all += counts[u];
+    irow[2 * padded(E) + e] = e == 0 ? all : 0;
+  }
 }
 
-// The blocks' sums joined, by one block: 512 / `slices` experts at a time.
-__global__ __launch_bounds__(kThreads) void balance_join_kernel(BalanceArgs a, int blocks, int lg_experts) {
-  __shared__ float sums[kThreads];
-  __shared__ int32_t counts[kThreads];
-  const int experts = 1 << lg_experts, e = threadIdx.x & (experts - 1), slice = threadIdx.x >> lg_experts;
-  const int slices = kThreads >> lg_experts;
-  float p = 0.f;
-  int32_t c = 0, n = 0;
+// The blocks' sums joined, by one block: 1 << lg_lanes lanes read a row of
+// them, 16 bytes each, as many rows at a time as the block has lanes for, and
+// their sums meet in LDS.  256 rows of 128 experts take 5.4 us, 2 of them the
+// 266 KB that one CU reads.
+constexpr int kJoinRows = 8;  // of a lane at a time
+__global__ __launch_bounds__(kThreads) void balance_join_kernel(BalanceArgs a, int blocks, int lg_lanes) {
+  __shared__ f32x4v sums[kThreads], counts[kThreads];
+  const int lanes = 1 << lg_lanes, l = threadIdx.x & (lanes - 1), slice = threadIdx.x >> lg_lanes;
+  const int slices = kThreads >> lg_lanes, stride = part_floats(a.E), E4 = padded(a.E);
+  f32x4v p = {};
+  i32x4v c = {};
+  int32_t live = 0;
+  for (int b = threadIdx.x; b < blocks; b += kThreads)
+    live += reinterpret_cast<const int32_t*>(a.part)[(size_t)b * stride + 2 * E4];
+  if (4 * l < E4) {
+    for (int b0 = slice; b0 < blocks; b0 += kJoinRows * slices) {
+      f32x4v pv[kJoinRows];
+      i32x4v cv[kJoinRows];
+#pragma unroll
+      for (int i = 0; i < kJoinRows; ++i) {
+        const int b = b0 + i * slices;
+        const float* row = a.part + (size_t)(b < blocks ? b : b0) * stride + 4 * l;
+        pv[i] = *reinterpret_cast<const f32x4loose*>(row);
+        cv[i] = *reinterpret_cast<const i32x4loose*>(row + E4);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // all loads on their way
+#pragma unroll
+      for (int i = 0; i < kJoinRows; ++i) {
+        if (b0 + i * slices >= blocks) break;
+        p += pv[i];
+        c += cv[i];
+      }
+    }
+  }
+  sums[threadIdx.x] = p;
+  counts[threadIdx.x] = __builtin_bit_cast(f32x4v, c);
+  __syncthreads();
+  const int e = threadIdx.x;
+  float sum = 0.f;
+  int32_t count = 0;
   if (e < a.E) {
 #pragma unroll 8
-    for (int b = slice; b < blocks; b += slices) {
-      p += a.part_p[(size_t)b * a.E + e];
-      c += a.part_c[(size_t)b * a.E + e];
+    for (int s = 0; s < min(slices, blocks); ++s) {
+      sum += reinterpret_cast<const float*>(sums)[4 * (s << lg_lanes) + e];
+      count += reinterpret_cast<const int32_t*>(counts)[4 * (s << lg_lanes) + e];
     }
   }
-  for (int b = threadIdx.x; b < blocks; b += kThreads) n += a.part_live[b];
-  sums[threadIdx.x] = p;
-  counts[threadIdx.x] = c;
-  __syncthreads();
-  if ((int)threadIdx.x < experts) {
-    for (int s = 1; s < slices; ++s) {
-      p += sums[s * experts + e];
-      c += counts[s * experts + e];
-    }
-  }
-  const int32_t live = block_sum<int32_t>(n, counts);
-  __syncthreads();
-  finish(a, p, c, live, sums);
+  finish(a, sum, count, live, reinterpret_cast<float*>(sums));
 }
 
 template <int kLanes, int kPer>
@@ -272,11 +333,15 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(const float* __re
   }
 }
 
-// Blocks of the loss's kernel: one for every CU at most.
+int lanes_of(int64_t E) { return E <= 32 ? 8 : E <= 128 ? 16 : 64; }  // of a token
+
+// Blocks of the loss's kernel: one for every CU at most, and a single one, which
+// needs no second launch, up to four rounds of its tokens (256 tokens of 32
+// experts in four rounds 5.5 us, in four blocks 3.2 and 5.4 to join them).
 int64_t loss_blocks(int64_t T, int64_t E) {
-  const int64_t round = kThreads / (E <= 128 ? 16 : 64), n = (T + round - 1) / round;
+  const int64_t round = kThreads / lanes_of(E), n = (T + round - 1) / round;
   const int64_t most = mxfp4moe::device_cu_count();
-  return n < 1 ? 1 : n < most ? n : most;
+  return n <= kAlone ? 1 : n < most ? n : most;
 }
 
 }  // namespace
@@ -285,26 +350,22 @@ namespace mxfp4moe {
 
 size_t balance_loss_workspace(int64_t T, int64_t E) {
   const int64_t blocks = loss_blocks(T, E);
-  return blocks > 1 ? (size_t)blocks * (2 * (size_t)E + 1) * 4 : 0;
+  return blocks > 1 ? (size_t)blocks * part_floats((int)E) * sizeof(float) : 0;
 }
 
 hipError_t launch_balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask, int64_t T, int64_t E,
                                int64_t top_k, float* loss, int32_t* counts, float* density, void* workspace,
                                hipStream_t stream) {
   const int64_t blocks = loss_blocks(T, E);
-  BalanceArgs a{logits, ids, mask, T, (int)E, (int)top_k, loss, counts, density, nullptr, nullptr, nullptr};
-  if (blocks > 1) {
-    a.part_p = static_cast<float*>(workspace);
-    a.part_c = static_cast<int32_t*>(workspace) + blocks * E;
-    a.part_live = a.part_c + blocks * E;
-  }
+  const BalanceArgs a{logits, ids, mask, T, (int)E, (int)top_k, loss, counts, density, static_cast<float*>(workspace)};
   ProfileScope prof(kStageBalance, stream);
-  if (E <= 64) balance_kernel<16, 4><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+  if (E <= 32) balance_kernel<8, 4><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+  else if (E <= 64) balance_kernel<16, 4><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
   else if (E <= 128) balance_kernel<16, 8><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
   else balance_kernel<64, 8><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
   if (blocks > 1) {
     int lg = 3;
-    while ((1 << lg) < E) ++lg;
+    while ((4 << lg) < E) ++lg;
     balance_join_kernel<<<1, kThreads, 0, stream>>>(a, (int)blocks, lg);
   }
   return hipGetLastError();
@@ -314,10 +375,12 @@ hipError_t launch_balance_loss_backward(const float* logits, const float* densit
                                         const uint8_t* mask, const float* add, int64_t T, int64_t E, float* d_logits,
                                         hipStream_t stream) {
   if (T == 0) return hipSuccess;
-  const int64_t round = 256 / (E <= 128 ? 16 : 64), n = (T + round - 1) / round, most = 16 * device_cu_count();
+  const int64_t round = 256 / lanes_of(E), n = (T + round - 1) / round, most = 16 * device_cu_count();
   const unsigned grid = (unsigned)(n < most ? n : most);
   ProfileScope prof(kStageBalanceBackward, stream);
-  if (E <= 64)
+  if (E <= 32)
+    balance_backward_kernel<8, 4><<<grid, 256, 0, stream>>>(logits, density, d_loss, mask, add, T, (int)E, d_logits);
+  else if (E <= 64)
     balance_backward_kernel<16, 4><<<grid, 256, 0, stream>>>(logits, density, d_loss, mask, add, T, (int)E, d_logits);
   else if (E <= 128)
     balance_backward_kernel<16, 8><<<grid, 256, 0, stream>>>(logits, density, d_loss, mask, add, T, (int)E, d_logits);

@@ -54,6 +54,7 @@ def check(gpu, lg, ids, mask, g=0.37):
 
 
 SIZES = [(1, 1, 1), (1, 8, 2), (5, 3, 3), (64, 32, 4), (65, 33, 4), (256, 32, 4), (1000, 64, 8), (777, 65, 3),
+         (512, 31, 4), (513, 32, 4), (9, 5, 2), (256, 66, 4), (257, 128, 4), (70, 500, 3), (17000, 1, 1),
          (300, 127, 4), (4096, 128, 4), (130, 129, 2), (515, 512, 32), (33000, 10, 2), (20000, 200, 1)]
 
 
