@@ -9,7 +9,10 @@
 // fp32 throughout, one rounding at the end.  A row lies in the registers of
 // one wave (or of four or sixteen of one block), 8 elements a piece, so that
 // each tensor moves once; HBM is the bound, and for a few rows the latency of
-// a launch.
+// a launch.  us and TB/s, bf16, with a residual: 4 x 2880 3.2 forward and 6.0
+// backward (two launches), 4096 x 2880 17.5 (5.4), in 8 bits 17.8 (4.6), backward
+// 21.7 (4.4), 16384 x 2880 74 (5.1), 68 (4.8) and 79 (4.8); 777 x 1001 float32 4.5
+// and 8.7.
 #include "fp8_device.h"
 #include "internal.h"
 #include "mx_device.h"
@@ -35,8 +38,8 @@ struct NormArgs {
   int H;
 };
 
-// The sum over a row's waves, in every lane of them.  kWaves > 1: they are the
-// block.
+// The sum over a row's waves, in every lane of them.  kWaves > 1: every wave of
+// the block takes part, for its row.
 template <int kWaves>
 __device__ __forceinline__ float row_sum(float v, float* part) {
   v = mx::wave_sum_f32(v);
@@ -45,8 +48,9 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
     if (mx::lane_id() == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
     v = 0.f;
+    const int first = threadIdx.x / (64 * kWaves) * kWaves;
 #pragma unroll
-    for (int u = 0; u < kWaves; ++u) v += part[u];
+    for (int u = 0; u < kWaves; ++u) v += part[first + u];
   }
   return v;
 }
@@ -116,16 +120,26 @@ struct NormBackArgs {
   int H;
 };
 
+// Pieces of a lane that the registers hold: 256 bytes of a row in each kernel's largest form.
+template <typename E>
+constexpr int kMostPieces = sizeof(E) == 4 ? 4 : 8;
+
+// Rows of a block at a time: what sixteen waves a CU, two blocks, have registers
+// for (4096 x 2880 bf16 21.7 us, with one row of four waves 24.3; 777 x 1001
+// float32, in one round instead of two, 8.7 and 10.3).
+constexpr int back_rows(int waves, int pieces, int most) { return waves == 1 ? 4 : waves == 4 && pieces < most ? 2 : 1; }
+
 // A block takes every gridDim.x-th group of kRows rows and keeps its columns'
 // sums of d_weight in registers; they meet in LDS in wave order and leave as
 // one row of `part`.
 template <typename E, typename W, int kWaves, int kP>
-__global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : 256) void rms_norm_backward_kernel(NormBackArgs a) {
+__global__ __launch_bounds__(64 * kWaves * back_rows(kWaves, kP, kMostPieces<E>)) void rms_norm_backward_kernel(
+    NormBackArgs a) {
   using Pc = Piece<E, kPiece>;
-  constexpr int kRows = kWaves > 4 ? 1 : 4 / kWaves;
+  constexpr int kRows = back_rows(kWaves, kP, kMostPieces<E>);
   __shared__ float part[16];
   const int lane = mx::lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = wave % kWaves;
-  const int H = a.H, nv = (H + kPiece - 1) / kPiece;
+  const int H = a.H, all = (H + kPiece - 1) / kPiece;
   const E* dys = static_cast<const E*>(a.dy);
   const E* ds = static_cast<const E*>(a.d_summed);
   const E* hs = static_cast<const E*>(a.summed);
@@ -133,7 +147,10 @@ __global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : 256) void rms_norm_backw
   f32x8 dw[kP];
 #pragma unroll
   for (int i = 0; i < kP; ++i) dw[i] = f32x8{};
-  for (int64_t t = (int64_t)blockIdx.x * kRows + wave / kWaves; t < a.T; t += (int64_t)gridDim.x * kRows) {
+  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < a.T; t0 += (int64_t)gridDim.x * kRows) {
+    const int64_t t = t0 + wave / kWaves;
+    if (kWaves == 1 && t >= a.T) break;
+    const int nv = t < a.T ? all : 0;  // (the block's barriers are for every wave)
     typename Pc::vec h[kP], g[kP], d[kP];
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
@@ -142,7 +159,7 @@ __global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : 256) void rms_norm_backw
       g[i] = v < nv ? mx8::load_piece(dys + t * H, v, H) : typename Pc::vec{};
       d[i] = ds != nullptr && v < nv ? mx8::load_piece(ds + t * H, v, H) : typename Pc::vec{};
     }
-    const float r = a.rstd[t];
+    const float r = t < a.T ? a.rstd[t] : 0.f;
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
@@ -167,68 +184,84 @@ __global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : 256) void rms_norm_backw
     }
   }
   float* out = a.part + (size_t)blockIdx.x * H;
-  if constexpr (kRows > 1) {
-    extern __shared__ __attribute__((aligned(32))) float sums[];  // [nv * kPiece]
-    for (int u = 0; u < kRows; ++u) {
-      if (wave == u) {
+  extern __shared__ __attribute__((aligned(32))) float sums[];  // [all * kPiece] where kRows > 1
 #pragma unroll
-        for (int i = 0; i < kP; ++i) {
-          const int v = i * 64 + lane;
-          if (v >= nv) continue;
-          f32x8* at = reinterpret_cast<f32x8*>(sums + kPiece * v);
-          if (u > 0) dw[i] += *at;
-          if (u + 1 < kRows) *at = dw[i];
-          else mx8::store_piece(out, v, H, dw[i]);
-        }
+  for (int u = 0; u < kRows; ++u) {
+    if (wave / kWaves == u) {
+#pragma unroll
+      for (int i = 0; i < kP; ++i) {
+        const int v = (i * kWaves + sub) * 64 + lane;
+        if (v >= all) continue;
+        f32x8* at = reinterpret_cast<f32x8*>(sums + kPiece * v);
+        if (u > 0) dw[i] += *at;
+        if (u + 1 < kRows) *at = dw[i];
+        else mx8::store_piece(out, v, H, dw[i]);
       }
-      __syncthreads();
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kP; ++i) {
-      const int v = (i * kWaves + sub) * 64 + lane;
-      if (v < nv) mx8::store_piece(out, v, H, dw[i]);
-    }
+    if (u + 1 < kRows) __syncthreads();
   }
 }
 
-// d_weight[i] = sum of the blocks' rows of `part`: 64 columns a block, its
-// sixteen waves a sixteenth of the rows each, added in wave order.
-constexpr int kJoinWaves = 16;
+// d_weight[i] = sum of the blocks' rows of `part`: 32 columns a block, eight
+// rows a wave at a time and sixteen bytes a lane, kJoinRows of them in flight;
+// the lanes' sums meet in the wave, then the waves' in order.
+constexpr int kJoinWaves = 16, kJoinCols = 32, kJoinRows = 4;
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+typedef f32x4v f32x4loose __attribute__((aligned(4)));
+
 __global__ __launch_bounds__(64 * kJoinWaves) void rms_norm_join_kernel(const float* __restrict__ part, int rows,
                                                                         int H, float* __restrict__ d_weight) {
-  __shared__ float sums[kJoinWaves][64];
-  const int lane = mx::lane_id(), wave = threadIdx.x >> 6, col = blockIdx.x * 64 + lane;
-  float s = 0.f;
-  if (col < H) {
-#pragma unroll 8
-    for (int r = wave; r < rows; r += kJoinWaves) s += part[(size_t)r * H + col];
+  __shared__ f32x4v sums[kJoinWaves][kJoinCols / 4];
+  constexpr int kStep = 8 * kJoinWaves;
+  const int lane = mx::lane_id(), wave = threadIdx.x >> 6, at = 4 * (lane & 7), col = blockIdx.x * kJoinCols + at;
+  f32x4v s = {};
+  for (int r0 = 8 * wave + (lane >> 3); r0 < rows; r0 += kJoinRows * kStep) {
+    f32x4v v[kJoinRows];
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i) {
+      const int r = r0 + i * kStep;
+      const float* from = part + (size_t)r * H + col;
+      v[i] = f32x4v{};
+      if (r < rows && col + 4 <= H) {
+        v[i] = *reinterpret_cast<const f32x4loose*>(from);
+      } else if (r < rows) {
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+          if (col + c < H) v[i][c] = from[c];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i) s += v[i];
   }
-  sums[wave][lane] = s;
+#pragma unroll
+  for (int m = 8; m < 64; m <<= 1)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s[c] += __shfl_xor(s[c], m);
+  if (lane < 8) sums[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && col < H) {
-    for (int u = 1; u < kJoinWaves; ++u) s += sums[u][lane];
-    d_weight[col] = s;
+  const int out = blockIdx.x * kJoinCols + (int)threadIdx.x;
+  if (threadIdx.x < kJoinCols && out < H) {
+    float v = 0.f;
+#pragma unroll
+    for (int u = 0; u < kJoinWaves; ++u) v += sums[u][threadIdx.x >> 2][threadIdx.x & 3];
+    d_weight[out] = v;
   }
 }
 
 // A launch holds fewer than 2^32 threads; the kernels loop past that.
 constexpr int64_t kMaxBlocks = 1 << 20;
 
-// Pieces of a lane that the registers hold: 256 bytes of a row in each kernel's largest form.
-template <typename E>
-constexpr int kMostPieces = sizeof(E) == 4 ? 4 : 8;
-
-// Rows from which a wave each fills the chip; below, four share one.
-constexpr int64_t kManyRows = 1024;
-
+// A wave takes a row of few pieces alone; longer rows are four waves' (4096 x
+// 2880 bf16, forward to 8 bits and backward: 17.8 and 21.7 us; a wave a row, of
+// eight pieces a lane, 20.9 and 27.4; 256 rows 3.9 and 7.2, 7.4 and 11.1), the
+// longest sixteen's.
 template <typename F>
-auto by_row(int64_t T, int64_t H, int most, F&& f) {
+auto by_row(int64_t H, int most, F&& f) {
   // -> f(waves of a row, pieces of a lane)
   const int64_t nv = (H + kPiece - 1) / kPiece;
   const int few = most / 4;
   if (nv <= 64 * few) return f(1, few);
-  if (nv <= 64 * most) return T >= kManyRows ? f(1, most) : f(4, few);
+  if (nv <= 256 * few) return f(4, few);
   if (nv <= 256 * most) return f(4, most);
   return f(16, 4);
 }
@@ -236,11 +269,10 @@ auto by_row(int64_t T, int64_t H, int most, F&& f) {
 template <typename E, typename W, bool kFp8>
 hipError_t norm(const NormArgs& a, hipStream_t stream) {
   constexpr int kMost = kMostPieces<E>, kFew = kMost / 4;
-  return by_row(a.T, a.H, kMost, [&](int waves, int pieces) {
+  return by_row(a.H, kMost, [&](int waves, int pieces) {
     const int64_t rows = waves > 4 ? 1 : 4 / waves, blocks = (a.T + rows - 1) / rows;
     const unsigned grid = (unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks);
-    if (waves == 1 && pieces == kFew) rms_norm_kernel<E, W, kFp8, 1, kFew><<<grid, 256, 0, stream>>>(a);
-    else if (waves == 1) rms_norm_kernel<E, W, kFp8, 1, kMost><<<grid, 256, 0, stream>>>(a);
+    if (waves == 1) rms_norm_kernel<E, W, kFp8, 1, kFew><<<grid, 256, 0, stream>>>(a);
     else if (waves == 4 && pieces == kFew) rms_norm_kernel<E, W, kFp8, 4, kFew><<<grid, 256, 0, stream>>>(a);
     else if (waves == 4) rms_norm_kernel<E, W, kFp8, 4, kMost><<<grid, 256, 0, stream>>>(a);
     else rms_norm_kernel<E, W, kFp8, 16, 4><<<grid, 1024, 0, stream>>>(a);
@@ -250,8 +282,8 @@ hipError_t norm(const NormArgs& a, hipStream_t stream) {
 
 // Blocks of the gradient's kernel, and rows of `part`: two for every CU at most.
 int64_t back_blocks(int64_t T, int64_t H, int most) {
-  return by_row(T, H, most, [&](int waves, int) {
-    const int64_t rows = waves > 4 ? 1 : 4 / waves, blocks = (T + rows - 1) / rows;
+  return by_row(H, most, [&](int waves, int pieces) {
+    const int64_t rows = back_rows(waves, pieces, most), blocks = (T + rows - 1) / rows;
     const int64_t full = 2 * mxfp4moe::device_cu_count();
     return blocks < full ? blocks : full;
   });
@@ -263,16 +295,15 @@ hipError_t norm_backward(const NormBackArgs& a, float* d_weight, hipStream_t str
   const unsigned grid = (unsigned)back_blocks(a.T, a.H, kMost);
   const size_t lds = (size_t)((a.H + kPiece - 1) / kPiece) * kPiece * sizeof(float);
   if (grid > 0) {
-    by_row(a.T, a.H, kMost, [&](int waves, int pieces) {
-      if (waves == 1 && pieces == kFew) rms_norm_backward_kernel<E, W, 1, kFew><<<grid, 256, lds, stream>>>(a);
-      else if (waves == 1) rms_norm_backward_kernel<E, W, 1, kMost><<<grid, 256, lds, stream>>>(a);
-      else if (waves == 4 && pieces == kFew) rms_norm_backward_kernel<E, W, 4, kFew><<<grid, 256, 0, stream>>>(a);
+    by_row(a.H, kMost, [&](int waves, int pieces) {
+      if (waves == 1) rms_norm_backward_kernel<E, W, 1, kFew><<<grid, 256, lds, stream>>>(a);
+      else if (waves == 4 && pieces == kFew) rms_norm_backward_kernel<E, W, 4, kFew><<<grid, 512, lds, stream>>>(a);
       else if (waves == 4) rms_norm_backward_kernel<E, W, 4, kMost><<<grid, 256, 0, stream>>>(a);
       else rms_norm_backward_kernel<E, W, 16, 4><<<grid, 1024, 0, stream>>>(a);
       return 0;
     });
   }
-  rms_norm_join_kernel<<<(unsigned)((a.H + 63) / 64), 64 * kJoinWaves, 0, stream>>>(a.part, (int)grid, a.H, d_weight);
+  rms_norm_join_kernel<<<(unsigned)((a.H + kJoinCols - 1) / kJoinCols), 64 * kJoinWaves, 0, stream>>>(a.part, (int)grid, a.H, d_weight);
   return hipGetLastError();
 }
 
