@@ -268,10 +268,10 @@ __global__ __launch_bounds__(512) void fp8_linear_backward_few_kernel(Fp8Args a)
 // through an LDS place of the wave's own into operands.  (Loaded as operands,
 // sixteen rows of 16 bytes at a time, they arrive at 8.9 TB/s from the caches,
 // whole lines at 25.)  Eight waves a CU.
-//   us at N = K = 2880: 512 dense rows 15.3, 2048 29.0, 4096 47.7, 16384 155 (1750
-// TFLOP/s); 128 experts: 256 rows 205 and 1024 rows 242 (1.06 GB of weights at
-// 4.4 TB/s), 16384 rows 335, with N = 5760 658 (826 TFLOP/s, 2.1 GB of weights
-// and 0.6 GB of rows at 4.2 TB/s: HBM and the matrix cores take turns).
+//   us at N = K = 2880: 512 dense rows 15.3, 2048 29.0, 4096 47.7, 16384 152 (1790
+// TFLOP/s); 128 experts: 256 rows 205 and 1024 rows 240 (1.06 GB of weights at
+// 4.4 TB/s), 16384 rows with N = 5760 602 (903 TFLOP/s, 2.4 GB of weights, rows
+// and results at 3.9 TB/s: HBM and the matrix cores take turns).
 template <int kRows, int kWaves>
 struct Tiles {
   static constexpr int kN = 64 * kWaves;
@@ -510,10 +510,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void fp8_linear_tile_kernel(Fp8Args
   __shared__ __attribute__((aligned(16))) u32x4 own[kWaves * T::kOwn];
   __shared__ __attribute__((aligned(16))) u32x4 st0[T::kSlots], st1[T::kSlots];
   const int n_tiles = (a.N + T::kN - 1) / T::kN;
-  int ti, nt;
-  if (!map_tile(a, a.tile_rows, n_tiles, ti, nt)) return;  // uniform per block
+  int nt;
   Tile t;
-  if (!find_tile(a, a.tile_rows, ti, t)) return;
+  if (!find_block(a, a.tile_rows, n_tiles, t, nt)) return;  // uniform per block
   const int K = a.K, N = a.N, n0 = nt * T::kN, kb = (K + kBlock - 1) / kBlock, nb = (N + kBlock - 1) / kBlock;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = n0 + wave * 64;
   const bool work = nw < N;  // uniform
@@ -569,9 +568,9 @@ hipError_t launch_tiles(Fp8Args a, int rows, hipStream_t stream) {
 // (ds_read_b64_tr_b8), and lane c gets byte c of the eight rows.  A half chunk's
 // operands are read while the products of the other are made, and a product's A
 // operand is converted while the one before runs.  Two blocks a CU.
-//   us at N = K = 2880: 512 dense rows 24.5, 2048 43, 16384 273 (990 TFLOP/s, the
+//   us at N = K = 2880: 512 dense rows 24.5, 2048 43, 16384 267 (1020 TFLOP/s, the
 // matrix cores busy for 52% of the cycles at 1.84 GHz); 128 experts: 256 rows 194
-// and 1024 rows 230 (1.06 GB of weights at 4.6 TB/s), 16384 rows 423.  Rows of dy
+// and 1024 rows 217 (1.06 GB of weights at 4.9 TB/s), 16384 rows 411.  Rows of dy
 // that no 16 bytes divide travel through registers, element by element: 2048
 // rows at N = 2876 93 us.
 constexpr int kBackK = 256, kBackRows = 64, kBackStages = 3;
@@ -769,10 +768,9 @@ __global__ __launch_bounds__(256, 2) void fp8_linear_backward_tile_kernel(Fp8Arg
   __shared__ __attribute__((aligned(16))) u32x4 w0[kWSlots], w1[kWSlots], w2[kWSlots];
   __shared__ __attribute__((aligned(16))) u32x4 d0[kDSlots], d1[kDSlots], d2[kDSlots];
   const int k_tiles = (a.K + kBackK - 1) / kBackK;
-  int ti, kt;
-  if (!map_tile(a, kBackRows, k_tiles, ti, kt)) return;  // uniform per block
+  int kt;
   Tile t;
-  if (!find_tile(a, kBackRows, ti, t)) return;
+  if (!find_block(a, kBackRows, k_tiles, t, kt)) return;  // uniform per block
   const int K = a.K, N = a.N, k0 = kt * kBackK;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool work = k0 + wave * 64 < K;  // uniform: a wave past K only loads its share
