@@ -142,6 +142,8 @@ def test_per_expert(gpu, counts, N, K):
 # and several, whole and cut ones, and counts of weight rows that leave waves with little or nothing.
 DENSE_TILES = [(R, N, K) for R, N in ((60, 2222), (120, 2500), (250, 2600), (500, 2564), (1000, 2690), (2100, 2600))
                for K in (16, 128, 144, 256, 400, 768)]
+# ... and the split of K over eight waves, in one round, several and a cut last one
+DENSE_TILES += [(60, 2222, 1168), (60, 2222, 4112), (120, 2500, 1040), (120, 2500, 2592), (250, 2600, 2064)]
 
 
 @pytest.mark.parametrize("R,N,K", DENSE_TILES)
