@@ -33,8 +33,8 @@ inline int64_t blocks_of(int64_t rows, int64_t cols, int64_t experts, int tile_r
 // 16 rows 21.6, 27.2 and 25.9; 64 rows 49.8, 46.7 and 54.6; over 128 experts 64
 // rows 90.7, 80.4 and 91.0; 1024 rows over 128: 282, 214 and 205; N = 5760, 256
 // rows over 32: 137, 116 and 98), and from 64 rows an expert tiles of 128 rows
-// (64 x 256 and 128 x 256, 128 experts, means of 32, 64 and 128: 242, 284 and 405
-// | 250, 277 and 335).
+// (64 x 256 and 128 x 256, 128 experts: means of 32 rows 242 and 250, of 128 411
+// and 333, with N = 5760 745 and 602).
 inline Plan plan_forward(int64_t rows, int64_t n, int64_t experts, int64_t cus) {
   const int64_t used = experts < rows ? experts : rows;
   auto blocks = [&](int tile_rows, int tile_cols) { return blocks_of(rows, n, experts, tile_rows, tile_cols); };
