@@ -98,8 +98,12 @@ __global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : 256) void rms_norm_kerne
     for (int i = 0; i < kP; ++i) {
       const int v = (i * kWaves + sub) * 64 + lane;
       if ((v & ~15) >= nv) continue;  // whole rows of sixteen lanes
-      const f32x8 y = mx8::to_f32<E>(h[i]) * r * mx8::to_f32<W>(wv[i]);
+      f32x8 y = mx8::to_f32<E>(h[i]) * r * mx8::to_f32<W>(wv[i]);
       if constexpr (kFp8) {
+        if (kPiece * v + kPiece > H) {  // what lies past the row counts for nothing, also where r is infinite
+#pragma unroll
+          for (int c = 0; c < kPiece; ++c) y[c] = kPiece * v + c < H ? y[c] : 0.f;
+        }
         mx8::store_quantized(y, v, H, a.codes + t * H, a.scales + t * mx8::blocks_of(H));
       } else if (v < nv) {
         mx8::store_piece(static_cast<E*>(a.y) + t * H, v, H, mx8::from_f32<E>(y));

@@ -156,6 +156,21 @@ def test_quantize_infinity_nan_zero_and_tiny(gpu):
     assert torch.all(torch.isnan(c[1, 128:])) and torch.all(c[2] == 0) and torch.all(c[3] == 0)
 
 
+@pytest.mark.parametrize("H", [5, 300, 1001, 1500, 2050, 9001, 20001])
+def test_norm_to_8_bits_is_the_norm_then_the_quantizer(gpu, H):
+    """To the bit, in every form of the kernel, also where r is infinite (eps = 0 and squares that
+    underflow): what lies behind a row's end has no part in its last block."""
+    x, w = normal(H, 5, H), 1 + 0.3 * normal(1, H)
+    x[1], x[2, -1], x[3, 0] = 1e-30, 1e19, float("inf")
+    for eps in (1e-5, 0.0):
+        y, _, r = gpu.moe_rms_norm(x, w, eps=eps)
+        assert torch.isinf(r[1]) == (eps == 0.0)
+        codes, scales, _, _ = gpu.moe_rms_norm_fp8(x, w, eps=eps)
+        want, s = gpu.moe_fp8_quantize(y)
+        assert np.array_equal(scales.cpu().numpy(), s.cpu().numpy(), equal_nan=True)
+        assert_same_codes(bytes_of(codes), bytes_of(want))
+
+
 def test_streams_and_graph(gpu):
     """Two streams at once, a stream passed in, and a captured step replayed on other inputs."""
     T, H = 600, 2880
