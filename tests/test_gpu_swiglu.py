@@ -69,6 +69,25 @@ def test_limits_and_special_values(gpu):
     assert dh[0, 0] != 0 and torch.all(dh[[1, 3], 0] == 0) and dh[6, 1] != 0 and torch.all(dh[7:9, 1] == 0)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("alpha,limit,offset", [(1.702, 7.0, 1.0), (1.702, math.inf, 0.0), (-3.0, math.inf, 0.5)])
+def test_gradient_of_the_largest_and_smallest_gates(gpu, dtype, split, alpha, limit, offset):
+    """Where alpha * gate overflows, the sigmoid is 0 or 1 and the gradient what the formula has there."""
+    lo, hi = torch.finfo(dtype).min, torch.finfo(dtype).max
+    gates = torch.tensor([lo, hi, lo / 2, hi / 2, lo, hi, -200.0, 200.0, -1.0, 0.0], dtype=dtype, device="cuda")
+    ups = torch.tensor([0.5, 0.5, -2.0, 3.0, 0.0, 0.0, 1.0, 1.0, 2.0, 2.0], dtype=dtype, device="cuda")
+    h = torch.stack([gates, ups], 0 if split else 1).reshape(1, -1)
+    da = torch.full((1, 10), 0.5, dtype=dtype, device="cuda")
+    dh = gpu.moe_swiglu_backward(da, h, split, alpha, limit, offset)
+    want, mag = L.swiglu_backward(f64(da), f64(h), split, alpha, limit, offset)
+    # past |alpha gate| = 128 the sigmoid is 0 or 1 in fp32 and its slope 0: the products' roundings alone are left
+    x, bound = np.abs(alpha * np.minimum(f64(gates), limit)), np.zeros_like(want)
+    for part, m, v in zip(L.halves(bound, split), L.halves(mag, split), L.halves(np.abs(want), split)):
+        part[...] = np.where(x <= 128, 2 * (1.4 * 1.4427 * x + 12) * m, 12 * v) * U
+    assert_near(dh, want, bound + LEAST, dtype, "dh")
+
+
 def test_rows_at_any_element(gpu):
     R, I = 6, 261
     flat, da = normal(1, R * 2 * I + 1, dtype=torch.float16), normal(2, R * I + 1, dtype=torch.float16)
