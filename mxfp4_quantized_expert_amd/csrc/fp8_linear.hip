@@ -92,11 +92,9 @@ __device__ __forceinline__ void store4(uint16_t* out, f32x4 v, const uint16_t* b
 // 9.3 for 128.  Weight row 4 kG (m / 4) + 4 i + m % 4 is operand row m
 // of subtile i, so that a lane's outputs are neighbours.  Loads past K, N or
 // the tile's rows return zero from the buffer's bounds.
-constexpr int kMeet = 8;  // subtiles that meet in LDS at a time
-
 template <int kC, int kG, int kR>
 __global__ __launch_bounds__(512) void fp8_linear_few_kernel(Fp8Args a) {
-  extern __shared__ f32x4 red[];  // [waves][min(kG kR, kMeet)][64]
+  extern __shared__ f32x4 red[];  // [waves][kG kR][64]
   const int n_chunks = (a.N + 16 * kG - 1) / (16 * kG);
   int ti, nc;
   if (!map_block(a.max_tiles, n_chunks, ti, nc)) return;  // uniform per block
@@ -150,22 +148,17 @@ __global__ __launch_bounds__(512) void fp8_linear_few_kernel(Fp8Args a) {
     }
   }
   // lane (row lr of subtile r, q): features n0 + 4 kG q + 4 i .. + 3 in acc[i][r]
-  constexpr int kAll = kG * kR, kAtOnce = kAll < kMeet ? kAll : kMeet;
+  constexpr int kAll = kG * kR;
 #pragma unroll
-  for (int first = 0; first < kAll; first += kAtOnce) {
-    if (first > 0) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i)
-      red[(wave * kAtOnce + i) * 64 + lane] = acc[(first + i) % kG][(first + i) / kG];
-    __syncthreads();
-    for (int i = wave; i < kAtOnce; i += waves) {
-      f32x4 v = red[i * 64 + lane];
-      for (int u = 1; u < waves; ++u) v += red[(u * kAtOnce + i) * 64 + lane];
-      const int n = n0 + 4 * kG * q + 4 * ((first + i) % kG), row = 16 * ((first + i) / kG) + lr;
-      if (row >= t.rows || n >= N) continue;
-      const uint16_t* bias = a.bias != nullptr ? a.bias + (size_t)t.e * N + n : nullptr;
-      store4(a.y + (size_t)(t.row0 + row) * N + n, v, bias, min(4, N - n), (N & 3) == 0);
-    }
+  for (int i = 0; i < kAll; ++i) red[(wave * kAll + i) * 64 + lane] = acc[i % kG][i / kG];
+  __syncthreads();
+  for (int i = wave; i < kAll; i += waves) {
+    f32x4 v = red[i * 64 + lane];
+    for (int u = 1; u < waves; ++u) v += red[(u * kAll + i) * 64 + lane];
+    const int n = n0 + 4 * kG * q + 4 * (i % kG), row = 16 * (i / kG) + lr;
+    if (row >= t.rows || n >= N) continue;
+    const uint16_t* bias = a.bias != nullptr ? a.bias + (size_t)t.e * N + n : nullptr;
+    store4(a.y + (size_t)(t.row0 + row) * N + n, v, bias, min(4, N - n), (N & 3) == 0);
   }
 }
 
@@ -793,7 +786,7 @@ hipError_t launch_few(Fp8Args a, hipStream_t stream) {
   const int chunks = (a.K + kBlock - 1) / kBlock, waves = chunks < 8 ? chunks : 8, c = (chunks + waves - 1) / waves;
   constexpr int c_most = kG + kR > 5 ? 2 : 3;  // what the registers hold
   const dim3 grid = grid_of(a.max_tiles, ((int64_t)a.N + 16 * kG - 1) / (16 * kG));
-  const size_t lds = (size_t)waves * (kG * kR < kMeet ? kG * kR : kMeet) * 64 * sizeof(f32x4);
+  const size_t lds = (size_t)waves * kG * kR * 64 * sizeof(f32x4);  // 64 KB at most
   if (c == 1) fp8_linear_few_kernel<1, kG, kR><<<grid, waves * 64, lds, stream>>>(a);
   else if (c == 2) fp8_linear_few_kernel<2, kG, kR><<<grid, waves * 64, lds, stream>>>(a);
   else fp8_linear_few_kernel<c_most, kG, kR><<<grid, waves * 64, lds, stream>>>(a);
