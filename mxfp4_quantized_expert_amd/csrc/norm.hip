@@ -55,6 +55,28 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
+// Sixteen waves have 128 registers each, which a row's own pieces fill: what is
+// wanted after the row's sum alone (the norm's weight, the gradient's d_s) is
+// loaded then, and the weight, which the caches hold, anew for every row and use.
+// (All of it held, up to 155 registers spill: 512 x 16384 float32, forward and
+// backward, 49 and 93 us, so 25 and 35; 512 x 32768 bf16 25 and 64, 24 and 46.)
+template <int kWaves>
+constexpr bool kLate = kWaves > 4;
+
+// The weight's address and the lane as numbers that the compiler does not know:
+// it would keep the weight, and where a lane's pieces lie, over all rows.
+template <int kWaves, typename W>
+__device__ __forceinline__ const W* fresh(const W* w) {
+  if constexpr (kLate<kWaves>) asm volatile("" : "+s"(w));
+  return w;
+}
+template <int kWaves>
+__device__ __forceinline__ int fresh_lane() {
+  int lane = mx::lane_id();
+  if constexpr (kLate<kWaves>) asm volatile("" : "+v"(lane));
+  return lane;
+}
+
 // kWaves waves a row, kP pieces of it a lane at most.
 template <typename E, typename W, bool kFp8, int kWaves, int kP>
 __global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : 256) void rms_norm_kernel(NormArgs a) {
@@ -74,11 +96,13 @@ __global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : 256) void rms_norm_kerne
       h[i] = v < nv ? mx8::load_piece(xs + t * H, v, H) : typename Pc::vec{};
       if (rs != nullptr) res[i] = v < nv ? mx8::load_piece(rs + t * H, v, H) : typename Pc::vec{};
     }
+    auto weight = [&](int v) {
+      return v < nv ? mx8::load_piece(fresh<kWaves>(w), v, H) : typename Piece<W, kPiece>::vec{};
+    };
     typename Piece<W, kPiece>::vec wv[kP];
+    if constexpr (!kLate<kWaves>) {
 #pragma unroll
-    for (int i = 0; i < kP; ++i) {
-      const int v = (i * kWaves + sub) * 64 + lane;
-      wv[i] = v < nv ? mx8::load_piece(w, v, H) : typename Piece<W, kPiece>::vec{};
+      for (int i = 0; i < kP; ++i) wv[i] = weight((i * kWaves + sub) * 64 + lane);
     }
     float sq = 0.f;
 #pragma unroll
@@ -98,6 +122,7 @@ __global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : 256) void rms_norm_kerne
     for (int i = 0; i < kP; ++i) {
       const int v = (i * kWaves + sub) * 64 + lane;
       if ((v & ~15) >= nv) continue;  // whole rows of sixteen lanes
+      if constexpr (kLate<kWaves>) wv[i] = weight(v);
       f32x8 y = mx8::to_f32<E>(h[i]) * r * mx8::to_f32<W>(wv[i]);
       if constexpr (kFp8) {
         if (kPiece * v + kPiece > H) {  // what lies past the row counts for nothing, also where r is infinite
@@ -156,20 +181,24 @@ __global__ __launch_bounds__(64 * kWaves * back_rows(kWaves, kP, kMostPieces<E>)
     if (kWaves == 1 && t >= a.T) break;
     const int nv = t < a.T ? all : 0;  // (the block's barriers are for every wave)
     typename Pc::vec h[kP], g[kP], d[kP];
+    auto stream_gradient = [&](int v) {
+      return ds != nullptr && v < nv ? mx8::load_piece(ds + t * H, v, H) : typename Pc::vec{};
+    };
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
-      const int v = (i * kWaves + sub) * 64 + lane;
+      const int v = (i * kWaves + sub) * 64 + fresh_lane<kWaves>();
       h[i] = v < nv ? mx8::load_piece(hs + t * H, v, H) : typename Pc::vec{};
       g[i] = v < nv ? mx8::load_piece(dys + t * H, v, H) : typename Pc::vec{};
-      d[i] = ds != nullptr && v < nv ? mx8::load_piece(ds + t * H, v, H) : typename Pc::vec{};
+      if constexpr (!kLate<kWaves>) d[i] = stream_gradient(v);
     }
     const float r = t < a.T ? a.rstd[t] : 0.f;
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
-      const int v = (i * kWaves + sub) * 64 + lane;
+      const int v = (i * kWaves + sub) * 64 + fresh_lane<kWaves>();
       if (v >= nv) continue;
-      const f32x8 s = mx8::to_f32<E>(h[i]), y = mx8::to_f32<E>(g[i]), f = y * mx8::to_f32<W>(mx8::load_piece(w, v, H));
+      const f32x8 s = mx8::to_f32<E>(h[i]), y = mx8::to_f32<E>(g[i]);
+      const f32x8 f = y * mx8::to_f32<W>(mx8::load_piece(fresh<kWaves>(w), v, H));
 #pragma unroll
       for (int c = 0; c < kPiece; ++c) {
         dot = __builtin_fmaf(f[c], s[c], dot);
@@ -180,9 +209,11 @@ __global__ __launch_bounds__(64 * kWaves * back_rows(kWaves, kP, kMostPieces<E>)
     const float mean = row_sum<kWaves>(dot, part) / (float)H * r;
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
-      const int v = (i * kWaves + sub) * 64 + lane;
+      const int v = (i * kWaves + sub) * 64 + fresh_lane<kWaves>();
       if (v >= nv) continue;
-      const f32x8 s = mx8::to_f32<E>(h[i]), f = mx8::to_f32<E>(g[i]) * mx8::to_f32<W>(mx8::load_piece(w, v, H));
+      const f32x8 s = mx8::to_f32<E>(h[i]);
+      const f32x8 f = mx8::to_f32<E>(g[i]) * mx8::to_f32<W>(mx8::load_piece(fresh<kWaves>(w), v, H));
+      if constexpr (kLate<kWaves>) d[i] = stream_gradient(v);
       const f32x8 dx = r * (f - s * r * mean) + mx8::to_f32<E>(d[i]);
       mx8::store_piece(static_cast<E*>(a.dx) + t * H, v, H, mx8::from_f32<E>(dx));
     }
