@@ -235,3 +235,9 @@ def test_refusals_of_the_binding(gpu):
     f = gpu.load().moe_rms_norm_backward
     args = [x.data_ptr(), None, x.data_ptr(), w.data_ptr(), 2, 2, x.data_ptr(), 4, 64, x.data_ptr(), w.data_ptr()]
     assert f(*args, x.data_ptr(), ctypes.byref(n), None) == -3
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_several_wide_rows_a_block(gpu, dtype):
+    """Sixteen waves a row, more rows than the gradient's launch has blocks."""
+    test_norm_and_gradients(gpu, 1030, 16500, dtype)
