@@ -568,7 +568,10 @@ int moe_fp8_linear_backward(const uint16_t* dy, const uint8_t* w, const float* w
  *         it were none
  *   limit > 0 (or infinity), alpha and offset finite; 1 <= I <=
  *   MXFP4MOE_MAX_ROW / 2, R * ceil(I / 128) < 2^31.  R == 0 is a no-op.
- * fp32, one rounding at the end.  Outputs alias no input.
+ * fp32, one rounding at the end.  Outputs alias no input.  The sigmoid is
+ * 1 / (1 + 2^(-alpha log2(e) g)) in the hardware's 2^x and reciprocal, which
+ * has no subnormal results: where it lies below 2^-126 (alpha g below -87.3) it
+ * is 0, and so are a and the gradients, of float32 rows too.
  */
 int moe_swiglu(const void* h, int dtype, int64_t R, int64_t I, float alpha, float limit, float offset, int split,
                void* a, void* stream);

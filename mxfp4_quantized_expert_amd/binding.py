@@ -862,8 +862,8 @@ def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
     """The norm ahead of the layer: s = x + residual (rounded to x's type; x without a residual),
     y = s / sqrt(mean(s^2) + eps) * weight over the rows of x [T, H] (bfloat16, float16 or float32;
     weight [H] of x's type or float32).  Returns (y [T, H], s [T, H], rstd [T] float32); without a
-    residual s is x itself.  s and rstd are what moe_rms_norm_backward takes; no output ever
-    requires a gradient."""
+    residual s is x itself.  s and rstd are what moe_rms_norm_backward takes; no output but x
+    itself ever requires a gradient."""
     if _host is not None and stream is None and out is None and summed is None and rstd is None:
         got = _host.rms_norm(x, weight, residual, eps, False)
         if got is not None:  # None: not a plain call, or one to refuse

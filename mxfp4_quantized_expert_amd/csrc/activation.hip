@@ -8,7 +8,9 @@
 // (gpt-oss: alpha 1.702, limit 7, offset 1; the plain gated SiLU: 1, infinity
 // and 0.)  Gate and up lie side by side or in two halves of a row.  A lane
 // takes eight outputs, sixteen lanes a scale's 128, so no block of threads
-// waits for another; HBM is the bound.
+// waits for another; HBM is the bound.  us and TB/s of launches in a row, bf16 rows
+// of 2880: 4096 rows 13.0 (5.5), to 8 bits 13.2 (4.5), gradient 21.1 (5.6), rows to 8
+// bits as they are 7.3 (4.9); 16384 rows 44 (6.4), 38 (6.3), 84 (5.6) and 22.8 (6.3).
 #include "fp8_device.h"
 #include "internal.h"
 #include "mx_device.h"

@@ -336,8 +336,10 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(const float* __re
 int lanes_of(int64_t E) { return E <= 32 ? 8 : E <= 128 ? 16 : 64; }  // of a token
 
 // Blocks of the loss's kernel: one for every CU at most, and a single one, which
-// needs no second launch, up to four rounds of its tokens (256 tokens of 32
-// experts in four rounds 5.5 us, in four blocks 3.2 and 5.4 to join them).
+// needs no second launch, up to four rounds of its tokens (us, four rounds in one
+// block and in four with the join: 512 tokens of 32 experts 5.5 and 6.3, 256 of
+// 128 6.7 and 6.7, 64 of 500 7.0 and 7.1; five rounds 6.0 and 6.5, 7.4 and 7.0,
+// 8.1 and 7.5; the second launch costs the host 3.5 besides).
 int64_t loss_blocks(int64_t T, int64_t E) {
   const int64_t round = kThreads / lanes_of(E), n = (T + round - 1) / round;
   const int64_t most = mxfp4moe::device_cu_count();

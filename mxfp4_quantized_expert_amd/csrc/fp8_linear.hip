@@ -88,8 +88,8 @@ __device__ __forceinline__ void store4(uint16_t* out, f32x4 v, const uint16_t* b
 // both straight to registers.  The waves of a block split K, kC blocks of 128
 // each at a time (all loads of a wave in flight before the first product), for
 // kG * 16 weight rows, so a block has no barrier before its sums meet in LDS,
-// added in wave order: one round of latency, 4.1 us for one row of 2880 x 2880,
-// 9.3 for 128.  Weight row 4 kG (m / 4) + 4 i + m % 4 is operand row m
+// added in wave order: one round of latency, 4.0 us for one row of 2880 x 2880,
+// 8.9 for 128.  Weight row 4 kG (m / 4) + 4 i + m % 4 is operand row m
 // of subtile i, so that a lane's outputs are neighbours.  Loads past K, N or
 // the tile's rows return zero from the buffer's bounds.
 template <int kC, int kG, int kR>
@@ -174,9 +174,9 @@ __device__ __forceinline__ uint32_t fp8x2_to_bf16x2(uint32_t four) {
 // converts them to pairs of k and exchanges halves between the rows of a pair
 // (v_perm) into four operands of eight n, one for each k.  The waves of a block
 // take every waves-th block of 128 n and add their sums in LDS in wave order: one
-// row of 2880 x 2880 8.1 us, 64 rows 9.2.  (32 or 64 rows a block, to convert the
-// weights for more rows at a time, were no faster at any size: 64 rows 12.4 and
-// 19.8 us, 256 rows 22.2 and 19.8.)
+// row of 2880 x 2880 7.5 us, 64 rows 8.8.  (32 or 64 rows a block, to convert the
+// weights for more rows at a time, gained nothing: 64 rows 12.4 and 19.8 us, 256
+// rows 22.2 and 19.8, where sixteen rows a block take 18.8 to 20.4.)
 constexpr int kBackFewK = 64;
 constexpr int kBackFewRows = 16;
 constexpr int kRedStride = 20;  // floats per lane in LDS: 16 and padding
@@ -261,10 +261,11 @@ __global__ __launch_bounds__(512) void fp8_linear_backward_few_kernel(Fp8Args a)
 // through an LDS place of the wave's own into operands.  (Loaded as operands,
 // sixteen rows of 16 bytes at a time, they arrive at 8.9 TB/s from the caches,
 // whole lines at 25.)  Eight waves a CU.
-//   us at N = K = 2880: 512 dense rows 15.3, 2048 29.0, 4096 47.7, 16384 152 (1790
-// TFLOP/s); 128 experts: 256 rows 205 and 1024 rows 240 (1.06 GB of weights at
-// 4.4 TB/s), 16384 rows with N = 5760 602 (903 TFLOP/s, 2.4 GB of weights, rows
-// and results at 3.9 TB/s: HBM and the matrix cores take turns).
+//   us at N = K = 2880: 512 dense rows 15.2, 2048 29.4, 4096 47.7, 16384 152 to
+// 156 (1790 to 1750 TFLOP/s); 128 experts: 256 rows 172 and 1024 rows 213 (1.06 GB
+// of weights at 5.0 TB/s), 16384 rows with N = 5760 602 to 633 (903 to 858 TFLOP/s,
+// 2.4 GB of weights, rows and results at 3.9 TB/s: HBM and the matrix cores take
+// turns).
 template <int kRows, int kWaves>
 struct Tiles {
   static constexpr int kN = 64 * kWaves;
@@ -561,9 +562,9 @@ hipError_t launch_tiles(Fp8Args a, int rows, hipStream_t stream) {
 // (ds_read_b64_tr_b8), and lane c gets byte c of the eight rows.  A half chunk's
 // operands are read while the products of the other are made, and a product's A
 // operand is converted while the one before runs.  Two blocks a CU.
-//   us at N = K = 2880: 512 dense rows 24.5, 2048 43, 16384 267 (1020 TFLOP/s, the
-// matrix cores busy for 52% of the cycles at 1.84 GHz); 128 experts: 256 rows 194
-// and 1024 rows 217 (1.06 GB of weights at 4.9 TB/s), 16384 rows 411.  Rows of dy
+//   us at N = K = 2880: 512 dense rows 24.8, 2048 43, 16384 267 (1020 TFLOP/s, the
+// matrix cores busy for 52% of the cycles at 1.88 GHz); 128 experts: 256 rows 166
+// and 1024 rows 187 (1.06 GB of weights at 5.7 TB/s), 16384 rows 404.  Rows of dy
 // that no 16 bytes divide travel through registers, element by element: 2048
 // rows at N = 2876 93 us.
 constexpr int kBackK = 256, kBackRows = 64, kBackStages = 3;

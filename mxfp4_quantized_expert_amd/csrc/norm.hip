@@ -9,10 +9,13 @@
 // fp32 throughout, one rounding at the end.  A row lies in the registers of
 // one wave (or of four or sixteen of one block), 8 elements a piece, so that
 // each tensor moves once; HBM is the bound, and for a few rows the latency of
-// a launch.  us and TB/s, bf16, with a residual: 4 x 2880 3.2 forward and 6.0
-// backward (two launches), 4096 x 2880 17.5 (5.4), in 8 bits 17.8 (4.6), backward
-// 21.7 (4.4), 16384 x 2880 74 (5.1), 68 (4.8) and 79 (4.8); 777 x 1001 float32 4.5
-// and 8.7.
+// a launch.  us and TB/s of launches in a row, bf16, with a residual: 4 x 2880
+// 3.2 forward and 5.9 backward (two launches), 4096 x 2880 17.4 (5.4), in 8 bits
+// 18.4 (4.5), backward 21.7 (4.4), 16384 x 2880 74 (5.1), 68 (4.9) and 80 (4.7),
+// 512 x 16384 14.4 (4.7), 15.5 (3.8) and 28.3 (2.4: the largest form of four waves,
+// whose registers leave eight waves a CU), 512 x 32768 23.9 (5.6), 24.9 (4.7) and
+// 45.6 (2.9); float32 777 x 1001 4.6 and 8.7, 512 x 16384 24.8 (5.4), 21.7 (5.0) and
+// 34.6 (3.9), 512 x 32768 52.7 (5.1), 38.8 (5.6) and 84 (3.2).
 #include "fp8_device.h"
 #include "internal.h"
 #include "mx_device.h"

@@ -122,10 +122,18 @@ __device__ __forceinline__ bool map_tile(const A& a, int tm, int chunks, int& ti
 // Block -> (tile, chunk), as map_tile and find_tile, with groups that end with
 // an expert: the blocks that run together on an XCD share one expert's weights.
 // (A group of four tiles of two or three experts reads all their weights at a
-// time: in 8 bits, 16384 rows over 128 experts, 5760 x 2880, 602 us, in groups
-// that mix them 651; the gradient of 1024 rows, 2880 x 2880, 217, mixed 228.  Of
-// one expert eight tiles share more rows' reads than two or four: 16384 rows 152
-// us, 163 and 158.)
+// time: in 8 bits, us, 16384 rows over 32 experts, 5760 x 2880, 369, in groups
+// that mix them 463, 2880 x 2880 196 and 238, over 128 experts, 5760 x 2880, 602
+// and 616; the gradient of 1024 rows over 128, 2880 x 2880, 181 and 194.  Of one
+// expert eight tiles share more rows' reads than two or four: 16384 rows 152 us,
+// 163 and 158.  Over 8 to 64 experts with 64 to 384 rows each, N = 1440 to 4096,
+// four batches of each size, this order takes 0.86 to 1.06 times the other's time
+// and 0.98 times on the average.  A batch with a few blocks more than run at once
+// can go either way by a tenth: 4096 rows over 32 experts, 2880 x 2880, 516 blocks,
+// have 65 for the 64 places of an XCD, and the 65th starts when the first ends,
+// after 47 to 57 us in mixed groups and 57 to 60 in these, and takes 35 to 45 more
+// by itself: 94 us and 104.  544 blocks of 16 experts, N = 4096, take 98 mixed and
+// 91 so.  What decides it is the counts, which are on the device.)
 constexpr int kExpertGroup = 8;
 template <typename A>
 __device__ bool find_block(const A& a, int tm, int chunks, Tile& t, int& chunk) {
