@@ -10,8 +10,8 @@
 // one wave (or of four or sixteen of one block), 8 elements a piece, so that
 // each tensor moves once; HBM is the bound, and for a few rows the latency of
 // a launch.  us and TB/s of launches in a row, bf16, with a residual: 4 x 2880
-// 3.2 forward and 5.9 backward (two launches), 4096 x 2880 17.4 (5.4), in 8 bits
-// 18.4 (4.5), backward 21.7 (4.4), 16384 x 2880 74 (5.1), 68 (4.9) and 80 (4.7),
+// 3.2 forward and 5.9 backward (two launches), 4096 x 2880 17.6 (5.4), in 8 bits
+// 18.1 (4.6), backward 21.8 (4.3), 16384 x 2880 74 (5.1), 68 (4.9) and 80 (4.7),
 // 512 x 16384 14.4 (4.7), 15.5 (3.8) and 28.3 (2.4: the largest form of four waves,
 // whose registers leave eight waves a CU), 512 x 32768 23.9 (5.6), 24.9 (4.7) and
 // 45.6 (2.9); float32 777 x 1001 4.6 and 8.7, 512 x 16384 24.8 (5.4), 21.7 (5.0) and
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : 256) void rms_norm_kerne
       if constexpr (kLate<kWaves>) wv[i] = weight(v);
       f32x8 y = mx8::to_f32<E>(h[i]) * r * mx8::to_f32<W>(wv[i]);
       if constexpr (kFp8) {
-        if (kPiece * v + kPiece > H) {  // what lies past the row counts for nothing, also where r is infinite
+        if (r == __builtin_inff()) {  // uniform: zeros past the row's end count for nothing then too
 #pragma unroll
           for (int c = 0; c < kPiece; ++c) y[c] = kPiece * v + c < H ? y[c] : 0.f;
         }
