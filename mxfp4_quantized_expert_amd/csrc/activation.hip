@@ -103,8 +103,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(ActArgs a) {
       const float u = __builtin_elementwise_maximum(__builtin_elementwise_minimum(up[c], a.limit), -a.limit);
       const float s = sigmoid(a.alpha, g);
       // (past 128 either way s or 1 - s is 0 in fp32, and so is the product: the bound keeps it from being 0 times an
-      // infinite alpha g)
-      const float x = __builtin_elementwise_maximum(__builtin_elementwise_minimum(a.alpha * g, 128.0f), -128.0f);
+      // infinite alpha g; s is NaN where that is)
+      const float x = __builtin_amdgcn_fmed3f(a.alpha * g, 128.0f, -128.0f);
       dg[c] = gate[c] <= a.limit ? da[c] * (u + a.offset) * s * (1.0f + x * (1.0f - s)) : 0.f;
       du[c] = fabsf(up[c]) <= a.limit ? da[c] * g * s : 0.f;
     }
