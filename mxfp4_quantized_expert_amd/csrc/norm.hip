@@ -290,7 +290,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void rms_norm_join_kernel(const fl
 constexpr int64_t kMaxBlocks = 1 << 20;
 
 // A wave takes a row of few pieces alone; longer rows are four waves' (4096 x
-// 2880 bf16, forward to 8 bits and backward: 17.8 and 21.7 us; a wave a row, of
+// 2880 bf16, forward to 8 bits and backward: 18.1 and 21.8 us; a wave a row, of
 // eight pieces a lane, 20.9 and 27.4; 256 rows 3.9 and 7.2, 7.4 and 11.1), the
 // longest sixteen's.
 template <typename F>
